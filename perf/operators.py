@@ -126,7 +126,8 @@ def prepare(case, seed):
     g = _generator(seed)
     idx, m, cap = _tile_list(g, case)
     s = dict(case=case, idx=idx, m=m, cap=cap,
-             count=torch.tensor([m], dtype=torch.int32, device="cuda"))
+             count=torch.tensor([m], dtype=torch.int32, device="cuda"),
+             workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))   # kept by a user from call to call
     n, h, w = case["n"], case["h"], case["w"]
     if case["op"] == "cache":
         c, dt = case["c"], DTYPES[case["dtype"]]
@@ -290,9 +291,10 @@ def _run_own(s):
         return dict(scales=s["scales"], y=s["y"])
     if case["op"] == "linear":
         return sige.sige_qlinear(sige.QCache(*s["a"], "s8"), sige.QCache(*s["w"], "s8"), s["bias"], s["y"],
-                                   residual=s["residual"], **where)
+                                   residual=s["residual"], workspace=s["workspace"], **where)
     k, v = sige.QCache(*s["k"], case["fmt"]), sige.QCache(*s["v"], case["fmt"])
-    return sige.sige_attention_qcache(s["q"], k, v, case["heads"], s["o"], key_counts=s["lens"], **where)
+    return sige.sige_attention_qcache(s["q"], k, v, case["heads"], s["o"], key_counts=s["lens"], workspace=s["workspace"],
+                                      **where)
 
 
 def run(state):
