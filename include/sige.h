@@ -460,6 +460,131 @@ int sige_attention_core(const void *q, const sige_tensor_desc *qd, const void *k
  * call would return them.  Host only. */
 int sige_attention_path(const sige_tensor_desc *qd, int32_t dv, int32_t heads);
 
+/* ------------------------------------------------- quantised cache */
+
+/* Formats of a quantised cache. */
+typedef enum {
+    SIGE_Q_S8 = 0,    /* signed 8-bit integers, -127 .. 127 */
+    SIGE_Q_E4M3 = 1,  /* 8-bit floats: 4 exponent, 3 mantissa bits, largest 448 */
+    SIGE_Q_S4 = 2     /* signed 4-bit integers, -7 .. 7: two to a byte, the even channel in the low half */
+} sige_qformat;
+
+/* A quantised NHWC map: codes [n][h][w][c] (c bytes a pixel, c / 2 for
+ * SIGE_Q_S4) and one float32 scale per `group` consecutive channels of a
+ * pixel, scales [n][h][w][c / group].  `group` divides c (and is even for
+ * SIGE_Q_S4).  A code stands for code * scale.  group == c gives the one scale
+ * per token that sige_qlinear reads; group == head width (or a multiple) the
+ * scales per token and head that sige_attention_qcache reads. */
+typedef struct {
+    int32_t n, h, w, c;
+    int32_t format;  /* sige_qformat */
+    int32_t group;
+} sige_qcache_desc;
+
+/* Bytes of the codes, and number of the scales, of such a cache; 0 for an
+ * invalid descriptor.  Host only. */
+size_t sige_qcache_code_bytes(const sige_qcache_desc *cd);
+size_t sige_qcache_scales(const sige_qcache_desc *cd);
+
+/* (9) Write a map into a quantised cache (mer.dev notes on SIGE, section 3
+ * "Method": the activations of the original are kept; section 4.2: for a
+ * diffusion model those of every step, which costs memory), at every in-image
+ * pixel of the first min(*count, capacity) tiles of `idx` (block x block), or
+ * at every pixel when idx == NULL (count, capacity and block are ignored).
+ * With t = T(x), T as in sige_gather (float32, not rounded), and m the largest
+ * |t| of a group:
+ *   S8, S4 : scale = m / 127 or m / 7, rounded to float32; code = t / scale, the
+ *            exact quotient rounded to the nearest integer, ties to even
+ *   E4M3   : scale = 2^ceil(log2(m / 448)); code = t / scale (exact) rounded to
+ *            the format, ties to even
+ * A group whose scale would be below 2^-126 (m of about 1e-36, zeros included)
+ * gets scale 0 and codes 0.  A group that holds an infinity or a NaN gets a
+ * NaN scale and codes 0: it reads back as NaN.  Codes and scales of other
+ * pixels are left as they are.
+ *   x      : device NHWC f32 or bf16 (xd), the cache's n, h, w, c
+ *   codes, scales : device, not overlapping x or each other
+ * A weight matrix [c_out][c_in] is written as a map of n = c_out, h = w = 1.
+ * Any c, group and alignment; 16-byte aligned maps with groups that are
+ * multiples of 8 (up to 2048) take the vector form.  Errors:
+ * SIGE_ERR_INVALID_ARG (NULL, sizes that differ, group not dividing c, bad
+ * format, overlap, misaligned list, x not aligned to its element or scales to
+ * 4 bytes), SIGE_ERR_UNSUPPORTED (dtype, layout, odd S4 group, block > 64, more than
+ * 2^31 - 1 pixels or listed slots), SIGE_ERR_CUDA. */
+int sige_qcache_write(const void *x, const sige_tensor_desc *xd, const float *gn_scale, const float *gn_shift,
+                      int32_t silu, int32_t block, const int32_t *idx, const int32_t *count, int32_t capacity,
+                      void *codes, float *scales, const sige_qcache_desc *cd, sige_stream_t stream);
+
+/* (9b) Read it back: y = round(code * scale) at the listed tiles (a restore
+ * of the original's tiles from the cache, as (7)) or at every pixel; every
+ * other byte of y is left as it is.  y: device NHWC f32 or bf16 (yd).
+ * Arguments and errors as (9). */
+int sige_qcache_read(const void *codes, const float *scales, const sige_qcache_desc *cd, int32_t block,
+                     const int32_t *idx, const int32_t *count, int32_t capacity, void *y, const sige_tensor_desc *yd,
+                     sige_stream_t stream);
+
+/* (10) A projection of a quantised map by quantised weights, the 1x1 layer in
+ * 8-bit integers:
+ *   y[t][o] = round(sum_c a[t][c] w[o][c] * a_scale[t] * w_scale[o] + bias[o] + residual[t][o])
+ * for every token (pixel) t under the listed tiles, or every token when
+ * idx == NULL; the integer sum is exact, the rest float32, one rounding to y's
+ * dtype.  Every other byte of y is left as it is.
+ *   a : SIGE_Q_S8 with group == c (ad)
+ *   w : SIGE_Q_S8 with group == c, described as a map of n = c_out, h = w = 1 (wd)
+ *   bias     : device float32 [c_out] or NULL
+ *   residual : device, same shape/dtype as y, or NULL
+ *   y        : device NHWC f32 or bf16 [n][h][w][c_out] (yd), not overlapping
+ *              any operand (the residual included)
+ *   workspace: device, >= SIGE_WORKSPACE_HEADER_BYTES (the device error word),
+ *              16-byte aligned, zero-filled before its first use
+ * sige_qlinear_path says which kernel a call gets: tensor cores (c a multiple
+ * of 16, codes 16-byte aligned) or CUDA cores.  A device-side wait
+ * that expires records SIGE_ERR_TIMEOUT and leaves outputs unwritten.  Errors:
+ * SIGE_ERR_INVALID_ARG, SIGE_ERR_UNSUPPORTED (format, group, dtype, layout,
+ * c > 131071, block > 64, more than 2^31 - 1 pixels or listed slots),
+ * SIGE_ERR_WORKSPACE, SIGE_ERR_CUDA. */
+int sige_qlinear(const void *a_codes, const float *a_scales, const sige_qcache_desc *ad, const void *w_codes,
+                 const float *w_scales, const sige_qcache_desc *wd, const float *bias, int32_t block,
+                 const int32_t *idx, const int32_t *count, int32_t capacity, const void *residual, void *y,
+                 const sige_tensor_desc *yd, void *workspace, size_t workspace_bytes, sige_stream_t stream);
+
+/* Which kernel sige_qlinear runs for c input channels (16-byte aligned codes):
+ * 1 = tcgen05 tensor cores, 0 = CUDA cores.  Host only. */
+int sige_qlinear_path(int32_t c);
+
+/* (11) The attention step of (8) over quantised key and value caches: for
+ * every token under the listed tiles, or every token when idx == NULL, per
+ * head h
+ *   o[n][y][x][h*dvh : (h+1)*dvh] = softmax(q_h K_h^T / sqrt(dh)) V_h
+ * over the first key_counts[n] keys of the item (a padded batch of contexts;
+ * values are clamped to [0, keys], NULL: all), K and V being what the codes
+ * stand for; a token of an item without keys gets 0.  Float32 accumulation,
+ * one rounding of o to bf16; every other element of o is left as it is.
+ * Keys past the count are not read into the result, whatever they hold.
+ *   q      : device bf16 [N][H][W][D] (qd), read at the tokens
+ *   k, v   : caches of any format, n = N, h * w = keys, c = D (kd) and Dv (vd);
+ *            each group a multiple of the head width (one scale per token and
+ *            head, or per token)
+ *   key_counts : device int32 [N] or NULL
+ *   o      : device bf16 [N][H][W][Dv], not overlapping any operand
+ *   workspace : as (10)
+ * sige_attention_qcache_path says which kernel a call gets.  On the tensor
+ * cores the weights exp(s - max), times the value's scale, are rounded to bf16
+ * before the second product (as in (8)).  Errors: SIGE_ERR_INVALID_ARG (NULL,
+ * sizes that differ, D or Dv not a multiple of heads, overlap, misaligned
+ * list), SIGE_ERR_UNSUPPORTED (q not bf16 NHWC, head width > 256, group not a
+ * multiple of the head width, block > 64, sizes past 32 bits),
+ * SIGE_ERR_WORKSPACE, SIGE_ERR_CUDA. */
+int sige_attention_qcache(const void *q, const sige_tensor_desc *qd, const void *k_codes, const float *k_scales,
+                          const sige_qcache_desc *kd, const void *v_codes, const float *v_scales,
+                          const sige_qcache_desc *vd, const int32_t *key_counts, int32_t heads, int32_t block,
+                          const int32_t *idx, const int32_t *count, int32_t capacity, void *o, void *workspace,
+                          size_t workspace_bytes, sige_stream_t stream);
+
+/* Which kernel sige_attention_qcache runs for head widths dh and dvh (16-byte
+ * aligned buffers): 1 = tcgen05 tensor cores, 0 = CUDA cores,
+ * SIGE_ERR_UNSUPPORTED above 256.  Host only. */
+int sige_attention_qcache_path(int32_t dh, int32_t dvh);
+
 /* ------------------------------------------------------------ utilities */
 
 /* Workspace bytes for sige_sparse_conv / sige_conv_fused / sige_dense_conv

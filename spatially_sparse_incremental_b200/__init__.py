@@ -46,7 +46,13 @@ class LayerExt(ctypes.Structure):
                 ("spade_gamma", ctypes.c_void_p), ("spade_beta", ctypes.c_void_p), ("act", ctypes.c_int32)]
 
 
+class QCacheDesc(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("h", ctypes.c_int32), ("w", ctypes.c_int32), ("c", ctypes.c_int32),
+                ("format", ctypes.c_int32), ("group", ctypes.c_int32)]
+
+
 ACT_NONE, ACT_SILU, ACT_LEAKY = 0, 1, 2
+Q_S8, Q_E4M3, Q_S4 = 0, 1, 2
 
 
 class ScaleDesc(ctypes.Structure):
@@ -58,6 +64,7 @@ class ScaleDesc(ctypes.Structure):
 _vp, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
 _TD, _CD, _SD = ctypes.POINTER(TensorDesc), ctypes.POINTER(ConvDesc), ctypes.POINTER(ScaleDesc)
 _LE = ctypes.POINTER(LayerExt)
+_QD = ctypes.POINTER(QCacheDesc)
 SIGNATURES = {
     "sige_reduce_mask_workspace_bytes": (_sz, [_TD, _i32, _SD]),
     "sige_reduce_mask": (_i32, [_vp, _vp, _TD, _f32, _i32, _i32, _SD, _vp, _vp, _vp, _vp, _sz, _vp]),
@@ -89,6 +96,15 @@ SIGNATURES = {
     "sige_conv_schedule": (_i32, [_CD, _i32, _i32, _i32, _vp, _i32]),
     "sige_attention_core": (_i32, [_vp, _TD, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _i32, _i32, _vp, _vp]),
     "sige_attention_path": (_i32, [_TD, _i32, _i32]),
+    "sige_qcache_code_bytes": (_sz, [_QD]),
+    "sige_qcache_scales": (_sz, [_QD]),
+    "sige_qcache_write": (_i32, [_vp, _TD, _vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _QD, _vp]),
+    "sige_qcache_read": (_i32, [_vp, _vp, _QD, _i32, _vp, _vp, _i32, _vp, _TD, _vp]),
+    "sige_qlinear": (_i32, [_vp, _vp, _QD, _vp, _vp, _QD, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _TD, _vp, _sz, _vp]),
+    "sige_qlinear_path": (_i32, [_i32]),
+    "sige_attention_qcache": (_i32, [_vp, _TD, _vp, _vp, _QD, _vp, _vp, _QD, _vp, _i32, _i32, _vp, _vp, _i32, _vp, _vp,
+                                     _sz, _vp]),
+    "sige_attention_qcache_path": (_i32, [_i32, _i32]),
     "sige_launch_count": (ctypes.c_uint64, []),
     "sige_status_string": (ctypes.c_char_p, [_i32]),
 }
@@ -509,6 +525,257 @@ def sige_attention_sparse(x, idx, count, capacity: int, block: int, wq, wo, bo, 
     sige_attention_core(q, k_map, v_map, heads, idx, count, capacity, block, o, stream)
     sige_conv_fused(o, wo, bo, conv_desc(1, 1, 0, Dv, Co, block), idx, count, capacity, y, residual=residual,
                     workspace=workspace, stream=stream)
+    return y
+
+
+# ------------------------------------------------------------------ quantised cache
+
+_QFMT = {"s8": Q_S8, "e4m3": Q_E4M3, "s4": Q_S4}
+_QSTORE = {"s8": torch.int8, "e4m3": torch.float8_e4m3fn, "s4": torch.uint8}
+
+
+class QCache:
+    """A quantised NHWC map: ``codes`` [N, H, W, C] (int8 for "s8", float8_e4m3fn
+    for "e4m3"; uint8 [N, H, W, C / 2] for "s4": two 4-bit codes a byte, the even
+    channel in the low half) and ``scales`` float32 [N, H, W, C / group]; a
+    code stands for code * scale.  A view of the two tensors: nothing is
+    copied or kept."""
+    __slots__ = ("codes", "scales", "format", "desc")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, format: str):
+        if format not in _QFMT:
+            raise ValueError(f"unknown format {format!r}: one of {sorted(_QFMT)}")
+        if codes.dtype != _QSTORE[format] or scales.dtype != torch.float32:
+            raise ValueError(f"{format} codes are {_QSTORE[format]}, scales are torch.float32")
+        if codes.dim() != 4 or scales.dim() != 4 or codes.shape[:3] != scales.shape[:3]:
+            raise ValueError("expected codes and scales [N, H, W, *] of one map")
+        if not codes.is_contiguous() or not scales.is_contiguous():
+            raise ValueError("expected contiguous codes and scales")
+        if codes.device != scales.device:
+            raise ValueError("codes and scales are on different devices")
+        n, h, w, c = codes.shape
+        c = 2 * c if format == "s4" else c
+        ng = scales.shape[3]
+        if ng < 1 or c % ng:
+            raise ValueError(f"{ng} scales a pixel do not divide {c} channels")
+        self.codes, self.scales, self.format = codes, scales, format
+        self.desc = QCacheDesc(n, h, w, c, _QFMT[format], c // ng)
+
+    @property
+    def shape(self):
+        d = self.desc
+        return d.n, d.h, d.w, d.c
+
+    @property
+    def group(self) -> int:
+        return self.desc.group
+
+
+def qcache_empty(n: int, h: int, w: int, c: int, format: str = "s8", group: int | None = None,
+                 device="cuda") -> QCache:
+    """An uninitialised cache of that map (``group`` None: one scale a pixel)."""
+    group = c if group is None else group
+    if group < 1 or c % group or (format == "s4" and group % 2):
+        raise ValueError(f"a group of {group} does not fit {c} channels of {format}")
+    codes = torch.empty((n, h, w, c // 2 if format == "s4" else c), dtype=_QSTORE[format], device=device)
+    return QCache(codes, torch.empty((n, h, w, c // group), dtype=torch.float32, device=device), format)
+
+
+def sige_qcache_code_bytes(cd: QCacheDesc) -> int:
+    return int(lib().sige_qcache_code_bytes(ctypes.byref(cd)))
+
+
+def sige_qcache_scales(cd: QCacheDesc) -> int:
+    return int(lib().sige_qcache_scales(ctypes.byref(cd)))
+
+
+def _on_device(what: str, *tensors) -> torch.device:
+    """The CUDA device that all the given tensors are on."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if t.device.type != "cuda":
+            raise ValueError(f"{what}: expected tensors on a CUDA device")
+        if dev is not None and t.device != dev:
+            raise ValueError(f"{what}: tensors on different devices ({dev} and {t.device})")
+        dev = t.device
+    return dev
+
+
+class _Launch:
+    """Makes ``dev`` and ``stream`` (None: that device's current stream) current
+    for a call: the library launches on the current device, and a workspace or
+    an output allocated meanwhile belongs to that stream."""
+    __slots__ = ("ctx", "dev", "stream")
+
+    def __init__(self, dev, stream):
+        self.dev, self.stream, self.ctx = dev, stream, None
+
+    def __enter__(self):
+        if self.stream is None:
+            if self.dev.index != torch.cuda.current_device():
+                self.ctx = torch.cuda.device(self.dev)
+                self.ctx.__enter__()
+            return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        st = self.stream
+        if not isinstance(st, torch.cuda.Stream):
+            st = torch.cuda.ExternalStream(int(st), device=self.dev)
+        if st.device != self.dev:
+            raise ValueError(f"the stream is on {st.device}, the tensors on {self.dev}")
+        self.ctx = torch.cuda.stream(st)
+        self.ctx.__enter__()
+        return ctypes.c_void_p(st.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _f32(what: str, t, shape):
+    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+        raise ValueError(f"{what}: expected a contiguous float32 tensor of shape {tuple(shape)}")
+
+
+def _tile_args(what: str, idx, count, capacity, block):
+    """(block, idx, count, capacity) of the C call; idx None: every pixel."""
+    if idx is None:
+        return 1, None, None, 0
+    if count is None or idx.dtype != torch.int32 or count.dtype != torch.int32 or not idx.is_contiguous():
+        raise ValueError(f"{what}: the tile list is a contiguous int32 [capacity, 2] with an int32 count")
+    if capacity > 0 and idx.numel() < 2 * capacity:
+        raise ValueError(f"{what}: the list holds {idx.numel() // 2} tiles, fewer than its capacity {capacity}")
+    return int(block), _ptr(idx), _ptr(count), int(capacity)
+
+
+def sige_qcache_write(x, cache: QCache, idx=None, count=None, capacity=0, block=1, gn_scale=None, gn_shift=None,
+                      silu=False, stream=None) -> QCache:
+    """Quantise the NHWC map ``x`` (bf16 or float32) into ``cache``, in place, at
+    the pixels under the tile list or, with ``idx`` None, at every pixel."""
+    if tuple(x.shape) != cache.shape:
+        raise ValueError(f"a map of shape {tuple(x.shape)} does not fit a cache of {cache.shape}")
+    xd = tensor_desc(x)
+    for name, t in (("gn_scale", gn_scale), ("gn_shift", gn_shift)):
+        _f32("sige_qcache_write: " + name, t, (x.shape[0], x.shape[3]))
+    b, i, c, cap = _tile_args("sige_qcache_write", idx, count, capacity, block)
+    dev = _on_device("sige_qcache_write", x, cache.codes, cache.scales, idx, count, gn_scale, gn_shift)
+    with _Launch(dev, stream) as st:
+        _check(lib().sige_qcache_write(_ptr(x), ctypes.byref(xd), _ptr(gn_scale), _ptr(gn_shift), int(bool(silu)), b, i,
+                                       c, cap, _ptr(cache.codes), _ptr(cache.scales), ctypes.byref(cache.desc), st),
+               "sige_qcache_write")
+    return cache
+
+
+def sige_qcache_read(cache: QCache, y=None, idx=None, count=None, capacity=0, block=1, dtype=torch.bfloat16,
+                     stream=None) -> torch.Tensor:
+    """What the cache stands for, into ``y`` [N, H, W, C] (bf16 or float32) at the
+    pixels under the tile list or at every pixel; other pixels keep their bytes
+    (zeros where ``y`` is allocated here, as ``dtype``)."""
+    if y is not None and tuple(y.shape) != cache.shape:
+        raise ValueError(f"a map of shape {tuple(y.shape)} does not fit a cache of {cache.shape}")
+    b, i, c, cap = _tile_args("sige_qcache_read", idx, count, capacity, block)
+    dev = _on_device("sige_qcache_read", cache.codes, cache.scales, y, idx, count)
+    with _Launch(dev, stream) as st:
+        if y is None:
+            y = (torch.empty if idx is None else torch.zeros)(cache.shape, dtype=dtype, device=dev)
+        yd = tensor_desc(y)
+        _check(lib().sige_qcache_read(_ptr(cache.codes), _ptr(cache.scales), ctypes.byref(cache.desc), b, i, c, cap,
+                                      _ptr(y), ctypes.byref(yd), st), "sige_qcache_read")
+    return y
+
+
+def sige_qlinear(a: QCache, w: QCache, bias=None, y=None, idx=None, count=None, capacity=0, block=1, residual=None,
+                 dtype=torch.bfloat16, workspace=None, stream=None) -> torch.Tensor:
+    """y = a w^T (8-bit integers, one scale per token and per output channel)
+    + bias + residual at the tokens under the tile list or at every token.
+    ``a``: an "s8" cache [N, H, W, C] with one scale a pixel; ``w``: an "s8"
+    cache [C_out, 1, 1, C] with one scale a row."""
+    shape = (*a.shape[:3], w.shape[0])
+    _f32("sige_qlinear: bias", bias, (shape[3],))
+    b, i, c, cap = _tile_args("sige_qlinear", idx, count, capacity, block)
+    dev = _on_device("sige_qlinear", a.codes, a.scales, w.codes, w.scales, bias, y, idx, count, residual, workspace)
+    with _Launch(dev, stream) as st:
+        if y is None:
+            y = (torch.empty if idx is None else torch.zeros)(shape, dtype=dtype, device=dev)
+        if residual is not None and (residual.shape != y.shape or residual.dtype != y.dtype or
+                                     not residual.is_contiguous()):
+            raise ValueError("sige_qlinear: the residual is a contiguous tensor of y's shape and dtype")
+        yd = tensor_desc(y)
+        if workspace is None:
+            workspace = zeros_workspace(WORKSPACE_HEADER, dev)
+        _check(lib().sige_qlinear(_ptr(a.codes), _ptr(a.scales), ctypes.byref(a.desc), _ptr(w.codes), _ptr(w.scales),
+                                  ctypes.byref(w.desc), _ptr(bias), b, i, c, cap, _ptr(residual), _ptr(y),
+                                  ctypes.byref(yd), _ptr(workspace), workspace.numel(), st), "sige_qlinear")
+    return y
+
+
+def sige_qlinear_path(c: int) -> int:
+    return int(lib().sige_qlinear_path(int(c)))
+
+
+def sige_attention_qcache(q, k: QCache, v: QCache, heads: int, o=None, idx=None, count=None, capacity=0, block=1,
+                          key_counts=None, workspace=None, stream=None) -> torch.Tensor:
+    """Attention of the tokens of ``q`` [N, H, W, D] (bf16) under the tile list,
+    or of every token, over the key and value caches ``k`` [N, h, w, D] and
+    ``v`` [N, h, w, Dv] (h * w keys; a context sequence is [N, keys, 1, *]),
+    into ``o`` [N, H, W, Dv].  ``key_counts``: int32 [N], the valid keys of each
+    item (0: its tokens get zeros)."""
+    if key_counts is not None and (key_counts.dtype != torch.int32 or key_counts.numel() != q.shape[0] or
+                                   not key_counts.is_contiguous()):
+        raise ValueError("sige_attention_qcache: key_counts is a contiguous int32 tensor of one count per item")
+    qd = tensor_desc(q)
+    shape = (*q.shape[:3], v.shape[3])
+    if o is not None and (tuple(o.shape) != shape or o.dtype != torch.bfloat16 or not o.is_contiguous()):
+        raise ValueError(f"sige_attention_qcache: o is a contiguous bf16 tensor of shape {shape}")
+    b, i, c, cap = _tile_args("sige_attention_qcache", idx, count, capacity, block)
+    dev = _on_device("sige_attention_qcache", q, k.codes, k.scales, v.codes, v.scales, o, idx, count, key_counts,
+                     workspace)
+    with _Launch(dev, stream) as st:
+        if o is None:
+            o = (torch.empty if idx is None else torch.zeros)(shape, dtype=torch.bfloat16, device=dev)
+        if workspace is None:
+            workspace = zeros_workspace(WORKSPACE_HEADER, dev)
+        _check(lib().sige_attention_qcache(_ptr(q), ctypes.byref(qd), _ptr(k.codes), _ptr(k.scales),
+                                           ctypes.byref(k.desc), _ptr(v.codes), _ptr(v.scales), ctypes.byref(v.desc),
+                                           _ptr(key_counts), int(heads), b, i, c, cap, _ptr(o), _ptr(workspace),
+                                           workspace.numel(), st), "sige_attention_qcache")
+    return o
+
+
+def sige_attention_qcache_path(dh: int, dvh: int) -> int:
+    return int(lib().sige_attention_qcache_path(int(dh), int(dvh)))
+
+
+def sige_attention_sparse_q(x, idx, count, capacity: int, block: int, wq: QCache, wo: QCache, bo, heads: int,
+                            k_map: QCache, v_map: QCache, y, wk: QCache | None = None, wv: QCache | None = None,
+                            residual=None, key_counts=None, workspace=None, stream=None):
+    """sige_attention_sparse with everything it keeps in codes: the tokens under
+    the tile list of ``x`` [N, H, W, C] are quantised (one scale a token), the
+    projections run in 8-bit integers (weights: "s8" caches [c_out, 1, 1, c_in]),
+    the key and value caches ``k_map`` / ``v_map`` (any format) are updated at
+    those tokens when ``wk`` / ``wv`` are given (self-attention; else they are
+    the context's), and y = o Wo + bo (+ residual) at those tokens of the
+    cached output ``y``."""
+    N, H, W, C = x.shape
+    dev = _on_device("sige_attention_sparse_q", x, y, k_map.codes, v_map.codes)
+    if not x.is_contiguous() or x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("sige_attention_sparse_q: x is a contiguous bf16 or float32 map")
+    where = dict(idx=idx, count=count, capacity=capacity, block=block)
+    with _Launch(dev, stream):
+        if workspace is None:
+            workspace = zeros_workspace(WORKSPACE_HEADER, dev)
+        xq = sige_qcache_write(x, qcache_empty(N, H, W, C, device=dev), **where)
+        q = torch.empty((N, H, W, wq.shape[0]), dtype=torch.bfloat16, device=dev)
+        sige_qlinear(xq, wq, None, q, workspace=workspace, **where)
+        for w, cache in ((wk, k_map), (wv, v_map)):
+            if w is not None:
+                t = torch.empty(cache.shape, dtype=torch.bfloat16, device=dev)
+                sige_qlinear(xq, w, None, t, workspace=workspace, **where)
+                sige_qcache_write(t, cache, **where)
+        o = torch.empty((N, H, W, v_map.shape[3]), dtype=torch.bfloat16, device=dev)
+        sige_attention_qcache(q, k_map, v_map, heads, o, key_counts=key_counts, workspace=workspace, **where)
+        oq = sige_qcache_write(o, qcache_empty(N, H, W, o.shape[3], device=dev), **where)
+        sige_qlinear(oq, wo, bo, y, residual=residual, workspace=workspace, **where)
     return y
 
 

@@ -1,0 +1,58 @@
+// Parameters of the attention step over a quantised key / value cache, shared
+// by its kernels.
+#pragma once
+
+#include "qcache.cuh"
+
+namespace sige {
+
+struct AttnQParams {
+    const __nv_bfloat16 *q;      // [N][H][W][D]
+    __nv_bfloat16 *o;            // [N][H][W][Dv]
+    const uint8_t *kc, *vc;      // codes [N][keys][D], [N][keys][Dv]
+    const float *ks, *vs;        // scales [N][keys][D / group], [N][keys][Dv / group]
+    const int32_t *key_counts;   // [N] or NULL: every key
+    const int32_t *idx, *count;  // tile list, or idx == NULL: every pixel
+    int32_t cap, b;
+    int32_t N, H, W, D, Dv, keys, heads, dh, dvh;
+    int32_t kfmt, vfmt;
+    int32_t kng, vng;            // scales of a key, of a value
+    int32_t kgroup, vgroup;
+    int64_t slots;               // most query slots of a batch item
+    float scale;                 // 1 / sqrt(dh)
+    UDiv dbb, db;
+    WsHeader *hdr;
+};
+
+// Query slots of one batch item on the device.
+__device__ __forceinline__ int query_slots(const AttnQParams &p)
+{
+    return p.idx ? max(0, min(__ldg(p.count), p.cap)) * p.b * p.b : p.H * p.W;
+}
+
+// The flat pixel (n H + y) W + x of query slot s (below query_slots) of item
+// n, -1 for a pixel outside the map.
+__device__ __forceinline__ int64_t query_pixel(const AttnQParams &p, int n, int s)
+{
+    if (!p.idx)
+        return (int64_t)n * p.H * p.W + s;
+    const uint32_t t = udiv((uint32_t)s, p.dbb), w = (uint32_t)s - t * (uint32_t)(p.b * p.b);
+    const uint32_t dy = udiv(w, p.db), dx = w - dy * (uint32_t)p.b;
+    const int2 org = __ldg(reinterpret_cast<const int2 *>(p.idx) + t);
+    if (org.x < 0 || org.y < 0 || org.x >= p.H || org.y >= p.W)
+        return -1;
+    const int y = org.x + (int)dy, x = org.y + (int)dx;
+    return y < p.H && x < p.W ? ((int64_t)n * p.H + y) * p.W + x : -1;
+}
+
+__device__ __forceinline__ int key_count(const AttnQParams &p, int n)
+{
+    return p.key_counts ? max(0, min(__ldg(p.key_counts + n), p.keys)) : p.keys;
+}
+
+// The tensor-core kernel: a sige_status, or 1 when the call is outside its
+// scope.
+int launch_attention_qcache_tc(const AttnQParams &p, cudaStream_t stream);
+bool attention_qcache_tc_scope(int dh, int dvh);
+
+} // namespace sige
