@@ -175,7 +175,8 @@ extern "C" int sige_qlinear(const void *a_codes, const float *a_scales, const si
     p.dtype = yd->dtype;
     p.rows = rows;
     p.hdr = static_cast<WsHeader *>(workspace);
-    return ql::launch_any(p, (cudaStream_t)stream);
+    const int tc = launch_qlinear_tc(p, (cudaStream_t)stream);
+    return tc != 1 ? tc : ql::launch_any(p, (cudaStream_t)stream);
 }
 
 extern "C" int sige_qlinear_path(int32_t c) { return c > 0 && qlinear_tc_scope(c) ? 1 : 0; }

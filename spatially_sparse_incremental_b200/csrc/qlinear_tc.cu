@@ -1,4 +1,609 @@
+// Product of 8-bit integers on the tensor cores (sige_qlinear): the integer
+// sums by tcgen05.mma kind::i8 (exact, int32 in tensor memory), the two scales,
+// bias and residual in the epilogue, one rounding into the cached output.
+//
+// A work unit is 128 rows x `bn` columns of the product, K in chunks of 128
+// bytes (four MMAs of 32):
+//   * many tokens: the tokens are the rows and bn (256 .. 32) output channels
+//     the columns;
+//   * at most kSwapTokens tokens: the output channels are the rows and the
+//     tokens (padded to 16) the columns, so that the 128 rows of an MMA are
+//     filled by the weights, whose reading bounds such a call.
+// The choice, bn and the K split depend on the number of tokens, which only
+// the device knows for a tile list, so every CTA derives them at its start.
+//   * warp 0 loads the operands by TMA into a ring of stages, 128-byte rows
+//     with the 128-byte swizzle (the K-major operands of the MMA): weights and
+//     whole maps by boxes, the tokens of a tile list by tile::gather4, four
+//     rows an instruction and lane, straight from the cache;
+//   * warp 1 issues the MMAs into one of two accumulators of up to 256
+//     columns, so that the next unit's products run under this one's epilogue;
+//   * warps 2 .. 9 (two warps to each quarter of the tensor memory's lanes,
+//     each with half of the columns) finish the outputs.
+// Where units are fewer than half the CTAs, a cluster's CTAs split a unit's K
+// chunks and exchange their int32 sums through distributed shared memory, each
+// finishing a slice of the columns; integer sums do not depend on the split.
+#include <algorithm>
+#include <atomic>
+
 #include "qlinear.cuh"
+#include "tc_ptx.cuh"
+
 namespace sige {
-bool qlinear_tc_scope(int) { return false; }
+namespace qt {
+
+constexpr int kEpiWarps = 8;
+constexpr int kEpiThreads = 32 * kEpiWarps;
+constexpr int kThreads = 64 + kEpiThreads;
+constexpr int kRows = 128;
+constexpr int kChunk = 128;              // bytes of K a stage
+constexpr int kMaxBn = 256;
+constexpr int kSplitBn = 64;             // widest unit whose K is split
+constexpr int kSwapTokens = 64;
+constexpr int kCluster = 4;
+constexpr int kMaxStages = 9;
+
+constexpr uint32_t kRing = 196608;       // 4 stages of 128 + 256 rows, more of narrower ones
+constexpr uint32_t kOffRecv = kRing;     // sums pushed by the other CTAs of a split unit
+constexpr uint32_t kRecvBytes = (kCluster - 1) * kRows * (kSplitBn / kCluster) * 4;
+constexpr uint32_t kOffCol = kOffRecv + kRecvBytes;          // per accumulator: column scales and biases
+constexpr uint32_t kOffTok = kOffCol + 2 * 2 * kMaxBn * 4;   // swapped units: the columns' pixels
+constexpr uint32_t kOffBar = kOffTok + kSwapTokens * 4;
+constexpr uint32_t kBarFull = 0;                             // + 8 stage
+constexpr uint32_t kBarEmpty = 8 * kMaxStages;
+constexpr uint32_t kBarAccFull = 16 * kMaxStages;            // + 8 accumulator
+constexpr uint32_t kBarAccEmpty = kBarAccFull + 16;
+constexpr uint32_t kBarRecv = kBarAccEmpty + 16;
+constexpr uint32_t kBarDrain = kBarRecv + 8;
+constexpr uint32_t kTmemSlot = kBarDrain + 8;
+constexpr uint32_t kAbort = kTmemSlot + 4;
+constexpr uint32_t kSmem = kOffBar + 256 + 1024;             // + alignment slack
+static_assert(kAbort + 4 <= 256, "barrier block");
+static_assert(kSmem <= 227 * 1024, "shared memory");
+
+// wait sites (the detail of a recorded SIGE_ERR_TIMEOUT)
+constexpr int kSiteEmpty = 301, kSiteFull = 302, kSiteAccEmpty = 303, kSiteAccFull = 304, kSiteRecv = 305;
+
+struct Plan {
+    int swap, bn, stages, split, nch;
+    uint32_t slots, rblocks, cblocks, units;
+};
+
+// The launch's work for `slots` tokens on `grid` CTAs in clusters of `cluster`.
+__host__ __device__ inline Plan make_plan(uint32_t slots, int Co, int C, int grid, int cluster)
+{
+    Plan q;
+    q.slots = slots;
+    q.nch = (C + kChunk - 1) / kChunk;
+    q.swap = slots <= kSwapTokens;
+    if (q.swap) {
+        // wide enough that every CTA of a split unit finishes 16 columns
+        const int least = cluster < 4 || q.nch < 4 ? 16 : q.nch < 8 ? 32 : 64;
+        q.bn = slots > 48 ? 64 : slots > 32 ? 48 : slots > 16 ? 32 : 16;
+        q.bn = q.bn > least ? q.bn : least;
+        q.rblocks = ((uint32_t)Co + kRows - 1) / kRows;
+        q.cblocks = slots > 0;
+    } else {
+        // the widest unit (fewest operand reads) that still gives every CTA one
+        q.rblocks = (slots + kRows - 1) / kRows;
+        int sh = 8;
+        while (sh > 5 && (q.rblocks * (((uint32_t)Co + (1u << sh) - 1) >> sh) < (uint32_t)grid || (1 << (sh - 1)) >= Co))
+            --sh;
+        q.bn = 1 << sh;
+        q.cblocks = ((uint32_t)Co + (1u << sh) - 1) >> sh;
+    }
+    q.units = q.rblocks * q.cblocks;
+    q.split = q.bn <= kSplitBn ? cluster : 1;
+    while (q.split > 1 && (q.units * (uint32_t)q.split > (uint32_t)grid || q.nch < 2 * q.split || q.bn % (16 * q.split)))
+        q.split >>= 1;
+    q.stages = q.bn > 128 ? 4 : q.bn > 64 ? 6 : q.bn > 32 ? 8 : 9;
+    return q;
 }
+static_assert(4 * (kRows + 256) * kChunk <= kRing && 6 * (kRows + 128) * kChunk <= kRing &&
+              8 * (kRows + 64) * kChunk <= kRing && 9 * (kRows + 32) * kChunk <= kRing && 9 <= kMaxStages, "ring");
+
+// kind::i8, A and B signed, D int32, both K-major, M = 128.
+__device__ __forceinline__ uint32_t idesc_s8(int n)
+{
+    return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_s8_w(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n .reg .pred p, e;\n .reg .b32 l;\n elect.sync l|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+                 " @e tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// Four rows of the token map into four 128-byte rows of a stage.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int r0, int r1,
+                                            int r2, int r3)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+                 : "memory");
+}
+
+// n columns of this warp's 32 tensor-memory lanes, without a wait.
+__device__ __forceinline__ void ld_cols(uint32_t taddr, int (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void ld_done() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void st_peer_s32x4(uint32_t addr, int a, int b, int c, int d)
+{
+    asm volatile("st.shared::cluster.v4.s32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ int4 lds_s32x4(uint32_t addr)
+{
+    int4 v;
+    asm volatile("ld.shared.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 lds_f32x4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); }
+
+struct Args {
+    QLinearParams q;
+    int vec;       // y and the residual take 16-byte accesses of whole groups of columns
+};
+
+// One output element.
+__device__ __forceinline__ void put1(const QLinearParams &p, int64_t e, float v)
+{
+    if (p.dtype == SIGE_BF16) {
+        if (p.residual)
+            v += __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.residual)[e]);
+        reinterpret_cast<__nv_bfloat16 *>(p.y)[e] = __float2bfloat16_rn(v);
+    } else {
+        if (p.residual)
+            v += reinterpret_cast<const float *>(p.residual)[e];
+        reinterpret_cast<float *>(p.y)[e] = v;
+    }
+}
+
+// 16 sums of one token from column c on: scales and biases from shared memory
+// (col: 16-byte rows of kMaxBn scales, then kMaxBn biases).
+__device__ __forceinline__ void finish16(const Args &a, const int (&acc)[16], uint32_t col, float sa, int64_t pix, int c)
+{
+    const QLinearParams &p = a.q;
+    float v[16];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const float4 s = lds_f32x4(col + 16u * q), b = lds_f32x4(col + 4u * kMaxBn + 16u * q);
+        v[4 * q] = qlinear_value(acc[4 * q], sa, s.x) + b.x;
+        v[4 * q + 1] = qlinear_value(acc[4 * q + 1], sa, s.y) + b.y;
+        v[4 * q + 2] = qlinear_value(acc[4 * q + 2], sa, s.z) + b.z;
+        v[4 * q + 3] = qlinear_value(acc[4 * q + 3], sa, s.w) + b.w;
+    }
+    const int64_t e = pix * p.Co + c;
+    if (!a.vec || c + 16 > p.Co) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            if (c + k < p.Co)
+                put1(p, e + k, v[k]);
+        return;
+    }
+    if (p.dtype == SIGE_BF16) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (p.residual) {
+                const uint4 r = ld_nc16(p.residual + e * 2 + 16 * h);
+                const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[8 * h + 2 * k] += bf16_lo(w[k]);
+                    v[8 * h + 2 * k + 1] += bf16_hi(w[k]);
+                }
+            }
+            const float *u = v + 8 * h;
+            *reinterpret_cast<uint4 *>(p.y + e * 2 + 16 * h) =
+                make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(u[4], u[5]), pack_bf16x2(u[6], u[7]));
+        }
+    } else {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            if (p.residual) {
+                const uint4 r = ld_nc16(p.residual + e * 4 + 16 * h);
+                v[4 * h] += __uint_as_float(r.x);
+                v[4 * h + 1] += __uint_as_float(r.y);
+                v[4 * h + 2] += __uint_as_float(r.z);
+                v[4 * h + 3] += __uint_as_float(r.w);
+            }
+            *reinterpret_cast<float4 *>(p.y + e * 4 + 16 * h) = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+        }
+    }
+}
+
+} // namespace qt
+
+using namespace qt;
+
+__global__ void __launch_bounds__(qt::kThreads, 1)
+    k_qlinear_tc(const __grid_constant__ qt::Args args, const __grid_constant__ CUtensorMap tw,
+                 const __grid_constant__ CUtensorMap tbox, const __grid_constant__ CUtensorMap trow)
+{
+    extern __shared__ __align__(1024) uint8_t qt_raw[];
+    const QLinearParams &p = args.q;
+    const uint32_t raw = smem_u32(qt_raw);
+    const uint32_t sb = (raw + 1023u) & ~1023u;
+    uint8_t *smem = qt_raw + (sb - raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t bar = sb + kOffBar;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffBar + kAbort);
+    WsHeader *hdr = p.hdr;
+    uint32_t csize;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kMaxStages; ++i) {
+            mbar_init(bar + kBarFull + 8u * i, 1);
+            mbar_init(bar + kBarEmpty + 8u * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar + kBarAccFull + 8u * i, 1);
+            mbar_init(bar + kBarAccEmpty + 8u * i, kEpiThreads);
+        }
+        mbar_init(bar + kBarDrain, 1);
+        *abort_flag = 0;
+    }
+    if (warp == 0 && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tw)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(p.px.idx ? &trow : &tbox)) : "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(bar + kTmemSlot),
+                     "r"(2 * kMaxBn));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    pdl_wait();
+    const Plan plan = make_plan((uint32_t)pixel_slots(p.px), p.Co, p.C, (int)gridDim.x, (int)csize);
+    const int split_n = plan.split;
+    const int per = (int)csize / split_n;                  // units a cluster takes at a time
+    const int rank = csize > 1 ? (int)cluster_rank() : 0;
+    const int sub = rank / split_n, split = rank - sub * split_n;
+    const uint32_t u_first = (blockIdx.x / csize) * (uint32_t)per + (uint32_t)sub;
+    const uint32_t u_step = (gridDim.x / csize) * (uint32_t)per;
+    const int c_lo = split * plan.nch / split_n, c_hi = (split + 1) * plan.nch / split_n;   // never empty
+    if (threadIdx.x == 0) {
+        // rows pushed by the other CTAs of the unit (each by 128 threads a half)
+        mbar_init(bar + kBarRecv, (uint32_t)max(1, (split_n - 1) * kEpiThreads));
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + kOffBar + kTmemSlot);
+    // the peers' barriers are initialised before the first push
+    if (csize > 1)
+        cluster_arrive();
+    bool joined = false;
+
+    const uint32_t stage_bytes = (uint32_t)(kRows + plan.bn) * kChunk;
+    if (warp == 0) {
+        // ---- operands
+        int it = 0, st = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        for (uint32_t u = u_first; ok && u < plan.units; u += u_step) {
+            const uint32_t rb = u / plan.cblocks;
+            const int cb = (int)(u - rb * plan.cblocks);
+            // this lane's four tokens of the unit (a padding slot reads row 0,
+            // and its products are not written)
+            int rows[4] = {0, 0, 0, 0};
+            const bool box = !plan.swap && !p.px.idx;
+            if (!box) {
+                const uint32_t s0 = (plan.swap ? 0 : rb * kRows) + 4 * lane;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (s0 + k < plan.slots)
+                        rows[k] = (int)max((int64_t)0, pixel_of(p.px, s0 + k));
+            }
+            for (int c = c_lo; c < c_hi; ++c, ++it) {
+                if (it >= plan.stages && !mbar_wait_w(bar + kBarEmpty + 8u * st, ph, abort_flag, hdr, kSiteEmpty)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t full = bar + kBarFull + 8u * st;
+                const uint32_t rdst = sb + (uint32_t)st * stage_bytes, cdst = rdst + kRows * kChunk;
+                const uint32_t tdst = plan.swap ? cdst : rdst, wdst = plan.swap ? rdst : cdst;
+                const int wrows = plan.swap ? kRows : plan.bn;
+                const int w0 = plan.swap ? (int)rb * kRows : cb * plan.bn;
+                if (lane == 0) {
+                    mbar_expect_tx(full, stage_bytes);
+                    for (int i = 0; i < wrows; i += 32)
+                        tma_load_2d(wdst + (uint32_t)i * kChunk, &tw, full, c * kChunk, w0 + i);
+                    if (box)
+                        tma_load_2d(tdst, &tbox, full, c * kChunk, (int)rb * kRows);
+                }
+                __syncwarp();
+                if (!box && 4 * lane < (plan.swap ? plan.bn : kRows))
+                    tma_gather4(tdst + (uint32_t)lane * 4 * kChunk, &trow, full, c * kChunk, rows[0], rows[1], rows[2],
+                                rows[3]);
+                __syncwarp();
+                if (++st == plan.stages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        if (!ok) {
+            // the copies in flight land before this CTA's memory is given up
+            for (int i = 0; i < min(it, plan.stages); ++i) {
+                const int k = it - 1 - i, s = k % plan.stages;
+                const long long t0 = clock64();
+                while (!mbar_try(bar + kBarFull + 8u * s, (k / plan.stages) & 1) && clock64() - t0 < kWaitCycles / 64)
+                    ;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---- products
+        const uint32_t id = idesc_s8(plan.bn);
+        int st = 0, nu = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (uint32_t u = u_first; ok && u < plan.units; u += u_step, ++nu) {
+            const int ab = nu & 1;
+            if (nu >= 2 && !mbar_wait_w(bar + kBarAccEmpty + 8u * ab, ((nu >> 1) & 1) ^ 1, abort_flag, hdr, kSiteAccEmpty)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem + (uint32_t)ab * kMaxBn;
+            for (int c = c_lo; c < c_hi; ++c) {
+                if (!mbar_wait_w(bar + kBarFull + 8u * st, ph, abort_flag, hdr, kSiteFull)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t ad = desc_sw128(sb + (uint32_t)st * stage_bytes);
+                const uint64_t bd = desc_sw128(sb + (uint32_t)st * stage_bytes + kRows * kChunk);
+                const int left = p.C - c * kChunk, steps = left >= kChunk ? 4 : (left + 31) / 32;
+                for (int k = 0; k < steps; ++k)
+                    mma_s8_w(d, ad + 2u * k, bd + 2u * k, id, c > c_lo || k > 0);
+                tc_commit_w(bar + kBarEmpty + 8u * st);
+                if (++st == plan.stages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+            if (ok)
+                tc_commit_w(bar + kBarAccFull + 8u * ab);
+        }
+        if (!ok) {
+            tc_commit_w(bar + kBarDrain);
+            const long long t0 = clock64();
+            while (!mbar_try(bar + kBarDrain, 0) && clock64() - t0 < kWaitCycles / 64)
+                ;
+        }
+        __syncwarp();
+    } else {
+        // ---- outputs
+        const int et = (int)threadIdx.x - 64;
+        const int r = (warp & 3) * 32 + lane;              // row of the unit = tensor-memory lane
+        const int half = (warp - 2) >> 2;
+        const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        int nu = 0;
+        bool ok = true;
+        for (uint32_t u = u_first; u < plan.units; u += u_step, ++nu) {
+            if (!ok) {   // a warp whose wait expired goes on meeting the others
+                epi_sync();
+                continue;
+            }
+            const int ab = nu & 1;
+            const uint32_t rb = u / plan.cblocks;
+            const int cb = (int)(u - rb * plan.cblocks);
+            const uint32_t col = sb + kOffCol + (uint32_t)ab * 2 * kMaxBn * 4;
+            float *colp = reinterpret_cast<float *>(smem + kOffCol + (uint32_t)ab * 2 * kMaxBn * 4);
+            int *tokp = reinterpret_cast<int *>(smem + kOffTok);
+            float rs = 0.0f, rbias = 0.0f;
+            int64_t pix = -1;
+            int chan = -1;
+            if (plan.swap) {
+                // columns: tokens (their scale and pixel); row: a channel
+                if (et < plan.bn) {
+                    const int64_t q = (uint32_t)et < plan.slots ? pixel_of(p.px, (uint32_t)et) : -1;
+                    tokp[et] = (int)q;
+                    colp[et] = q >= 0 ? __ldg(p.sa + q) : 0.0f;
+                }
+                chan = (int)rb * kRows + r < p.Co ? (int)rb * kRows + r : -1;
+                if (chan >= 0) {
+                    rs = __ldg(p.sw + chan);
+                    rbias = p.bias ? __ldg(p.bias + chan) : 0.0f;
+                }
+            } else {
+                if (et < plan.bn) {
+                    const int c = cb * plan.bn + et;
+                    colp[et] = c < p.Co ? __ldg(p.sw + c) : 0.0f;
+                    colp[kMaxBn + et] = c < p.Co && p.bias ? __ldg(p.bias + c) : 0.0f;
+                }
+                const uint32_t s = rb * kRows + (uint32_t)r;
+                pix = s < plan.slots ? pixel_of(p.px, s) : -1;
+                if (pix >= 0)
+                    rs = __ldg(p.sa + pix);
+            }
+            epi_sync();
+            if (!mbar_wait_w(bar + kBarAccFull + 8u * ab, (nu >> 1) & 1, abort_flag, hdr, kSiteAccFull)) {
+                ok = false;
+                continue;
+            }
+            tc_fence_after();
+            const uint32_t t_acc = t_row + (uint32_t)ab * kMaxBn;
+            // this CTA's columns: all, or its slice of a split unit
+            const int cw = plan.bn / split_n, col0 = split * cw;
+            if (split_n > 1) {
+                if (!joined) {
+                    cluster_wait();
+                    joined = true;
+                }
+                // push the other slices to their owners: 16 columns at a time,
+                // [sender][4 columns][row] of 16 bytes
+                for (int o = 1; o < split_n; ++o) {
+                    const int to = (split + o) % split_n;
+                    const int from = (split - to + split_n) % split_n - 1;   // this CTA among the owner's senders
+                    for (int g = 16 * half; g < cw; g += 32) {
+                        int acc[16];
+                        ld_cols(t_acc + (uint32_t)(to * cw + g), acc);
+                        ld_done();
+                        const uint32_t dst = map_peer(sb + kOffRecv + (uint32_t)((from * (cw / 4) + g / 4) * kRows + r) * 16,
+                                                      (uint32_t)(sub * split_n + to));
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            st_peer_s32x4(dst + (uint32_t)q * kRows * 16, acc[4 * q], acc[4 * q + 1], acc[4 * q + 2],
+                                          acc[4 * q + 3]);
+                    }
+                    mbar_arrive_peer(map_peer(bar + kBarRecv, (uint32_t)(sub * split_n + to)));
+                }
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar + kBarRecv, 0, abort_flag, hdr, kSiteRecv))) {
+                    ok = false;
+                    continue;
+                }
+            }
+            for (int g = 16 * half; g < cw; g += 32) {
+                int acc[16];
+                ld_cols(t_acc + (uint32_t)(col0 + g), acc);
+                ld_done();
+                for (int f = 0; f < split_n - 1; ++f) {
+                    const uint32_t src = sb + kOffRecv + (uint32_t)((f * (cw / 4) + g / 4) * kRows + r) * 16;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int4 v = lds_s32x4(src + (uint32_t)q * kRows * 16);
+                        acc[4 * q] += v.x;
+                        acc[4 * q + 1] += v.y;
+                        acc[4 * q + 2] += v.z;
+                        acc[4 * q + 3] += v.w;
+                    }
+                }
+                if (plan.swap) {
+                    if (chan >= 0) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const int t = tokp[col0 + g + k];
+                            if (t >= 0)
+                                put1(p, (int64_t)t * p.Co + chan, qlinear_value(acc[k], colp[col0 + g + k], rs) + rbias);
+                        }
+                    }
+                } else if (pix >= 0) {
+                    finish16(args, acc, col + 4u * (uint32_t)(col0 + g), rs, pix, cb * plan.bn + col0 + g);
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(bar + kBarAccEmpty + 8u * ab);
+        }
+    }
+    if (csize > 1 && !joined)
+        cluster_wait();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * kMaxBn));
+    }
+    // no CTA leaves while a peer may still address its shared memory
+    if (csize > 1) {
+        cluster_arrive();
+        cluster_wait();
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+static bool encode_rows(CUtensorMap *map, const void *base, int64_t rows, int C, int box_rows, CUtensorMapL2promotion l2,
+                        PFN_cuTensorMapEncodeTiled_v12000 encode)
+{
+    cuuint64_t dims[2] = {(cuuint64_t)C, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)C};
+    cuuint32_t box[2] = {(cuuint32_t)qt::kChunk, (cuuint32_t)box_rows};
+    cuuint32_t es[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, l2,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool qlinear_tc_scope(int c) { return c % 16 == 0; }
+
+int launch_qlinear_tc(const QLinearParams &p, cudaStream_t stream)
+{
+    // (units are counted in 32 bits)
+    const int64_t narrowest = ((p.slots + qt::kRows - 1) / qt::kRows) * (((int64_t)p.Co + 31) / 32);
+    if (!qlinear_tc_scope(p.C) || !aligned_to(p.a, 16) || !aligned_to(p.w, 16) || narrowest > INT32_MAX / 8)
+        return 1;
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = get_encode();
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return SIGE_ERR_CUDA;
+    CUtensorMap tw, tbox, trow;
+    if (!encode || !encode_rows(&tw, p.w, p.Co, p.C, 32, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, encode) ||
+        !encode_rows(&tbox, p.a, p.rows, p.C, qt::kRows, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, encode) ||
+        !encode_rows(&trow, p.a, p.rows, p.C, 1, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, encode))
+        return SIGE_ERR_CUDA;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = qt::kCluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(qt::kThreads);
+    cfg.dynamicSmemBytes = qt::kSmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    static std::atomic<int> clusters_of[64];   // co-resident clusters, per device
+    int ncl = clusters_of[dev].load(std::memory_order_acquire);
+    if (ncl == 0) {
+        if (cudaFuncSetAttribute(k_qlinear_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)qt::kSmem) != cudaSuccess) {
+            cudaGetLastError();
+            return SIGE_ERR_CUDA;
+        }
+        cfg.gridDim = dim3(qt::kCluster * (device_sm_count() / qt::kCluster));
+        cfg.attrs = attr + 1;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&ncl, k_qlinear_tc, &cfg) != cudaSuccess || ncl < 1) {
+            cudaGetLastError();
+            return SIGE_ERR_CUDA;
+        }
+        cfg.attrs = attr;
+        clusters_of[dev].store(ncl, std::memory_order_release);
+    }
+    prefer_max_shared(k_qlinear_tc);
+    qt::Args a{};
+    a.q = p;
+    const int esz = p.dtype == SIGE_BF16 ? 2 : 4;
+    a.vec = (int64_t)p.Co * esz % 16 == 0 && aligned_to(p.y, 16) && aligned_to(p.residual, 16);
+    // a whole map of enough units needs no cluster (every SM takes part); a
+    // list's length is known on the device only
+    const int sms = device_sm_count();
+    const bool solo = !p.px.idx && qt::make_plan((uint32_t)p.slots, p.Co, p.C, sms, qt::kCluster).split == 1;
+    cfg.numAttrs = solo ? 1 : 2;
+    if (solo) {
+        const qt::Plan plan = qt::make_plan((uint32_t)p.slots, p.Co, p.C, sms, 1);
+        cfg.gridDim = dim3((unsigned)std::min<int64_t>(sms, plan.units));
+    } else {
+        // no more clusters than the narrowest units of a full list can use
+        cfg.gridDim = dim3((unsigned)(qt::kCluster * std::max<int64_t>(1, std::min<int64_t>(ncl, narrowest))));
+    }
+    if (cudaLaunchKernelEx(&cfg, k_qlinear_tc, a, tw, tbox, trow) != cudaSuccess) {
+        cudaGetLastError();
+        return SIGE_ERR_CUDA;
+    }
+    count_launch();
+    return launch_check();
+}
+
+} // namespace sige
