@@ -540,31 +540,25 @@ class QCache:
     channel in the low half) and ``scales`` float32 [N, H, W, C / group]; a
     code stands for code * scale.  A view of the two tensors: nothing is
     copied or kept."""
-    __slots__ = ("codes", "scales", "format", "desc")
+    __slots__ = ("codes", "scales", "format", "shape", "desc")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, format: str):
         if format not in _QFMT:
             raise ValueError(f"unknown format {format!r}: one of {sorted(_QFMT)}")
         if codes.dtype != _QSTORE[format] or scales.dtype != torch.float32:
             raise ValueError(f"{format} codes are {_QSTORE[format]}, scales are torch.float32")
-        if codes.dim() != 4 or scales.dim() != 4 or codes.shape[:3] != scales.shape[:3]:
+        cs, ss = codes.shape, scales.shape
+        if len(cs) != 4 or len(ss) != 4 or cs[:3] != ss[:3]:
             raise ValueError("expected codes and scales [N, H, W, *] of one map")
         if not codes.is_contiguous() or not scales.is_contiguous():
             raise ValueError("expected contiguous codes and scales")
-        if codes.device != scales.device:
-            raise ValueError("codes and scales are on different devices")
-        n, h, w, c = codes.shape
+        n, h, w, c = cs
         c = 2 * c if format == "s4" else c
-        ng = scales.shape[3]
+        ng = ss[3]
         if ng < 1 or c % ng:
             raise ValueError(f"{ng} scales a pixel do not divide {c} channels")
-        self.codes, self.scales, self.format = codes, scales, format
+        self.codes, self.scales, self.format, self.shape = codes, scales, format, (n, h, w, c)
         self.desc = QCacheDesc(n, h, w, c, _QFMT[format], c // ng)
-
-    @property
-    def shape(self):
-        d = self.desc
-        return d.n, d.h, d.w, d.c
 
     @property
     def group(self) -> int:
@@ -589,51 +583,66 @@ def sige_qcache_scales(cd: QCacheDesc) -> int:
     return int(lib().sige_qcache_scales(ctypes.byref(cd)))
 
 
-def _on_device(what: str, *tensors) -> torch.device:
-    """The CUDA device that all the given tensors are on."""
+def _device_index(what: str, *tensors) -> int:
+    """Index of the CUDA device that all the given tensors (None: left out) are on."""
     dev = None
     for t in tensors:
-        if t is None:
-            continue
-        if t.device.type != "cuda":
-            raise ValueError(f"{what}: expected tensors on a CUDA device")
-        if dev is not None and t.device != dev:
-            raise ValueError(f"{what}: tensors on different devices ({dev} and {t.device})")
-        dev = t.device
+        if t is not None:
+            d = t.get_device()
+            if d != dev:
+                if d < 0:
+                    raise ValueError(f"{what}: expected tensors on a CUDA device")
+                if dev is not None:
+                    raise ValueError(f"{what}: tensors on different devices (cuda:{dev} and cuda:{d})")
+                dev = d
     return dev
 
 
 class _Launch:
-    """Makes ``dev`` and ``stream`` (None: that device's current stream) current
-    for a call: the library launches on the current device, and a workspace or
-    an output allocated meanwhile belongs to that stream."""
+    """Makes device ``dev`` and ``stream`` (None: that device's current stream)
+    current for a call and gives the stream's handle: the library launches on
+    the current device, and a workspace or an output allocated meanwhile
+    belongs to that stream."""
     __slots__ = ("ctx", "dev", "stream")
 
-    def __init__(self, dev, stream):
+    def __init__(self, dev: int, stream):
         self.dev, self.stream, self.ctx = dev, stream, None
 
     def __enter__(self):
-        if self.stream is None:
-            if self.dev.index != torch.cuda.current_device():
+        st = self.stream
+        if st is None:
+            if self.dev != torch.cuda.current_device():
                 self.ctx = torch.cuda.device(self.dev)
                 self.ctx.__enter__()
-            return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-        st = self.stream
+            return torch._C._cuda_getCurrentRawStream(self.dev)
         if not isinstance(st, torch.cuda.Stream):
             st = torch.cuda.ExternalStream(int(st), device=self.dev)
-        if st.device != self.dev:
-            raise ValueError(f"the stream is on {st.device}, the tensors on {self.dev}")
+        if st.device.index != self.dev:
+            raise ValueError(f"the stream is on {st.device}, the tensors on cuda:{self.dev}")
         self.ctx = torch.cuda.stream(st)
         self.ctx.__enter__()
-        return ctypes.c_void_p(st.cuda_stream)
+        return st.cuda_stream
 
     def __exit__(self, *exc):
         if self.ctx is not None:
             self.ctx.__exit__(*exc)
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _map_desc(what: str, t, shape) -> TensorDesc:
+    """Descriptor of a contiguous NHWC map of that shape."""
+    if t.shape != shape:
+        raise ValueError(f"{what}: a map of shape {tuple(t.shape)} does not fit, {tuple(shape)} is expected")
+    if not t.is_contiguous() or t.dtype not in _DT:
+        raise ValueError(f"{what}: expected a contiguous bf16 or float32 map")
+    return TensorDesc(*shape, _DT[t.dtype], NHWC)
+
+
 def _f32(what: str, t, shape):
-    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+    if t is not None and (t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous()):
         raise ValueError(f"{what}: expected a contiguous float32 tensor of shape {tuple(shape)}")
 
 
@@ -641,28 +650,29 @@ def _tile_args(what: str, idx, count, capacity, block):
     """(block, idx, count, capacity) of the C call; idx None: every pixel."""
     if idx is None:
         return 1, None, None, 0
-    if count is None or idx.dtype != torch.int32 or count.dtype != torch.int32 or not idx.is_contiguous():
+    if count is None or idx.dtype != torch.int32 or count.dtype != torch.int32 or not idx.is_contiguous() or \
+            count.numel() < 1:
         raise ValueError(f"{what}: the tile list is a contiguous int32 [capacity, 2] with an int32 count")
     if capacity > 0 and idx.numel() < 2 * capacity:
         raise ValueError(f"{what}: the list holds {idx.numel() // 2} tiles, fewer than its capacity {capacity}")
-    return int(block), _ptr(idx), _ptr(count), int(capacity)
+    return block, idx.data_ptr(), count.data_ptr(), capacity
 
 
 def sige_qcache_write(x, cache: QCache, idx=None, count=None, capacity=0, block=1, gn_scale=None, gn_shift=None,
                       silu=False, stream=None) -> QCache:
     """Quantise the NHWC map ``x`` (bf16 or float32) into ``cache``, in place, at
     the pixels under the tile list or, with ``idx`` None, at every pixel."""
-    if tuple(x.shape) != cache.shape:
-        raise ValueError(f"a map of shape {tuple(x.shape)} does not fit a cache of {cache.shape}")
-    xd = tensor_desc(x)
-    for name, t in (("gn_scale", gn_scale), ("gn_shift", gn_shift)):
-        _f32("sige_qcache_write: " + name, t, (x.shape[0], x.shape[3]))
-    b, i, c, cap = _tile_args("sige_qcache_write", idx, count, capacity, block)
-    dev = _on_device("sige_qcache_write", x, cache.codes, cache.scales, idx, count, gn_scale, gn_shift)
+    what = "sige_qcache_write"
+    xd = _map_desc(what, x, cache.shape)
+    if gn_scale is not None or gn_shift is not None:
+        _f32(what + ": gn_scale", gn_scale, (xd.n, xd.c))
+        _f32(what + ": gn_shift", gn_shift, (xd.n, xd.c))
+    b, i, c, cap = _tile_args(what, idx, count, capacity, block)
+    dev = _device_index(what, x, cache.codes, cache.scales, idx, count, gn_scale, gn_shift)
     with _Launch(dev, stream) as st:
-        _check(lib().sige_qcache_write(_ptr(x), ctypes.byref(xd), _ptr(gn_scale), _ptr(gn_shift), int(bool(silu)), b, i,
-                                       c, cap, _ptr(cache.codes), _ptr(cache.scales), ctypes.byref(cache.desc), st),
-               "sige_qcache_write")
+        _check(lib().sige_qcache_write(x.data_ptr(), ctypes.byref(xd), _addr(gn_scale), _addr(gn_shift),
+                                       1 if silu else 0, b, i, c, cap, cache.codes.data_ptr(), cache.scales.data_ptr(),
+                                       ctypes.byref(cache.desc), st), what)
     return cache
 
 
@@ -671,16 +681,15 @@ def sige_qcache_read(cache: QCache, y=None, idx=None, count=None, capacity=0, bl
     """What the cache stands for, into ``y`` [N, H, W, C] (bf16 or float32) at the
     pixels under the tile list or at every pixel; other pixels keep their bytes
     (zeros where ``y`` is allocated here, as ``dtype``)."""
-    if y is not None and tuple(y.shape) != cache.shape:
-        raise ValueError(f"a map of shape {tuple(y.shape)} does not fit a cache of {cache.shape}")
-    b, i, c, cap = _tile_args("sige_qcache_read", idx, count, capacity, block)
-    dev = _on_device("sige_qcache_read", cache.codes, cache.scales, y, idx, count)
+    what = "sige_qcache_read"
+    b, i, c, cap = _tile_args(what, idx, count, capacity, block)
+    dev = _device_index(what, cache.codes, cache.scales, y, idx, count)
     with _Launch(dev, stream) as st:
         if y is None:
-            y = (torch.empty if idx is None else torch.zeros)(cache.shape, dtype=dtype, device=dev)
-        yd = tensor_desc(y)
-        _check(lib().sige_qcache_read(_ptr(cache.codes), _ptr(cache.scales), ctypes.byref(cache.desc), b, i, c, cap,
-                                      _ptr(y), ctypes.byref(yd), st), "sige_qcache_read")
+            y = (torch.empty if idx is None else torch.zeros)(cache.shape, dtype=dtype, device=cache.codes.device)
+        yd = _map_desc(what, y, cache.shape)
+        _check(lib().sige_qcache_read(cache.codes.data_ptr(), cache.scales.data_ptr(), ctypes.byref(cache.desc), b, i, c,
+                                      cap, y.data_ptr(), ctypes.byref(yd), st), what)
     return y
 
 
@@ -690,22 +699,24 @@ def sige_qlinear(a: QCache, w: QCache, bias=None, y=None, idx=None, count=None, 
     + bias + residual at the tokens under the tile list or at every token.
     ``a``: an "s8" cache [N, H, W, C] with one scale a pixel; ``w``: an "s8"
     cache [C_out, 1, 1, C] with one scale a row."""
-    shape = (*a.shape[:3], w.shape[0])
+    what = "sige_qlinear"
+    n, h, wd, _ = a.shape
+    shape = (n, h, wd, w.shape[0])
     _f32("sige_qlinear: bias", bias, (shape[3],))
-    b, i, c, cap = _tile_args("sige_qlinear", idx, count, capacity, block)
-    dev = _on_device("sige_qlinear", a.codes, a.scales, w.codes, w.scales, bias, y, idx, count, residual, workspace)
+    b, i, c, cap = _tile_args(what, idx, count, capacity, block)
+    dev = _device_index(what, a.codes, a.scales, w.codes, w.scales, bias, y, idx, count, residual, workspace)
     with _Launch(dev, stream) as st:
         if y is None:
-            y = (torch.empty if idx is None else torch.zeros)(shape, dtype=dtype, device=dev)
+            y = (torch.empty if idx is None else torch.zeros)(shape, dtype=dtype, device=a.codes.device)
         if residual is not None and (residual.shape != y.shape or residual.dtype != y.dtype or
                                      not residual.is_contiguous()):
             raise ValueError("sige_qlinear: the residual is a contiguous tensor of y's shape and dtype")
-        yd = tensor_desc(y)
+        yd = _map_desc(what, y, shape)
         if workspace is None:
-            workspace = zeros_workspace(WORKSPACE_HEADER, dev)
-        _check(lib().sige_qlinear(_ptr(a.codes), _ptr(a.scales), ctypes.byref(a.desc), _ptr(w.codes), _ptr(w.scales),
-                                  ctypes.byref(w.desc), _ptr(bias), b, i, c, cap, _ptr(residual), _ptr(y),
-                                  ctypes.byref(yd), _ptr(workspace), workspace.numel(), st), "sige_qlinear")
+            workspace = zeros_workspace(WORKSPACE_HEADER, a.codes.device)
+        _check(lib().sige_qlinear(a.codes.data_ptr(), a.scales.data_ptr(), ctypes.byref(a.desc), w.codes.data_ptr(),
+                                  w.scales.data_ptr(), ctypes.byref(w.desc), _addr(bias), b, i, c, cap, _addr(residual),
+                                  y.data_ptr(), ctypes.byref(yd), workspace.data_ptr(), workspace.nbytes, st), what)
     return y
 
 
@@ -720,25 +731,28 @@ def sige_attention_qcache(q, k: QCache, v: QCache, heads: int, o=None, idx=None,
     ``v`` [N, h, w, Dv] (h * w keys; a context sequence is [N, keys, 1, *]),
     into ``o`` [N, H, W, Dv].  ``key_counts``: int32 [N], the valid keys of each
     item (0: its tokens get zeros)."""
+    what = "sige_attention_qcache"
     if key_counts is not None and (key_counts.dtype != torch.int32 or key_counts.numel() != q.shape[0] or
                                    not key_counts.is_contiguous()):
         raise ValueError("sige_attention_qcache: key_counts is a contiguous int32 tensor of one count per item")
-    qd = tensor_desc(q)
-    shape = (*q.shape[:3], v.shape[3])
-    if o is not None and (tuple(o.shape) != shape or o.dtype != torch.bfloat16 or not o.is_contiguous()):
+    qs = q.shape
+    if len(qs) != 4 or q.dtype != torch.bfloat16:
+        raise ValueError("sige_attention_qcache: q is a bf16 map [N, H, W, D]")
+    qd = _map_desc(what, q, qs)
+    shape = (qs[0], qs[1], qs[2], v.shape[3])
+    if o is not None and (o.shape != shape or o.dtype != torch.bfloat16 or not o.is_contiguous()):
         raise ValueError(f"sige_attention_qcache: o is a contiguous bf16 tensor of shape {shape}")
-    b, i, c, cap = _tile_args("sige_attention_qcache", idx, count, capacity, block)
-    dev = _on_device("sige_attention_qcache", q, k.codes, k.scales, v.codes, v.scales, o, idx, count, key_counts,
-                     workspace)
+    b, i, c, cap = _tile_args(what, idx, count, capacity, block)
+    dev = _device_index(what, q, k.codes, k.scales, v.codes, v.scales, o, idx, count, key_counts, workspace)
     with _Launch(dev, stream) as st:
         if o is None:
-            o = (torch.empty if idx is None else torch.zeros)(shape, dtype=torch.bfloat16, device=dev)
+            o = (torch.empty if idx is None else torch.zeros)(shape, dtype=torch.bfloat16, device=q.device)
         if workspace is None:
-            workspace = zeros_workspace(WORKSPACE_HEADER, dev)
-        _check(lib().sige_attention_qcache(_ptr(q), ctypes.byref(qd), _ptr(k.codes), _ptr(k.scales),
-                                           ctypes.byref(k.desc), _ptr(v.codes), _ptr(v.scales), ctypes.byref(v.desc),
-                                           _ptr(key_counts), int(heads), b, i, c, cap, _ptr(o), _ptr(workspace),
-                                           workspace.numel(), st), "sige_attention_qcache")
+            workspace = zeros_workspace(WORKSPACE_HEADER, q.device)
+        _check(lib().sige_attention_qcache(q.data_ptr(), ctypes.byref(qd), k.codes.data_ptr(), k.scales.data_ptr(),
+                                           ctypes.byref(k.desc), v.codes.data_ptr(), v.scales.data_ptr(),
+                                           ctypes.byref(v.desc), _addr(key_counts), heads, b, i, c, cap, o.data_ptr(),
+                                           workspace.data_ptr(), workspace.nbytes, st), what)
     return o
 
 
@@ -757,11 +771,9 @@ def sige_attention_sparse_q(x, idx, count, capacity: int, block: int, wq: QCache
     the context's), and y = o Wo + bo (+ residual) at those tokens of the
     cached output ``y``."""
     N, H, W, C = x.shape
-    dev = _on_device("sige_attention_sparse_q", x, y, k_map.codes, v_map.codes)
-    if not x.is_contiguous() or x.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("sige_attention_sparse_q: x is a contiguous bf16 or float32 map")
+    dev = x.device
     where = dict(idx=idx, count=count, capacity=capacity, block=block)
-    with _Launch(dev, stream):
+    with _Launch(_device_index("sige_attention_sparse_q", x, y, k_map.codes, v_map.codes), stream):
         if workspace is None:
             workspace = zeros_workspace(WORKSPACE_HEADER, dev)
         xq = sige_qcache_write(x, qcache_empty(N, H, W, C, device=dev), **where)

@@ -258,7 +258,8 @@ extern "C" int sige_attention_qcache(const void *q, const sige_tensor_desc *qd, 
     p.scale = (float)(1.0 / std::sqrt((double)p.dh));
     p.dbb = px.dbb; p.db = px.db;
     p.hdr = static_cast<WsHeader *>(workspace);
-    return aq::launch(p, (cudaStream_t)stream);
+    const int tc = launch_attention_qcache_tc(p, (cudaStream_t)stream);
+    return tc != 1 ? tc : aq::launch(p, (cudaStream_t)stream);
 }
 
 extern "C" int sige_attention_qcache_path(int32_t dh, int32_t dvh)

@@ -1,4 +1,761 @@
+// Tensor-core form of the attention step over a quantised key / value cache
+// (sige_attention_qcache): o = softmax(q K^T / sqrt(dh)) V with K and V in
+// codes.  A code is an integer of at most 8 bits or an e4m3 value: exact in
+// bf16.  So both products run on the codes as bf16 operands, and the scales,
+// one per key and head, are applied in float32 where a score meets its key: to
+// the score before the softmax (key scale), to the weight after it (value
+// scale); the only rounding of an operand is that of weight * scale to bf16.
+//
+// Work unit: 128 query slots of one (batch item, head), the keys in chunks of
+// 64.  Roles of a CTA's 12 warps:
+//   * warps 9 .. 11 stage the operands: the unit's queries once, and for each
+//     chunk the codes (global loads of 8 codes a lane, one chunk ahead), turned
+//     into bf16 rows of 128 bytes with the 128-byte swizzle (K-major for the
+//     first product, MN-major for the second), and the chunk's scales;
+//   * warp 8 issues S = Q K^T (M 128, N 64) and O += P V (M 128, K 64);
+//   * warps 0 .. 3 and 4 .. 7 are two softmax groups that take every other
+//     chunk, one query row a thread: running maximum and sum (float32),
+//     P = 2^(s - max) * value scale as bf16 over the chunk's own S columns, the
+//     O row in tensor memory rescaled only when the maximum has grown by more
+//     than 8 (base 2).  Each group has two S buffers, so the scores of its next
+//     chunk are there when it has finished one; with one group waiting the
+//     other keeps the exponentials busy.
+// The groups' rows (O, max, sum) are merged through shared memory at the end
+// of a unit.  Where units are fewer than half the CTAs, the CTAs of a cluster
+// also split the keys and push their rows to the row's owner through
+// distributed shared memory.
+#include <algorithm>
+#include <atomic>
+#include <math.h>
+
 #include "attention_qcache.cuh"
+#include "attn_ptx.cuh"
+
 namespace sige {
-bool attention_qcache_tc_scope(int, int) { return false; }
+namespace at {
+
+using namespace attn;
+
+constexpr int kRows = 128;
+constexpr int kKeys = 64;           // keys of a chunk
+constexpr int kGroup = 128;         // threads of a softmax group
+constexpr int kSoft = 2 * kGroup;
+constexpr int kStage = 96;          // staging threads (12 warps: 3 to a scheduler, 168 registers a thread)
+constexpr int kThreads = kSoft + 32 + kStage;
+constexpr int kCluster = 4;
+constexpr int kMaxStages = 6;
+
+// Shared memory for heads of up to KD (64 or 128) channels.
+template <int KD>
+struct Lay {
+    static constexpr int kAtoms = KD / 64;                            // 64-channel blocks of 128-byte rows
+    static constexpr int kStages = KD == 64 ? 6 : 3;                  // chunk ring
+    static constexpr int kAhead = KD == 64 ? 4 : 2;                   // chunks whose S may be issued before their P V:
+                                                                      // fewer than the ring's, whose next is being staged
+    static constexpr uint32_t kQAtom = kRows * 128, kKvAtom = kKeys * 128;
+    static constexpr uint32_t kOffQ = 0;
+    static constexpr uint32_t kOffX = kAtoms * kQAtom;                // rows exchanged by the two groups
+    static constexpr uint32_t kOffK = kOffX + kRows * KD * 4;         // [stage][K atoms, V atoms]
+    static constexpr uint32_t kKvStage = 2 * kAtoms * kKvAtom;
+    static constexpr uint32_t kOffSc = kOffK + kStages * kKvStage;    // [stage][64 key scales, 64 value scales]
+    static constexpr uint32_t kOffMl = kOffSc + kStages * 512;        // [256] (max, sum)
+    static constexpr uint32_t kOffBar = kOffMl + 2048;
+    static constexpr uint32_t kBytes = kOffBar + 256 + 1024;          // + alignment slack
+    // rows pushed by the CTAs of a split unit, over the exchange rows and the
+    // ring (both idle by then): 256 rows of KD floats
+    static constexpr uint32_t kOffPush = kOffX;
+    static_assert(kOffPush + 256 * KD * 4 <= kOffSc, "pushed rows");
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+constexpr uint32_t kBarKvFull = 0;      // + 8 stage
+constexpr uint32_t kBarKvEmpty = 48;    // + 8 stage
+constexpr uint32_t kBarSFull = 96;      // + 16 group + 8 buffer
+constexpr uint32_t kBarPFull = 128;     // + 16 group + 8 buffer
+constexpr uint32_t kBarPvDone = 160;    // + 8 group
+constexpr uint32_t kBarQFull = 176;
+constexpr uint32_t kBarQEmpty = 184;
+constexpr uint32_t kBarReady = 192;     // every CTA of a split unit has finished its products
+constexpr uint32_t kBarPush = 200;      // the rows this CTA owns have been pushed
+constexpr uint32_t kBarDrain = 208;
+constexpr uint32_t kTmemSlot = 216;
+constexpr uint32_t kAbort = 220;
+constexpr uint32_t kTmemCols = 512;     // S / P: four buffers of 64 columns, O: 256 + 128 group
+constexpr uint32_t kTmemO = 256;
+
+// wait sites (the detail of a recorded SIGE_ERR_TIMEOUT)
+constexpr int kSiteKvEmpty = 401, kSiteKvFull = 402, kSiteQEmpty = 403, kSitePFull = 404, kSiteQFull = 405,
+              kSiteSFull = 406, kSitePvDone = 407, kSiteReady = 408, kSitePush = 409;
+
+struct Args {
+    AttnQParams a;
+    int32_t dhp, dvp;         // head widths padded to 16
+    float sc;                 // log2(e) / sqrt(dh): scores in base-2 exponent units
+    UDiv dkv, dvv;            // 8-channel vectors of a key row (padded), of a value row
+};
+
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b)
+{
+    __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
+    return *reinterpret_cast<uint32_t *>(&r);
 }
+
+// Two codes to a pair of bf16, exactly.  Integers by way of the bf16 numbers
+// 128 + n (0x4300 | n, n < 128, unit spacing): a signed code is its low bits
+// less the weight of its sign bit, so (128 + low) - (128 + sign weight) is one
+// exact subtraction (256 = 0x4380).
+__device__ __forceinline__ uint32_t s8_pair(uint32_t t)   // codes in the low bytes of the halves
+{
+    return sub_bf16x2((t & 0x007F007Fu) | 0x43004300u, (t & 0x00800080u) | 0x43004300u);
+}
+__device__ __forceinline__ uint32_t s4_pair(uint32_t t)   // codes in the low nibbles of the halves
+{
+    return sub_bf16x2((t & 0x00070007u) | 0x43004300u, (t & 0x00080008u) | 0x43004300u);
+}
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t t)  // codes in the two low bytes
+{
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)t, __NV_E4M3);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    return pack_bf16x2(f.x, f.y);
+}
+
+// 8 codes (two words; one for s4) to 8 bf16.
+template <int kFmt>
+__device__ __forceinline__ uint4 codes8(uint2 w)
+{
+    if constexpr (kFmt == SIGE_Q_S8) {
+        return make_uint4(s8_pair(__byte_perm(w.x, 0, 0x4140)), s8_pair(__byte_perm(w.x, 0, 0x4342)),
+                          s8_pair(__byte_perm(w.y, 0, 0x4140)), s8_pair(__byte_perm(w.y, 0, 0x4342)));
+    } else if constexpr (kFmt == SIGE_Q_E4M3) {
+        return make_uint4(e4m3_pair(w.x & 0xFFFFu), e4m3_pair(w.x >> 16), e4m3_pair(w.y & 0xFFFFu),
+                          e4m3_pair(w.y >> 16));
+    } else {
+        const uint32_t lo = w.x, hi = w.x << 12;   // even codes in lo, odd ones in hi's upper half
+        return make_uint4(s4_pair((lo & 0xFu) | (hi & 0xF0000u)), s4_pair(((lo >> 8) & 0xFu) | ((hi >> 8) & 0xF0000u)),
+                          s4_pair(((lo >> 16) & 0xFu) | ((w.x >> 4) & 0xF0000u)),
+                          s4_pair(((lo >> 24) & 0xFu) | ((w.x >> 12) & 0xF0000u)));
+    }
+}
+
+__device__ __forceinline__ uint2 load_codes8(const uint8_t *codes, int64_t e, int fmt)
+{
+    if (fmt == SIGE_Q_S4)
+        return make_uint2(__ldg(reinterpret_cast<const uint32_t *>(codes + (e >> 1))), 0);
+    return __ldg(reinterpret_cast<const uint2 *>(codes + e));
+}
+
+__device__ __forceinline__ uint4 to_bf16(uint2 w, int fmt)
+{
+    return fmt == SIGE_Q_S8 ? codes8<SIGE_Q_S8>(w) : fmt == SIGE_Q_E4M3 ? codes8<SIGE_Q_E4M3>(w) : codes8<SIGE_Q_S4>(w);
+}
+
+__device__ __forceinline__ void sts_f1(uint32_t addr, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory"); }
+__device__ __forceinline__ void sts_f4(uint32_t addr, const float *v)
+{
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+}
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory"); }
+
+// A unit and the chunks of it that one CTA takes.
+struct Unit {
+    int qb, head, n, keys, c_lo, c_hi;
+};
+
+struct Work {
+    int qblocks, slots, units, split, per, u_first, u_step, rank_split, base;
+};
+
+__device__ __forceinline__ Unit unit_at(const AttnQParams &p, const Work &w, int u)
+{
+    Unit x;
+    x.qb = u % w.qblocks;
+    const int rest = u / w.qblocks;
+    x.head = rest % p.heads;
+    x.n = rest / p.heads;
+    x.keys = key_count(p, x.n);
+    const int nch = (x.keys + kKeys - 1) / kKeys;
+    x.c_lo = (int)((int64_t)w.rank_split * nch / w.split);
+    x.c_hi = (int)((int64_t)(w.rank_split + 1) * nch / w.split);
+    return x;
+}
+
+} // namespace at
+
+using namespace at;
+
+template <int KD>
+__global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid_constant__ at::Args args)
+{
+    using L = Lay<KD>;
+    extern __shared__ __align__(1024) uint8_t at_raw[];
+    const AttnQParams &p = args.a;
+    const uint32_t raw = smem_u32(at_raw);
+    const uint32_t sb = (raw + 1023u) & ~1023u;
+    uint8_t *smem = at_raw + (sb - raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t bar = sb + L::kOffBar;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kOffBar + kAbort);
+    WsHeader *hdr = p.hdr;
+
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(bar + kTmemSlot),
+                     "r"(kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    pdl_wait();
+    Work w;
+    w.slots = query_slots(p);
+    w.qblocks = (w.slots + kRows - 1) / kRows;
+    w.units = w.qblocks * p.N * p.heads;
+    {
+        // the key split: the same on every CTA (it depends on the list's
+        // length and the cache's keys); a split unit is its CTAs' only one
+        const int nch = (p.keys + kKeys - 1) / kKeys;
+        w.split = kCluster;
+        while (w.split > 1 && ((int64_t)w.units * w.split > (int64_t)gridDim.x || nch < 4 * w.split))
+            w.split >>= 1;
+        w.per = kCluster / w.split;
+        const int rank = (int)cluster_rank(), sub = rank / w.split;
+        w.rank_split = rank - sub * w.split;
+        w.base = sub * w.split;
+        w.u_first = (int)(blockIdx.x / kCluster) * w.per + sub;
+        w.u_step = (int)(gridDim.x / kCluster) * w.per;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kMaxStages; ++i) {
+            mbar_init(bar + kBarKvFull + 8u * i, kStage);
+            mbar_init(bar + kBarKvEmpty + 8u * i, 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar + kBarSFull + 8u * i, 1);
+            mbar_init(bar + kBarPFull + 8u * i, kGroup);
+        }
+        mbar_init(bar + kBarPvDone, 1);
+        mbar_init(bar + kBarPvDone + 8u, 1);
+        mbar_init(bar + kBarQFull, kStage);
+        mbar_init(bar + kBarQEmpty, 1);
+        mbar_init(bar + kBarReady, (uint32_t)(kSoft * w.split));
+        // 2 s parts of each of the CTA's 128 / s rows
+        mbar_init(bar + kBarPush, (uint32_t)kSoft);
+        mbar_init(bar + kBarDrain, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kOffBar + kTmemSlot);
+    cluster_arrive();   // the peers' barriers are initialised before the first remote arrival
+    bool joined = false;
+
+    if (warp >= 9) {
+        // ---- staging
+        const int t = (int)threadIdx.x - (kSoft + 32);
+        const int nkv = args.dhp >> 3, nvv = p.dvh >> 3;   // 8-channel vectors of a key (padded to 16 channels), of a value
+        const int nk = p.dh >> 3;
+        const int kdj = kStage / nkv, kdv = kStage - kdj * nkv, vdj = kStage / nvv, vdv = kStage - vdj * nvv;
+        const int kj0 = (int)udiv((uint32_t)t, args.dkv), kv0 = t - kj0 * nkv;
+        const int vj0 = (int)udiv((uint32_t)t, args.dvv), vv0 = t - vj0 * nvv;
+        constexpr int kPer = (kKeys * KD / 8 + kStage - 1) / kStage;   // vectors of K, and of V, a thread
+        uint2 kr[kPer], vr[kPer];
+        float sr[2];
+        // the codes and scales of chunk c of unit x
+        auto fetch = [&](const Unit &x, int c) {
+            const int k0 = c * kKeys, nkeys = x.keys - k0;
+            const int64_t row0 = (int64_t)x.n * p.keys + k0;
+            int j = kj0, v = kv0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                kr[i] = make_uint2(0, 0);
+                if (j < kKeys && j < nkeys && v < nk)
+                    kr[i] = load_codes8(p.kc, (row0 + j) * p.D + x.head * p.dh + 8 * v, p.kfmt);
+                j += kdj;
+                v += kdv;
+                if (v >= nkv) {
+                    v -= nkv;
+                    ++j;
+                }
+            }
+            j = vj0;
+            v = vv0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                vr[i] = make_uint2(0, 0);
+                if (j < kKeys && j < nkeys)
+                    vr[i] = load_codes8(p.vc, (row0 + j) * p.Dv + x.head * p.dvh + 8 * v, p.vfmt);
+                j += vdj;
+                v += vdv;
+                if (v >= nvv) {
+                    v -= nvv;
+                    ++j;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int e = t + i * kStage, key = e & (kKeys - 1);
+                sr[i] = 0.0f;
+                if (e < 2 * kKeys && key < nkeys)
+                    sr[i] = e < kKeys ? __ldg(p.ks + (row0 + key) * p.kng + x.head * p.dh / p.kgroup) * args.sc
+                                      : __ldg(p.vs + (row0 + key) * p.vng + x.head * p.dvh / p.vgroup);
+            }
+        };
+        // swizzled place of vector v of row j: block v / 8, 16 bytes at v ^ j
+        auto place = [](uint32_t base, uint32_t atom, int j, int v) {
+            return base + (uint32_t)(v >> 3) * atom + (uint32_t)j * 128u + (uint32_t)(((v & 7) ^ (j & 7)) << 4);
+        };
+        int it = 0, st = 0, nu = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        for (int u = w.u_first; ok && u < w.units; u += w.u_step) {
+            const Unit x = unit_at(p, w, u);
+            if (x.c_lo >= x.c_hi)
+                continue;
+            fetch(x, x.c_lo);
+            // the unit's queries: rows t and t + 96, zeros for padding slots and channels
+            if (nu > 0 && !mbar_wait_w(bar + kBarQEmpty, (nu - 1) & 1, abort_flag, hdr, kSiteQEmpty))
+                break;
+            for (int row = t; row < kRows; row += kStage) {
+                const int slot = x.qb * kRows + row;
+                const int64_t pix = slot < w.slots ? query_pixel(p, x.n, slot) : -1;
+#pragma unroll 1
+                for (int g0 = 0; g0 < nkv; g0 += 8) {
+                    uint4 q[8];
+#pragma unroll
+                    for (int g = 0; g < 8; ++g) {
+                        q[g] = make_uint4(0, 0, 0, 0);
+                        if (pix >= 0 && g0 + g < nk)
+                            q[g] = ld_nc16(p.q + pix * p.D + x.head * p.dh + 8 * (g0 + g));
+                    }
+#pragma unroll
+                    for (int g = 0; g < 8; ++g)
+                        if (g0 + g < nkv)
+                            sts128(place(sb + L::kOffQ, L::kQAtom, row, g0 + g), q[g]);
+                }
+            }
+            fence_async_smem();
+            mbar_arrive(bar + kBarQFull);
+            ++nu;
+            for (int c = x.c_lo; c < x.c_hi; ++c, ++it) {
+                if (it >= L::kStages && !mbar_wait_w(bar + kBarKvEmpty + 8u * st, ph, abort_flag, hdr, kSiteKvEmpty)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t kb = sb + L::kOffK + (uint32_t)st * L::kKvStage, vb = kb + L::kAtoms * L::kKvAtom;
+                int j = kj0, v = kv0;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    if (j < kKeys)
+                        sts128(place(kb, L::kKvAtom, j, v), to_bf16(kr[i], p.kfmt));
+                    j += kdj;
+                    v += kdv;
+                    if (v >= nkv) {
+                        v -= nkv;
+                        ++j;
+                    }
+                }
+                j = vj0;
+                v = vv0;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    if (j < kKeys)
+                        sts128(place(vb, L::kKvAtom, j, v), to_bf16(vr[i], p.vfmt));
+                    j += vdj;
+                    v += vdv;
+                    if (v >= nvv) {
+                        v -= nvv;
+                        ++j;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (t + i * kStage < 2 * kKeys)
+                        sts_f1(sb + L::kOffSc + (uint32_t)st * 512u + (uint32_t)(t + i * kStage) * 4u, sr[i]);
+                if (c + 1 < x.c_hi)
+                    fetch(x, c + 1);
+                fence_async_smem();
+                mbar_arrive(bar + kBarKvFull + 8u * st);
+                if (++st == L::kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 8) {
+        // ---- products
+        const uint32_t id_s = idesc_bf16(kKeys);
+        const int dv0 = min(args.dvp, 64), dv1 = args.dvp - dv0;
+        const uint32_t id_o0 = idesc_bf16(dv0) | (1u << 16), id_o1 = idesc_bf16(dv1) | (1u << 16);   // B (V) MN-major
+        const int ks = args.dhp / 16;
+        int s_it = 0, pv_it = 0, nu = 0;      // chunks whose S / P V has been issued
+        int ns[2] = {0, 0}, np[2] = {0, 0};   // of each softmax group
+        bool ok = true;
+        for (int u = w.u_first; ok && u < w.units; u += w.u_step) {
+            const Unit x = unit_at(p, w, u);
+            const int n = x.c_hi - x.c_lo;
+            if (n <= 0)
+                continue;
+            if (!mbar_wait_w(bar + kBarQFull, nu & 1, abort_flag, hdr, kSiteQFull))
+                break;
+            ++nu;
+            auto issue_s = [&](int i) -> bool {
+                const int st = s_it % L::kStages, g = i & 1, b = ns[g] & 1;
+                if (!mbar_wait_w(bar + kBarKvFull + 8u * st, (s_it / L::kStages) & 1, abort_flag, hdr, kSiteKvFull))
+                    return false;
+                tc_fence_after();
+                const uint32_t kb = sb + L::kOffK + (uint32_t)st * L::kKvStage;
+                for (int kk = 0; kk < ks; ++kk)
+                    mma_ss_w(tmem + 128u * g + 64u * b, desc_sw128(sb + L::kOffQ + (kk >> 2) * L::kQAtom) + 2u * (kk & 3),
+                             desc_sw128(kb + (kk >> 2) * L::kKvAtom) + 2u * (kk & 3), id_s, kk > 0);
+                tc_commit_w(bar + kBarSFull + 16u * g + 8u * b);
+                ++ns[g];
+                ++s_it;
+                if (i + 1 == n)
+                    tc_commit_w(bar + kBarQEmpty);
+                return true;
+            };
+            constexpr int kAhead = L::kAhead;
+            for (int i = 0; ok && i < min(kAhead, n); ++i)
+                ok = issue_s(i);
+            for (int i = 0; ok && i < n; ++i) {
+                const int g = i & 1, b = np[g] & 1;
+                if (!mbar_wait_w(bar + kBarPFull + 16u * g + 8u * b, (np[g] >> 1) & 1, abort_flag, hdr, kSitePFull)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const int st = pv_it % L::kStages;
+                const uint32_t vb = sb + L::kOffK + (uint32_t)st * L::kKvStage + L::kAtoms * L::kKvAtom;
+                const uint32_t d = tmem + kTmemO + 128u * g, pa = tmem + 128u * g + 64u * b;
+                for (int kk = 0; kk < kKeys / 16; ++kk)
+                    mma_ts_w(d, pa + 8u * kk, desc_sw128(vb + kk * 2048), id_o0, i > 1 || kk > 0);
+                if (dv1 > 0)
+                    for (int kk = 0; kk < kKeys / 16; ++kk)
+                        mma_ts_w(d + 64u, pa + 8u * kk, desc_sw128(vb + L::kKvAtom + kk * 2048), id_o1, i > 1 || kk > 0);
+                tc_commit_w(bar + kBarPvDone + 8u * g);
+                tc_commit_w(bar + kBarKvEmpty + 8u * st);
+                ++np[g];
+                ++pv_it;
+                if (i + kAhead < n)
+                    ok = issue_s(i + kAhead);
+            }
+        }
+        if (!ok) {
+            // the products in flight finish before this CTA's memory is given up
+            tc_commit_w(bar + kBarDrain);
+            const long long t0 = clock64();
+            while (!mbar_try(bar + kBarDrain, 0) && clock64() - t0 < kWaitCycles / 64)
+                ;
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax: thread = query row r of group g
+        const int g = warp >> 2;
+        const int r = (warp & 3) * 32 + lane;
+        const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t t_s = t_row + 128u * g, t_o = t_row + kTmemO + 128u * g;
+        const int ng = p.dvh >> 3;             // 8-channel groups of an output row
+        int chunk = 0, m_it = 0;               // chunks of the CTA so far; of this group
+        bool ok = true;
+        for (int u = w.u_first; u < w.units; u += w.u_step) {
+            const Unit x = unit_at(p, w, u);
+            const int n = x.c_hi - x.c_lo;
+            float m_used = -INFINITY, l = 0.0f;
+            for (int i = g; ok && i < n; i += 2, ++m_it) {
+                const int b = m_it & 1;
+                // (the staged scales are seen through the stage's own barrier; its
+                // next phase waits for this chunk's P V)
+                const int ci = chunk + i;
+                if (!mbar_wait_w(bar + kBarKvFull + 8u * (ci % L::kStages), (ci / L::kStages) & 1, abort_flag, hdr, kSiteKvFull) ||
+                    !mbar_wait_w(bar + kBarSFull + 16u * g + 8u * b, (m_it >> 1) & 1, abort_flag, hdr, kSiteSFull)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sc = sb + L::kOffSc + (uint32_t)(ci % L::kStages) * 512u;
+                uint32_t sr[2][32];
+                ld32(t_s + 64u * b, sr[0]);
+                ld32(t_s + 64u * b + 32u, sr[1]);
+                float ksc[4];
+                ld_wait();
+                float sv[kKeys], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                const int kvalid = x.keys - (x.c_lo + i) * kKeys;
+#pragma unroll
+                for (int k = 0; k < kKeys; k += 4) {
+                    const float4 s4 = lds_f4(sc + 4u * k);
+                    ksc[0] = s4.x; ksc[1] = s4.y; ksc[2] = s4.z; ksc[3] = s4.w;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sv[k + e] = __uint_as_float(sr[(k + e) >> 5][(k + e) & 31]) * ksc[e];
+                }
+                if (kvalid < kKeys) {
+#pragma unroll
+                    for (int k = 0; k < kKeys; ++k)
+                        if (k >= kvalid)
+                            sv[k] = -INFINITY;
+                }
+#pragma unroll
+                for (int k = 0; k < kKeys; ++k)
+                    mx[k & 3] = fmaxf(mx[k & 3], sv[k]);
+                const float t_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                // the exponent base moves only when the maximum has grown by
+                // more than 8 (weights <= 2^8 otherwise)
+                const bool grow = t_max > m_used + 8.0f;
+                const float m_new = grow ? t_max : m_used;
+                const float corr = ex2(m_used - m_new);   // 0 on the group's first chunk, 1 when kept
+                float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                uint32_t pk[32];
+#pragma unroll
+                for (int k = 0; k < kKeys; k += 4) {
+                    const float4 v4 = lds_f4(sc + 256u + 4u * k);
+                    float e[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        e[q] = ex2(sv[k + q] - m_new);
+                        ls[q] += e[q];
+                    }
+                    pk[k >> 1] = pack_bf16x2(e[0] * v4.x, e[1] * v4.y);
+                    pk[(k >> 1) + 1] = pack_bf16x2(e[2] * v4.z, e[3] * v4.w);
+                }
+                st32(t_s + 64u * b, pk);   // over the scores just read
+                l = l * corr + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
+                if (i > 1 && __any_sync(0xFFFFFFFFu, grow)) {
+                    // rescale this warp's O rows once the group's previous P V has landed
+                    if (!mbar_wait_w(bar + kBarPvDone + 8u * g, (m_it - 1) & 1, abort_flag, hdr, kSitePvDone)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int pc = 0; pc < KD / 16; ++pc) {
+                        if (pc * 16 < args.dvp) {
+                            float v[16];
+                            tmem_ld16(t_o + 16u * pc, v);
+#pragma unroll
+                            for (int q = 0; q < 16; ++q)
+                                v[q] *= corr;
+                            st16(t_o + 16u * pc, v);
+                        }
+                    }
+                }
+                st_wait();
+                tc_fence_before();
+                mbar_arrive(bar + kBarPFull + 16u * g + 8u * b);
+                m_used = m_new;
+            }
+            chunk += max(0, n);
+            // the group's last P V of the unit has landed.  (Its scores may have
+            // been issued before the one before it: a wait for a phase must not
+            // meet the barrier two phases back, so that one is waited for first;
+            // all earlier ones were issued before the last scores.)
+            const bool mine = n > g;
+            if (ok && n > g + 2)
+                ok = mbar_wait_w(bar + kBarPvDone + 8u * g, m_it & 1, abort_flag, hdr, kSitePvDone);
+            if (ok && mine)
+                ok = mbar_wait_w(bar + kBarPvDone + 8u * g, (m_it - 1) & 1, abort_flag, hdr, kSitePvDone);
+            tc_fence_after();
+            if (w.split == 1) {
+                // ---- merge of the two groups: each thread finishes the 8-channel
+                // groups of its parity of its row, from the other's copy of them
+                soft_sync();   // the previous unit's rows have been read
+                float o[KD / 2];   // this thread's own groups
+                if (ok) {
+#pragma unroll
+                    for (int pc = 0; pc < KD / 16; ++pc) {
+                        if (pc * 16 < args.dvp) {
+                            float v[16];
+                            if (mine)
+                                tmem_ld16(t_o + 16u * pc, v);
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                const float a = mine ? v[q] : 0.0f, c = mine ? v[8 + q] : 0.0f;
+                                o[8 * pc + q] = g == 0 ? a : c;   // even groups stay with group 0
+                                v[q] = g == 0 ? c : a;
+                            }
+                            const uint32_t dst = sb + L::kOffX + (uint32_t)((g * (KD / 16) + pc) * 2 * kRows + r) * 16u;
+                            sts_f4(dst, v);
+                            sts_f4(dst + kRows * 16u, v + 4);
+                        }
+                    }
+                    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sb + L::kOffMl + (uint32_t)(g * kRows + r) * 8u),
+                                 "f"(m_used), "f"(l) : "memory");
+                    tc_fence_before();
+                }
+                soft_sync();
+                const int slot = x.qb * kRows + r;
+                const int64_t pix = slot < w.slots ? query_pixel(p, x.n, slot) : -1;
+                if (ok && pix >= 0) {
+                    const float2 ml = lds_f2(sb + L::kOffMl + (uint32_t)((1 - g) * kRows + r) * 8u);
+                    const float mm = fmaxf(m_used, ml.x);
+                    // a group without a chunk has weight 0 (and no key at all leaves zeros)
+                    const float wa = mine ? ex2(m_used - mm) : 0.0f, wb = n > 1 - g ? ex2(ml.x - mm) : 0.0f;
+                    const float inv = n > 0 ? 1.0f / (l * wa + ml.y * wb) : 0.0f;
+#pragma unroll
+                    for (int pc = 0; pc < KD / 16; ++pc) {
+                        const int gi = 2 * pc + g;
+                        if (gi < ng) {
+                            const uint32_t src = sb + L::kOffX + (uint32_t)(((1 - g) * (KD / 16) + pc) * 2 * kRows + r) * 16u;
+                            const float4 y0 = lds_f4(src), y1 = lds_f4(src + kRows * 16u);
+                            float *oo = o + 8 * pc;
+                            oo[0] = fmaf(y0.x, wb, oo[0] * wa); oo[1] = fmaf(y0.y, wb, oo[1] * wa);
+                            oo[2] = fmaf(y0.z, wb, oo[2] * wa); oo[3] = fmaf(y0.w, wb, oo[3] * wa);
+                            oo[4] = fmaf(y1.x, wb, oo[4] * wa); oo[5] = fmaf(y1.y, wb, oo[5] * wa);
+                            oo[6] = fmaf(y1.z, wb, oo[6] * wa); oo[7] = fmaf(y1.w, wb, oo[7] * wa);
+                            store8(p.o + pix * p.Dv + x.head * p.dvh + 8 * gi, oo, inv);
+                        }
+                    }
+                }
+                continue;
+            }
+            // ---- merge of a split unit's 2 s partial rows: each is pushed to the
+            // CTA that owns the row, over the memory of the ring, once every CTA
+            // of the unit has finished its products
+            const int s = w.split, rows = kRows / s;
+            if (!joined) {
+                cluster_wait();
+                joined = true;
+            }
+            tc_fence_before();
+            for (int i = 0; i < s; ++i)
+                mbar_arrive_peer(map_peer(bar + kBarReady, (uint32_t)(w.base + i)));
+            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar + kBarReady, 0, abort_flag, hdr, kSiteReady));
+            if (!ok)
+                continue;
+            {
+                const int owner = r / rows;
+                const uint32_t slot = (uint32_t)((w.rank_split * 2 + g) * rows + (r - owner * rows));   // of 256
+                const uint32_t dst = map_peer(sb + L::kOffPush + slot * 16u, (uint32_t)(w.base + owner));
+#pragma unroll
+                for (int pc = 0; pc < KD / 16; ++pc) {
+                    if (pc * 16 < args.dvp) {
+                        float v[16];
+                        if (mine)
+                            tmem_ld16(t_o + 16u * pc, v);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            st_peer_f32x4(dst + (uint32_t)(4 * pc + q) * 4096u, mine ? v[4 * q] : 0.0f, mine ? v[4 * q + 1] : 0.0f,
+                                          mine ? v[4 * q + 2] : 0.0f, mine ? v[4 * q + 3] : 0.0f);
+                    }
+                }
+                st_peer_f32x2(map_peer(sb + L::kOffMl + slot * 8u, (uint32_t)(w.base + owner)), m_used, mine ? l : -1.0f);
+                mbar_arrive_peer(map_peer(bar + kBarPush, (uint32_t)(w.base + owner)));   // releases the pushes
+            }
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar + kBarPush, 0, abort_flag, hdr, kSitePush))) {
+                ok = false;
+                continue;
+            }
+            for (int item = (int)threadIdx.x; item < rows * ng; item += kSoft) {
+                const int j = item % rows, gi = item / rows;
+                const int slot = x.qb * kRows + w.rank_split * rows + j;
+                const int64_t pix = slot < w.slots ? query_pixel(p, x.n, slot) : -1;
+                if (pix < 0)
+                    continue;
+                float mm = -INFINITY;
+                for (int i = 0; i < 2 * s; ++i)
+                    mm = fmaxf(mm, lds_f2(sb + L::kOffMl + (uint32_t)(i * rows + j) * 8u).x);
+                float sum = 0.0f, acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                for (int i = 0; i < 2 * s; ++i) {
+                    const float2 ml = lds_f2(sb + L::kOffMl + (uint32_t)(i * rows + j) * 8u);
+                    if (ml.y == -1.0f)   // a part without a chunk
+                        continue;
+                    const float wt = ex2(ml.x - mm);
+                    sum = fmaf(ml.y, wt, sum);
+                    const uint32_t src = sb + L::kOffPush + (uint32_t)(i * rows + j) * 16u + (uint32_t)(2 * gi) * 4096u;
+                    const float4 y0 = lds_f4(src), y1 = lds_f4(src + 4096u);
+                    acc[0] = fmaf(wt, y0.x, acc[0]); acc[1] = fmaf(wt, y0.y, acc[1]);
+                    acc[2] = fmaf(wt, y0.z, acc[2]); acc[3] = fmaf(wt, y0.w, acc[3]);
+                    acc[4] = fmaf(wt, y1.x, acc[4]); acc[5] = fmaf(wt, y1.y, acc[5]);
+                    acc[6] = fmaf(wt, y1.z, acc[6]); acc[7] = fmaf(wt, y1.w, acc[7]);
+                }
+                store8(p.o + pix * p.Dv + x.head * p.dvh + 8 * gi, acc, x.keys > 0 ? 1.0f / sum : 0.0f);
+            }
+        }
+    }
+    if (!joined)
+        cluster_wait();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+    }
+    // no CTA leaves while a peer may still address its shared memory
+    cluster_arrive();
+    cluster_wait();
+}
+
+// ------------------------------------------------------------------ host
+
+bool attention_qcache_tc_scope(int dh, int dvh)
+{
+    return dh > 0 && dvh > 0 && dh % 8 == 0 && dvh % 8 == 0 && dh <= 128 && dvh <= 128;
+}
+
+template <int KD>
+static int launch_kd(const at::Args &a, int64_t units_max, cudaStream_t stream)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return SIGE_ERR_CUDA;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = at::kCluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(at::kThreads);
+    cfg.dynamicSmemBytes = at::Lay<KD>::kBytes;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    static std::atomic<int> clusters_of[64];   // co-resident clusters, per device
+    int ncl = clusters_of[dev].load(std::memory_order_acquire);
+    if (ncl == 0) {
+        if (cudaFuncSetAttribute(k_attn_qcache_tc<KD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)at::Lay<KD>::kBytes) != cudaSuccess) {
+            cudaGetLastError();
+            return SIGE_ERR_CUDA;
+        }
+        cfg.gridDim = dim3(at::kCluster * (device_sm_count() / at::kCluster));
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&ncl, k_attn_qcache_tc<KD>, &cfg) != cudaSuccess || ncl < 1) {
+            cudaGetLastError();
+            return SIGE_ERR_CUDA;
+        }
+        clusters_of[dev].store(ncl, std::memory_order_release);
+    }
+    prefer_max_shared(k_attn_qcache_tc<KD>);
+    cfg.numAttrs = 2;
+    // every unit a launch can have needs at most one cluster
+    cfg.gridDim = dim3((unsigned)(at::kCluster * std::max<int64_t>(1, std::min<int64_t>(ncl, units_max))));
+    if (cudaLaunchKernelEx(&cfg, k_attn_qcache_tc<KD>, a) != cudaSuccess) {
+        cudaGetLastError();
+        return SIGE_ERR_CUDA;
+    }
+    count_launch();
+    return launch_check();
+}
+
+int launch_attention_qcache_tc(const AttnQParams &p, cudaStream_t stream)
+{
+    if (!attention_qcache_tc_scope(p.dh, p.dvh))
+        return 1;
+    // 16-byte query and output vectors, 8 codes at once
+    if (!aligned_to(p.q, 16) || !aligned_to(p.o, 16) || !aligned_to(p.kc, p.kfmt == SIGE_Q_S4 ? 4 : 8) ||
+        !aligned_to(p.vc, p.vfmt == SIGE_Q_S4 ? 4 : 8))
+        return 1;
+    const int64_t units_max = (p.slots + at::kRows - 1) / at::kRows * p.N * p.heads;
+    if (units_max > INT32_MAX / 16)
+        return 1;
+    at::Args a{};
+    a.a = p;
+    a.dhp = (p.dh + 15) / 16 * 16;
+    a.dvp = (p.dvh + 15) / 16 * 16;
+    a.sc = (float)(1.4426950408889634 / std::sqrt((double)p.dh));
+    a.dkv = udiv_make((uint32_t)(a.dhp / 8));
+    a.dvv = udiv_make((uint32_t)(p.dvh / 8));
+    return a.dhp <= 64 && a.dvp <= 64 ? launch_kd<64>(a, units_max, stream) : launch_kd<128>(a, units_max, stream);
+}
+
+} // namespace sige
