@@ -27,6 +27,7 @@
 #include <algorithm>
 #include <atomic>
 #include <math.h>
+#include <type_traits>
 
 #include "attention_qcache.cuh"
 #include "attn_ptx.cuh"
@@ -137,18 +138,109 @@ __device__ __forceinline__ uint4 codes8(uint2 w)
     }
 }
 
-__device__ __forceinline__ uint2 load_codes8(const uint8_t *codes, int64_t e, int fmt)
+// Swizzled place of 8-channel vector v of row j: block v / 8, 16 bytes at v ^ j.
+__device__ __forceinline__ uint32_t place(uint32_t atom, int j, int v)
 {
-    if (fmt == SIGE_Q_S4)
-        return make_uint2(__ldg(reinterpret_cast<const uint32_t *>(codes + (e >> 1))), 0);
-    return __ldg(reinterpret_cast<const uint2 *>(codes + e));
+    return (uint32_t)(v >> 3) * atom + (uint32_t)j * 128u + (uint32_t)(((v & 7) ^ (j & 7)) << 4);
 }
 
-__device__ __forceinline__ uint4 to_bf16(uint2 w, int fmt)
-{
-    return fmt == SIGE_Q_S8 ? codes8<SIGE_Q_S8>(w) : fmt == SIGE_Q_E4M3 ? codes8<SIGE_Q_E4M3>(w) : codes8<SIGE_Q_S4>(w);
-}
+// One staging thread's share of a chunk of K or V: up to N vectors of 8 codes,
+// vector i being (key j, vector v) number t + 96 i of the chunk, v fastest.
+// Where they lie in the chunk and in shared memory is worked out once; kSets
+// register sets hold the codes on their way.
+template <int N, int kSets>
+struct Stager {
+    uint32_t src[N];      // byte offset from the chunk's first key
+    uint32_t to[N];       // offset in the staged rows | key << 16 (kKeys: no such vector, kZero: zeros for padded channels)
+    uint2 raw[kSets][N];
+    static constexpr uint32_t kZero = 0x7FFF;
+    const uint8_t *at;    // the next chunk to fetch
+    uint32_t step;        // bytes of a chunk's keys
+    int fmt;
 
+    __device__ __forceinline__ void init(int t, int nv, UDiv dnv, int real, int ch, int format, uint32_t atom)
+    {
+        fmt = format;
+        const int sh = format == SIGE_Q_S4 ? 1 : 0;
+        step = ((uint32_t)kKeys * (uint32_t)ch) >> sh;
+        const int dj = (int)udiv(kStage, dnv), dv = kStage - dj * nv;
+        int j = (int)udiv((uint32_t)t, dnv), v = t - j * nv;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            src[i] = ((uint32_t)j * (uint32_t)ch + 8u * (uint32_t)v) >> sh;
+            to[i] = j >= kKeys ? (uint32_t)kKeys << 16 : place(atom, j, v) | ((v < real ? (uint32_t)j : kZero) << 16);
+            j += dj;
+            v += dv;
+            if (v >= nv) {
+                v -= nv;
+                ++j;
+            }
+        }
+    }
+    __device__ __forceinline__ void start(const uint8_t *codes, int64_t e) { at = codes + (fmt == SIGE_Q_S4 ? e >> 1 : e); }
+
+    // the next chunk, of which `nkeys` keys exist (zeros for the others)
+    template <int S>
+    __device__ __forceinline__ void fetch(int nkeys)
+    {
+        const uint32_t lim = (uint32_t)min(nkeys, kKeys) << 16;
+        if (fmt == SIGE_Q_S4) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                raw[S][i] = make_uint2(to[i] < lim ? __ldg(reinterpret_cast<const uint32_t *>(at + src[i])) : 0u, 0u);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                raw[S][i] = make_uint2(0, 0);
+                if (to[i] < lim)
+                    raw[S][i] = __ldg(reinterpret_cast<const uint2 *>(at + src[i]));
+            }
+        }
+        at += step;
+    }
+
+    template <int S, int kFmt>
+    __device__ __forceinline__ void store_as(uint32_t base)
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (to[i] >> 16 != kKeys)
+                sts128(base + (to[i] & 0xFFFFu), codes8<kFmt>(raw[S][i]));
+    }
+    template <int S>
+    __device__ __forceinline__ void store(uint32_t base)
+    {
+        if (fmt == SIGE_Q_S8)
+            store_as<S, SIGE_Q_S8>(base);
+        else if (fmt == SIGE_Q_E4M3)
+            store_as<S, SIGE_Q_E4M3>(base);
+        else
+            store_as<S, SIGE_Q_S4>(base);
+    }
+};
+
+// Pairs of float32.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; }
+__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ ulonglong2 lds_2x2(uint32_t addr)
+{
+    ulonglong2 v;
+    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ void sts_f1(uint32_t addr, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory"); }
 __device__ __forceinline__ void sts_f4(uint32_t addr, const float *v)
 {
@@ -251,66 +343,43 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
     if (warp >= 9) {
         // ---- staging
         const int t = (int)threadIdx.x - (kSoft + 32);
-        const int nkv = args.dhp >> 3, nvv = p.dvh >> 3;   // 8-channel vectors of a key (padded to 16 channels), of a value
-        const int nk = p.dh >> 3;
-        const int kdj = kStage / nkv, kdv = kStage - kdj * nkv, vdj = kStage / nvv, vdv = kStage - vdj * nvv;
-        const int kj0 = (int)udiv((uint32_t)t, args.dkv), kv0 = t - kj0 * nkv;
-        const int vj0 = (int)udiv((uint32_t)t, args.dvv), vv0 = t - vj0 * nvv;
+        const int nk = p.dh >> 3, nkv = args.dhp >> 3;   // 8-channel vectors of a query row; padded to 16 channels
         constexpr int kPer = (kKeys * KD / 8 + kStage - 1) / kStage;   // vectors of K, and of V, a thread
-        uint2 kr[kPer], vr[kPer];
-        float sr[2];
-        // the codes and scales of chunk c of unit x
-        auto fetch = [&](const Unit &x, int c) {
-            const int k0 = c * kKeys, nkeys = x.keys - k0;
-            const int64_t row0 = (int64_t)x.n * p.keys + k0;
-            int j = kj0, v = kv0;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                kr[i] = make_uint2(0, 0);
-                if (j < kKeys && j < nkeys && v < nk)
-                    kr[i] = load_codes8(p.kc, (row0 + j) * p.D + x.head * p.dh + 8 * v, p.kfmt);
-                j += kdj;
-                v += kdv;
-                if (v >= nkv) {
-                    v -= nkv;
-                    ++j;
-                }
-            }
-            j = vj0;
-            v = vv0;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                vr[i] = make_uint2(0, 0);
-                if (j < kKeys && j < nkeys)
-                    vr[i] = load_codes8(p.vc, (row0 + j) * p.Dv + x.head * p.dvh + 8 * v, p.vfmt);
-                j += vdj;
-                v += vdv;
-                if (v >= nvv) {
-                    v -= nvv;
-                    ++j;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int e = t + i * kStage, key = e & (kKeys - 1);
-                sr[i] = 0.0f;
-                if (e < 2 * kKeys && key < nkeys)
-                    sr[i] = e < kKeys ? __ldg(p.ks + (row0 + key) * p.kng + x.head * p.dh / p.kgroup) * args.sc
-                                      : __ldg(p.vs + (row0 + key) * p.vng + x.head * p.dvh / p.vgroup);
-            }
-        };
-        // swizzled place of vector v of row j: block v / 8, 16 bytes at v ^ j
-        auto place = [](uint32_t base, uint32_t atom, int j, int v) {
-            return base + (uint32_t)(v >> 3) * atom + (uint32_t)j * 128u + (uint32_t)(((v & 7) ^ (j & 7)) << 4);
-        };
+        constexpr int kSets = KD == 64 ? 2 : 1;   // chunks on their way while one is converted (the registers' limit)
+        Stager<kPer, kSets> K, V;
+        K.init(t, nkv, args.dkv, nk, p.D, p.kfmt, L::kKvAtom);
+        V.init(t, p.dvh >> 3, args.dvv, p.dvh >> 3, p.Dv, p.vfmt, L::kKvAtom);
         int it = 0, st = 0, nu = 0;
         uint32_t ph = 1;
         bool ok = true;
         for (int u = w.u_first; ok && u < w.units; u += w.u_step) {
             const Unit x = unit_at(p, w, u);
-            if (x.c_lo >= x.c_hi)
+            const int n = x.c_hi - x.c_lo;
+            if (n <= 0)
                 continue;
-            fetch(x, x.c_lo);
+            const int64_t row0 = (int64_t)x.n * p.keys + (int64_t)x.c_lo * kKeys;   // the first chunk's first key
+            K.start(p.kc, row0 * p.D + x.head * p.dh);
+            V.start(p.vc, row0 * p.Dv + x.head * p.dvh);
+            const float *ks = p.ks + row0 * p.kng + x.head * p.dh / p.kgroup;
+            const float *vs = p.vs + row0 * p.vng + x.head * p.dvh / p.vgroup;
+            const int left = x.keys - x.c_lo * kKeys;   // keys from the first chunk on
+            float sr[kSets][2];
+            auto fetch = [&](int i, auto set) {
+                constexpr int s = decltype(set)::value;
+                const int nkeys = left - i * kKeys;
+                K.template fetch<s>(nkeys);
+                V.template fetch<s>(nkeys);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int k = t + e * kStage, key = k & (kKeys - 1), row = i * kKeys + key;
+                    sr[s][e] = 0.0f;
+                    if (k < 2 * kKeys && key < nkeys)
+                        sr[s][e] = k < kKeys ? __ldg(ks + (int64_t)row * p.kng) * args.sc : __ldg(vs + (int64_t)row * p.vng);
+                }
+            };
+            fetch(0, std::integral_constant<int, 0>());
+            if (kSets > 1 && n > 1)
+                fetch(1, std::integral_constant<int, kSets - 1>());
             // the unit's queries: rows t and t + 96, zeros for padding slots and channels
             if (nu > 0 && !mbar_wait_w(bar + kBarQEmpty, (nu - 1) & 1, abort_flag, hdr, kSiteQEmpty))
                 break;
@@ -329,55 +398,38 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
 #pragma unroll
                     for (int g = 0; g < 8; ++g)
                         if (g0 + g < nkv)
-                            sts128(place(sb + L::kOffQ, L::kQAtom, row, g0 + g), q[g]);
+                            sts128(sb + L::kOffQ + place(L::kQAtom, row, g0 + g), q[g]);
                 }
             }
             fence_async_smem();
             mbar_arrive(bar + kBarQFull);
             ++nu;
-            for (int c = x.c_lo; c < x.c_hi; ++c, ++it) {
-                if (it >= L::kStages && !mbar_wait_w(bar + kBarKvEmpty + 8u * st, ph, abort_flag, hdr, kSiteKvEmpty)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t kb = sb + L::kOffK + (uint32_t)st * L::kKvStage, vb = kb + L::kAtoms * L::kKvAtom;
-                int j = kj0, v = kv0;
+            auto stage = [&](int i, auto set) -> bool {
+                constexpr int s = decltype(set)::value;
+                if (it >= L::kStages && !mbar_wait_w(bar + kBarKvEmpty + 8u * st, ph, abort_flag, hdr, kSiteKvEmpty))
+                    return false;
+                const uint32_t kb = sb + L::kOffK + (uint32_t)st * L::kKvStage;
+                K.template store<s>(kb);
+                V.template store<s>(kb + L::kAtoms * L::kKvAtom);
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    if (j < kKeys)
-                        sts128(place(kb, L::kKvAtom, j, v), to_bf16(kr[i], p.kfmt));
-                    j += kdj;
-                    v += kdv;
-                    if (v >= nkv) {
-                        v -= nkv;
-                        ++j;
-                    }
-                }
-                j = vj0;
-                v = vv0;
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    if (j < kKeys)
-                        sts128(place(vb, L::kKvAtom, j, v), to_bf16(vr[i], p.vfmt));
-                    j += vdj;
-                    v += vdv;
-                    if (v >= nvv) {
-                        v -= nvv;
-                        ++j;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (t + i * kStage < 2 * kKeys)
-                        sts_f1(sb + L::kOffSc + (uint32_t)st * 512u + (uint32_t)(t + i * kStage) * 4u, sr[i]);
-                if (c + 1 < x.c_hi)
-                    fetch(x, c + 1);
+                for (int e = 0; e < 2; ++e)
+                    if (t + e * kStage < 2 * kKeys)
+                        sts_f1(sb + L::kOffSc + (uint32_t)st * 512u + (uint32_t)(t + e * kStage) * 4u, sr[s][e]);
                 fence_async_smem();
                 mbar_arrive(bar + kBarKvFull + 8u * st);
+                if (i + kSets < n)
+                    fetch(i + kSets, set);
+                ++it;
                 if (++st == L::kStages) {
                     st = 0;
                     ph ^= 1;
                 }
+                return true;
+            };
+            for (int i = 0; ok && i < n; i += 2) {
+                ok = stage(i, std::integral_constant<int, 0>());
+                if (ok && i + 1 < n)
+                    ok = stage(i + 1, std::integral_constant<int, kSets - 1>());
             }
         }
         __syncwarp();
@@ -476,55 +528,62 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
                 uint32_t sr[2][32];
                 ld32(t_s + 64u * b, sr[0]);
                 ld32(t_s + 64u * b + 32u, sr[1]);
-                float ksc[4];
                 ld_wait();
-                float sv[kKeys], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                // scores in pairs (the packed float32 instructions: half as many)
+                uint64_t sv[kKeys / 2];
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                 const int kvalid = x.keys - (x.c_lo + i) * kKeys;
 #pragma unroll
                 for (int k = 0; k < kKeys; k += 4) {
-                    const float4 s4 = lds_f4(sc + 4u * k);
-                    ksc[0] = s4.x; ksc[1] = s4.y; ksc[2] = s4.z; ksc[3] = s4.w;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        sv[k + e] = __uint_as_float(sr[(k + e) >> 5][(k + e) & 31]) * ksc[e];
+                    const ulonglong2 s4 = lds_2x2(sc + 4u * k);
+                    sv[k / 2] = mul2(pair(sr[k >> 5][k & 31], sr[k >> 5][(k + 1) & 31]), s4.x);
+                    sv[k / 2 + 1] = mul2(pair(sr[k >> 5][(k + 2) & 31], sr[k >> 5][(k + 3) & 31]), s4.y);
                 }
                 if (kvalid < kKeys) {
 #pragma unroll
-                    for (int k = 0; k < kKeys; ++k)
+                    for (int k = 0; k < kKeys; k += 2) {
                         if (k >= kvalid)
-                            sv[k] = -INFINITY;
+                            sv[k / 2] = 0xFF800000FF800000ull;   // two -inf
+                        else if (k + 1 >= kvalid)
+                            sv[k / 2] = (sv[k / 2] & 0xFFFFFFFFull) | 0xFF80000000000000ull;
+                    }
                 }
 #pragma unroll
-                for (int k = 0; k < kKeys; ++k)
-                    mx[k & 3] = fmaxf(mx[k & 3], sv[k]);
+                for (int k = 0; k < kKeys / 2; ++k) {
+                    mx[(2 * k) & 3] = fmaxf(mx[(2 * k) & 3], lo_of(sv[k]));
+                    mx[(2 * k + 1) & 3] = fmaxf(mx[(2 * k + 1) & 3], hi_of(sv[k]));
+                }
                 const float t_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 // the exponent base moves only when the maximum has grown by
                 // more than 8 (weights <= 2^8 otherwise)
                 const bool grow = t_max > m_used + 8.0f;
                 const float m_new = grow ? t_max : m_used;
                 const float corr = ex2(m_used - m_new);   // 0 on the group's first chunk, 1 when kept
-                float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const uint64_t nm = pair(__float_as_uint(-m_new), __float_as_uint(-m_new));
+                uint64_t ls[2] = {0, 0};
                 uint32_t pk[32];
 #pragma unroll
                 for (int k = 0; k < kKeys; k += 4) {
-                    const float4 v4 = lds_f4(sc + 256u + 4u * k);
-                    float e[4];
+                    const ulonglong2 v4 = lds_2x2(sc + 256u + 4u * k);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        e[q] = ex2(sv[k + q] - m_new);
-                        ls[q] += e[q];
+                    for (int h = 0; h < 2; ++h) {
+                        const uint64_t d = add2(sv[k / 2 + h], nm);
+                        const uint64_t e = pair(__float_as_uint(ex2(lo_of(d))), __float_as_uint(ex2(hi_of(d))));
+                        ls[h] = add2(ls[h], e);
+                        const uint64_t q = mul2(e, h ? v4.y : v4.x);
+                        pk[k / 2 + h] = pack_bf16x2(lo_of(q), hi_of(q));
                     }
-                    pk[k >> 1] = pack_bf16x2(e[0] * v4.x, e[1] * v4.y);
-                    pk[(k >> 1) + 1] = pack_bf16x2(e[2] * v4.z, e[3] * v4.w);
                 }
                 st32(t_s + 64u * b, pk);   // over the scores just read
-                l = l * corr + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
+                l = l * corr + ((lo_of(ls[0]) + hi_of(ls[0])) + (lo_of(ls[1]) + hi_of(ls[1])));
+                // the group's previous P V has landed (each of its phases is waited
+                // for in turn: a parity tells two neighbouring phases apart, no more)
+                if (i > 1 && !mbar_wait_w(bar + kBarPvDone + 8u * g, (m_it - 1) & 1, abort_flag, hdr, kSitePvDone)) {
+                    ok = false;
+                    break;
+                }
                 if (i > 1 && __any_sync(0xFFFFFFFFu, grow)) {
-                    // rescale this warp's O rows once the group's previous P V has landed
-                    if (!mbar_wait_w(bar + kBarPvDone + 8u * g, (m_it - 1) & 1, abort_flag, hdr, kSitePvDone)) {
-                        ok = false;
-                        break;
-                    }
+                    // rescale this warp's O rows
                     tc_fence_after();
 #pragma unroll
                     for (int pc = 0; pc < KD / 16; ++pc) {
@@ -544,13 +603,8 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
                 m_used = m_new;
             }
             chunk += max(0, n);
-            // the group's last P V of the unit has landed.  (Its scores may have
-            // been issued before the one before it: a wait for a phase must not
-            // meet the barrier two phases back, so that one is waited for first;
-            // all earlier ones were issued before the last scores.)
+            // the group's last P V of the unit has landed
             const bool mine = n > g;
-            if (ok && n > g + 2)
-                ok = mbar_wait_w(bar + kBarPvDone + 8u * g, m_it & 1, abort_flag, hdr, kSitePvDone);
             if (ok && mine)
                 ok = mbar_wait_w(bar + kBarPvDone + 8u * g, (m_it - 1) & 1, abort_flag, hdr, kSitePvDone);
             tc_fence_after();
@@ -746,7 +800,8 @@ int launch_attention_qcache_tc(const AttnQParams &p, cudaStream_t stream)
         !aligned_to(p.vc, p.vfmt == SIGE_Q_S4 ? 4 : 8))
         return 1;
     const int64_t units_max = (p.slots + at::kRows - 1) / at::kRows * p.N * p.heads;
-    if (units_max > INT32_MAX / 16)
+    // (units and the bytes of a chunk's rows are counted in 32 bits)
+    if (units_max > INT32_MAX / 16 || p.D > (1 << 24) || p.Dv > (1 << 24))
         return 1;
     at::Args a{};
     a.a = p;
