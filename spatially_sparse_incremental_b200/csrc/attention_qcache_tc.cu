@@ -7,8 +7,8 @@
 // scale); the only rounding of an operand is that of weight * scale to bf16.
 //
 // Work unit: 128 query slots of one (batch item, head), the keys in chunks of
-// 64.  Roles of a CTA's 12 warps:
-//   * warps 9 .. 11 stage the operands: the unit's queries once, and for each
+// 64.  Roles of a CTA's 16 warps:
+//   * warps 9 .. 15 stage the operands: the unit's queries once, and for each
 //     chunk the codes (global loads of 8 codes a lane, one chunk ahead), turned
 //     into bf16 rows of 128 bytes with the 128-byte swizzle (K-major for the
 //     first product, MN-major for the second), and the chunk's scales;
@@ -41,7 +41,11 @@ constexpr int kRows = 128;
 constexpr int kKeys = 64;           // keys of a chunk
 constexpr int kGroup = 128;         // threads of a softmax group
 constexpr int kSoft = 2 * kGroup;
-constexpr int kStage = 96;          // staging threads (12 warps: 3 to a scheduler, 168 registers a thread)
+constexpr int kStage = 224;         // staging threads
+// Registers: 512 threads are launched with 128 each; the softmax groups take
+// 152, the warpgroup of the MMA warp and the other staging one 104 (2 x 152 +
+// 2 x 104 = 4 x 128).
+constexpr int kSoftRegs = 152, kStageRegs = 104;
 constexpr int kThreads = kSoft + 32 + kStage;
 constexpr int kCluster = 4;
 constexpr int kMaxStages = 6;
@@ -145,7 +149,7 @@ __device__ __forceinline__ uint32_t place(uint32_t atom, int j, int v)
 }
 
 // One staging thread's share of a chunk of K or V: up to N vectors of 8 codes,
-// vector i being (key j, vector v) number t + 96 i of the chunk, v fastest.
+// vector i being (key j, vector v) number t + kStage i of the chunk, v fastest.
 // Where they lie in the chunk and in shared memory is worked out once; kSets
 // register sets hold the codes on their way.
 template <int N, int kSets>
@@ -248,6 +252,31 @@ __device__ __forceinline__ void sts_f4(uint32_t addr, const float *v)
 }
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory"); }
 
+// Bounded waits by every lane of a warp, inline (a call would keep the
+// compiler from splitting the registers between the roles): false, in all
+// lanes, when the limit expired or another role gave up.
+template <bool kPeer>
+__device__ __forceinline__ bool wait_w(uint32_t b, uint32_t parity, volatile int *abort_flag, WsHeader *hdr, int where)
+{
+    bool ok = kPeer ? mbar_try_cluster(b, parity) : mbar_try(b, parity);
+    if (__all_sync(0xFFFFFFFFu, ok))
+        return true;
+    const long long t0 = clock64();
+    while (!__all_sync(0xFFFFFFFFu, ok)) {
+        if (!ok)
+            ok = kPeer ? mbar_try_cluster(b, parity) : mbar_try(b, parity);
+        const bool late = clock64() - t0 > kWaitCycles;
+        if (__any_sync(0xFFFFFFFFu, *abort_flag || late)) {
+            if (!*abort_flag) {
+                *abort_flag = 1;
+                record_error(hdr, SIGE_ERR_TIMEOUT, where);
+            }
+            return false;
+        }
+    }
+    return true;
+}
+
 // A unit and the chunks of it that one CTA takes.
 struct Unit {
     int qb, head, n, keys, c_lo, c_hi;
@@ -340,168 +369,167 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
     cluster_arrive();   // the peers' barriers are initialised before the first remote arrival
     bool joined = false;
 
-    if (warp >= 9) {
-        // ---- staging
-        const int t = (int)threadIdx.x - (kSoft + 32);
-        const int nk = p.dh >> 3, nkv = args.dhp >> 3;   // 8-channel vectors of a query row; padded to 16 channels
-        constexpr int kPer = (kKeys * KD / 8 + kStage - 1) / kStage;   // vectors of K, and of V, a thread
-        constexpr int kSets = KD == 64 ? 2 : 1;   // chunks on their way while one is converted (the registers' limit)
-        Stager<kPer, kSets> K, V;
-        K.init(t, nkv, args.dkv, nk, p.D, p.kfmt, L::kKvAtom);
-        V.init(t, p.dvh >> 3, args.dvv, p.dvh >> 3, p.Dv, p.vfmt, L::kKvAtom);
-        int it = 0, st = 0, nu = 0;
-        uint32_t ph = 1;
-        bool ok = true;
-        for (int u = w.u_first; ok && u < w.units; u += w.u_step) {
-            const Unit x = unit_at(p, w, u);
-            const int n = x.c_hi - x.c_lo;
-            if (n <= 0)
-                continue;
-            const int64_t row0 = (int64_t)x.n * p.keys + (int64_t)x.c_lo * kKeys;   // the first chunk's first key
-            K.start(p.kc, row0 * p.D + x.head * p.dh);
-            V.start(p.vc, row0 * p.Dv + x.head * p.dvh);
-            const float *ks = p.ks + row0 * p.kng + x.head * p.dh / p.kgroup;
-            const float *vs = p.vs + row0 * p.vng + x.head * p.dvh / p.vgroup;
-            const int left = x.keys - x.c_lo * kKeys;   // keys from the first chunk on
-            float sr[kSets][2];
-            auto fetch = [&](int i, auto set) {
-                constexpr int s = decltype(set)::value;
-                const int nkeys = left - i * kKeys;
-                K.template fetch<s>(nkeys);
-                V.template fetch<s>(nkeys);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int k = t + e * kStage, key = k & (kKeys - 1), row = i * kKeys + key;
-                    sr[s][e] = 0.0f;
-                    if (k < 2 * kKeys && key < nkeys)
-                        sr[s][e] = k < kKeys ? __ldg(ks + (int64_t)row * p.kng) * args.sc : __ldg(vs + (int64_t)row * p.vng);
-                }
-            };
-            fetch(0, std::integral_constant<int, 0>());
-            if (kSets > 1 && n > 1)
-                fetch(1, std::integral_constant<int, kSets - 1>());
-            // the unit's queries: rows t and t + 96, zeros for padding slots and channels
-            if (nu > 0 && !mbar_wait_w(bar + kBarQEmpty, (nu - 1) & 1, abort_flag, hdr, kSiteQEmpty))
-                break;
-            for (int row = t; row < kRows; row += kStage) {
-                const int slot = x.qb * kRows + row;
-                const int64_t pix = slot < w.slots ? query_pixel(p, x.n, slot) : -1;
-#pragma unroll 1
-                for (int g0 = 0; g0 < nkv; g0 += 8) {
-                    uint4 q[8];
-#pragma unroll
-                    for (int g = 0; g < 8; ++g) {
-                        q[g] = make_uint4(0, 0, 0, 0);
-                        if (pix >= 0 && g0 + g < nk)
-                            q[g] = ld_nc16(p.q + pix * p.D + x.head * p.dh + 8 * (g0 + g));
-                    }
-#pragma unroll
-                    for (int g = 0; g < 8; ++g)
-                        if (g0 + g < nkv)
-                            sts128(sb + L::kOffQ + place(L::kQAtom, row, g0 + g), q[g]);
-                }
-            }
-            fence_async_smem();
-            mbar_arrive(bar + kBarQFull);
-            ++nu;
-            auto stage = [&](int i, auto set) -> bool {
-                constexpr int s = decltype(set)::value;
-                if (it >= L::kStages && !mbar_wait_w(bar + kBarKvEmpty + 8u * st, ph, abort_flag, hdr, kSiteKvEmpty))
-                    return false;
-                const uint32_t kb = sb + L::kOffK + (uint32_t)st * L::kKvStage;
-                K.template store<s>(kb);
-                V.template store<s>(kb + L::kAtoms * L::kKvAtom);
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (t + e * kStage < 2 * kKeys)
-                        sts_f1(sb + L::kOffSc + (uint32_t)st * 512u + (uint32_t)(t + e * kStage) * 4u, sr[s][e]);
-                fence_async_smem();
-                mbar_arrive(bar + kBarKvFull + 8u * st);
-                if (i + kSets < n)
-                    fetch(i + kSets, set);
-                ++it;
-                if (++st == L::kStages) {
-                    st = 0;
-                    ph ^= 1;
-                }
-                return true;
-            };
-            for (int i = 0; ok && i < n; i += 2) {
-                ok = stage(i, std::integral_constant<int, 0>());
-                if (ok && i + 1 < n)
-                    ok = stage(i + 1, std::integral_constant<int, kSets - 1>());
-            }
-        }
-        __syncwarp();
-    } else if (warp == 8) {
-        // ---- products
-        const uint32_t id_s = idesc_bf16(kKeys);
-        const int dv0 = min(args.dvp, 64), dv1 = args.dvp - dv0;
-        const uint32_t id_o0 = idesc_bf16(dv0) | (1u << 16), id_o1 = idesc_bf16(dv1) | (1u << 16);   // B (V) MN-major
-        const int ks = args.dhp / 16;
-        int s_it = 0, pv_it = 0, nu = 0;      // chunks whose S / P V has been issued
-        int ns[2] = {0, 0}, np[2] = {0, 0};   // of each softmax group
-        bool ok = true;
-        for (int u = w.u_first; ok && u < w.units; u += w.u_step) {
-            const Unit x = unit_at(p, w, u);
-            const int n = x.c_hi - x.c_lo;
-            if (n <= 0)
-                continue;
-            if (!mbar_wait_w(bar + kBarQFull, nu & 1, abort_flag, hdr, kSiteQFull))
-                break;
-            ++nu;
-            auto issue_s = [&](int i) -> bool {
-                const int st = s_it % L::kStages, g = i & 1, b = ns[g] & 1;
-                if (!mbar_wait_w(bar + kBarKvFull + 8u * st, (s_it / L::kStages) & 1, abort_flag, hdr, kSiteKvFull))
-                    return false;
-                tc_fence_after();
-                const uint32_t kb = sb + L::kOffK + (uint32_t)st * L::kKvStage;
-                for (int kk = 0; kk < ks; ++kk)
-                    mma_ss_w(tmem + 128u * g + 64u * b, desc_sw128(sb + L::kOffQ + (kk >> 2) * L::kQAtom) + 2u * (kk & 3),
-                             desc_sw128(kb + (kk >> 2) * L::kKvAtom) + 2u * (kk & 3), id_s, kk > 0);
-                tc_commit_w(bar + kBarSFull + 16u * g + 8u * b);
-                ++ns[g];
-                ++s_it;
-                if (i + 1 == n)
-                    tc_commit_w(bar + kBarQEmpty);
-                return true;
-            };
-            constexpr int kAhead = L::kAhead;
-            for (int i = 0; ok && i < min(kAhead, n); ++i)
-                ok = issue_s(i);
-            for (int i = 0; ok && i < n; ++i) {
-                const int g = i & 1, b = np[g] & 1;
-                if (!mbar_wait_w(bar + kBarPFull + 16u * g + 8u * b, (np[g] >> 1) & 1, abort_flag, hdr, kSitePFull)) {
-                    ok = false;
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kStageRegs));
+        if (warp > 8) {
+            // ---- staging
+            const int t = (int)threadIdx.x - (kSoft + 32);
+            const int nk = p.dh >> 3, nkv = args.dhp >> 3;   // 8-channel vectors of a query row; padded to 16 channels
+            constexpr int kPer = (kKeys * KD / 8 + kStage - 1) / kStage;   // vectors of K, and of V, a thread
+            constexpr int kSets = 2;   // chunks on their way while one is converted
+            Stager<kPer, kSets> K, V;
+            K.init(t, nkv, args.dkv, nk, p.D, p.kfmt, L::kKvAtom);
+            V.init(t, p.dvh >> 3, args.dvv, p.dvh >> 3, p.Dv, p.vfmt, L::kKvAtom);
+            int it = 0, st = 0, nu = 0;
+            uint32_t ph = 1;
+            bool ok = true;
+            for (int u = w.u_first; ok && u < w.units; u += w.u_step) {
+                const Unit x = unit_at(p, w, u);
+                const int n = x.c_hi - x.c_lo;
+                if (n <= 0)
+                    continue;
+                const int64_t row0 = (int64_t)x.n * p.keys + (int64_t)x.c_lo * kKeys;   // the first chunk's first key
+                K.start(p.kc, row0 * p.D + x.head * p.dh);
+                V.start(p.vc, row0 * p.Dv + x.head * p.dvh);
+                const float *ks = p.ks + row0 * p.kng + x.head * p.dh / p.kgroup;
+                const float *vs = p.vs + row0 * p.vng + x.head * p.dvh / p.vgroup;
+                const int left = x.keys - x.c_lo * kKeys;   // keys from the first chunk on
+                float sr[kSets];
+                auto fetch = [&](int i, auto set) {
+                    constexpr int s = decltype(set)::value;
+                    const int nkeys = left - i * kKeys;
+                    K.template fetch<s>(nkeys);
+                    V.template fetch<s>(nkeys);
+                    const int key = t & (kKeys - 1), row = i * kKeys + key;
+                    sr[s] = 0.0f;
+                    if (t < 2 * kKeys && key < nkeys)
+                        sr[s] = t < kKeys ? __ldg(ks + (int64_t)row * p.kng) * args.sc : __ldg(vs + (int64_t)row * p.vng);
+                };
+                fetch(0, std::integral_constant<int, 0>());
+                if (kSets > 1 && n > 1)
+                    fetch(1, std::integral_constant<int, kSets - 1>());
+                // the unit's queries: row t, zeros for padding slots and channels
+                if (nu > 0 && !wait_w<false>(bar + kBarQEmpty, (nu - 1) & 1, abort_flag, hdr, kSiteQEmpty))
                     break;
+                if (t < kRows) {
+                    const int row = t, slot = x.qb * kRows + row;
+                    const int64_t pix = slot < w.slots ? query_pixel(p, x.n, slot) : -1;
+#pragma unroll 1
+                    for (int g0 = 0; g0 < nkv; g0 += 4) {
+                        uint4 q[4];
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            q[g] = make_uint4(0, 0, 0, 0);
+                            if (pix >= 0 && g0 + g < nk)
+                                q[g] = ld_nc16(p.q + pix * p.D + x.head * p.dh + 8 * (g0 + g));
+                        }
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            if (g0 + g < nkv)
+                                sts128(sb + L::kOffQ + place(L::kQAtom, row, g0 + g), q[g]);
+                    }
                 }
-                tc_fence_after();
-                const int st = pv_it % L::kStages;
-                const uint32_t vb = sb + L::kOffK + (uint32_t)st * L::kKvStage + L::kAtoms * L::kKvAtom;
-                const uint32_t d = tmem + kTmemO + 128u * g, pa = tmem + 128u * g + 64u * b;
-                for (int kk = 0; kk < kKeys / 16; ++kk)
-                    mma_ts_w(d, pa + 8u * kk, desc_sw128(vb + kk * 2048), id_o0, i > 1 || kk > 0);
-                if (dv1 > 0)
-                    for (int kk = 0; kk < kKeys / 16; ++kk)
-                        mma_ts_w(d + 64u, pa + 8u * kk, desc_sw128(vb + L::kKvAtom + kk * 2048), id_o1, i > 1 || kk > 0);
-                tc_commit_w(bar + kBarPvDone + 8u * g);
-                tc_commit_w(bar + kBarKvEmpty + 8u * st);
-                ++np[g];
-                ++pv_it;
-                if (i + kAhead < n)
-                    ok = issue_s(i + kAhead);
+                fence_async_smem();
+                mbar_arrive(bar + kBarQFull);
+                ++nu;
+                auto stage = [&](int i, auto set) -> bool {
+                    constexpr int s = decltype(set)::value;
+                    if (it >= L::kStages && !wait_w<false>(bar + kBarKvEmpty + 8u * st, ph, abort_flag, hdr, kSiteKvEmpty))
+                        return false;
+                    const uint32_t kb = sb + L::kOffK + (uint32_t)st * L::kKvStage;
+                    K.template store<s>(kb);
+                    V.template store<s>(kb + L::kAtoms * L::kKvAtom);
+                    if (t < 2 * kKeys)
+                        sts_f1(sb + L::kOffSc + (uint32_t)st * 512u + (uint32_t)t * 4u, sr[s]);
+                    fence_async_smem();
+                    mbar_arrive(bar + kBarKvFull + 8u * st);
+                    if (i + kSets < n)
+                        fetch(i + kSets, set);
+                    ++it;
+                    if (++st == L::kStages) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                    return true;
+                };
+                for (int i = 0; ok && i < n; i += 2) {
+                    ok = stage(i, std::integral_constant<int, 0>());
+                    if (ok && i + 1 < n)
+                        ok = stage(i + 1, std::integral_constant<int, kSets - 1>());
+                }
             }
+            __syncwarp();
+        } else {
+            // ---- products
+            const uint32_t id_s = idesc_bf16(kKeys);
+            const int dv0 = min(args.dvp, 64), dv1 = args.dvp - dv0;
+            const uint32_t id_o0 = idesc_bf16(dv0) | (1u << 16), id_o1 = idesc_bf16(dv1) | (1u << 16);   // B (V) MN-major
+            const int ks = args.dhp / 16;
+            int s_it = 0, pv_it = 0, nu = 0;      // chunks whose S / P V has been issued
+            int ns[2] = {0, 0}, np[2] = {0, 0};   // of each softmax group
+            bool ok = true;
+            for (int u = w.u_first; ok && u < w.units; u += w.u_step) {
+                const Unit x = unit_at(p, w, u);
+                const int n = x.c_hi - x.c_lo;
+                if (n <= 0)
+                    continue;
+                if (!wait_w<false>(bar + kBarQFull, nu & 1, abort_flag, hdr, kSiteQFull))
+                    break;
+                ++nu;
+                auto issue_s = [&](int i) -> bool {
+                    const int st = s_it % L::kStages, g = i & 1, b = ns[g] & 1;
+                    if (!wait_w<false>(bar + kBarKvFull + 8u * st, (s_it / L::kStages) & 1, abort_flag, hdr, kSiteKvFull))
+                        return false;
+                    tc_fence_after();
+                    const uint32_t kb = sb + L::kOffK + (uint32_t)st * L::kKvStage;
+                    for (int kk = 0; kk < ks; ++kk)
+                        mma_ss_w(tmem + 128u * g + 64u * b, desc_sw128(sb + L::kOffQ + (kk >> 2) * L::kQAtom) + 2u * (kk & 3),
+                                 desc_sw128(kb + (kk >> 2) * L::kKvAtom) + 2u * (kk & 3), id_s, kk > 0);
+                    tc_commit_w(bar + kBarSFull + 16u * g + 8u * b);
+                    ++ns[g];
+                    ++s_it;
+                    if (i + 1 == n)
+                        tc_commit_w(bar + kBarQEmpty);
+                    return true;
+                };
+                constexpr int kAhead = L::kAhead;
+                for (int i = 0; ok && i < min(kAhead, n); ++i)
+                    ok = issue_s(i);
+                for (int i = 0; ok && i < n; ++i) {
+                    const int g = i & 1, b = np[g] & 1;
+                    if (!wait_w<false>(bar + kBarPFull + 16u * g + 8u * b, (np[g] >> 1) & 1, abort_flag, hdr, kSitePFull)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const int st = pv_it % L::kStages;
+                    const uint32_t vb = sb + L::kOffK + (uint32_t)st * L::kKvStage + L::kAtoms * L::kKvAtom;
+                    const uint32_t d = tmem + kTmemO + 128u * g, pa = tmem + 128u * g + 64u * b;
+                    for (int kk = 0; kk < kKeys / 16; ++kk)
+                        mma_ts_w(d, pa + 8u * kk, desc_sw128(vb + kk * 2048), id_o0, i > 1 || kk > 0);
+                    if (dv1 > 0)
+                        for (int kk = 0; kk < kKeys / 16; ++kk)
+                            mma_ts_w(d + 64u, pa + 8u * kk, desc_sw128(vb + L::kKvAtom + kk * 2048), id_o1, i > 1 || kk > 0);
+                    tc_commit_w(bar + kBarPvDone + 8u * g);
+                    tc_commit_w(bar + kBarKvEmpty + 8u * st);
+                    ++np[g];
+                    ++pv_it;
+                    if (i + kAhead < n)
+                        ok = issue_s(i + kAhead);
+                }
+            }
+            if (!ok) {
+                // the products in flight finish before this CTA's memory is given up
+                tc_commit_w(bar + kBarDrain);
+                const long long t0 = clock64();
+                while (!mbar_try(bar + kBarDrain, 0) && clock64() - t0 < kWaitCycles / 64)
+                    ;
+            }
+            __syncwarp();
         }
-        if (!ok) {
-            // the products in flight finish before this CTA's memory is given up
-            tc_commit_w(bar + kBarDrain);
-            const long long t0 = clock64();
-            while (!mbar_try(bar + kBarDrain, 0) && clock64() - t0 < kWaitCycles / 64)
-                ;
-        }
-        __syncwarp();
     } else {
         // ---- softmax: thread = query row r of group g
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         const int g = warp >> 2;
         const int r = (warp & 3) * 32 + lane;
         const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -513,33 +541,37 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
             const Unit x = unit_at(p, w, u);
             const int n = x.c_hi - x.c_lo;
             float m_used = -INFINITY, l = 0.0f;
-            for (int i = g; ok && i < n; i += 2, ++m_it) {
+            // one chunk; kTail: the item's last, with keys to mask
+            auto one = [&](int i, auto tail) {
+                constexpr bool kTail = decltype(tail)::value;
+                const int kvalid = x.keys - (x.c_lo + i) * kKeys;
                 const int b = m_it & 1;
                 // (the staged scales are seen through the stage's own barrier; its
                 // next phase waits for this chunk's P V)
                 const int ci = chunk + i;
-                if (!mbar_wait_w(bar + kBarKvFull + 8u * (ci % L::kStages), (ci / L::kStages) & 1, abort_flag, hdr, kSiteKvFull) ||
-                    !mbar_wait_w(bar + kBarSFull + 16u * g + 8u * b, (m_it >> 1) & 1, abort_flag, hdr, kSiteSFull)) {
+                if (!wait_w<false>(bar + kBarKvFull + 8u * (ci % L::kStages), (ci / L::kStages) & 1, abort_flag, hdr, kSiteKvFull) ||
+                    !wait_w<false>(bar + kBarSFull + 16u * g + 8u * b, (m_it >> 1) & 1, abort_flag, hdr, kSiteSFull)) {
                     ok = false;
-                    break;
+                    return;
                 }
                 tc_fence_after();
                 const uint32_t sc = sb + L::kOffSc + (uint32_t)(ci % L::kStages) * 512u;
-                uint32_t sr[2][32];
-                ld32(t_s + 64u * b, sr[0]);
-                ld32(t_s + 64u * b + 32u, sr[1]);
-                ld_wait();
                 // scores in pairs (the packed float32 instructions: half as many)
                 uint64_t sv[kKeys / 2];
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                const int kvalid = x.keys - (x.c_lo + i) * kKeys;
 #pragma unroll
-                for (int k = 0; k < kKeys; k += 4) {
-                    const ulonglong2 s4 = lds_2x2(sc + 4u * k);
-                    sv[k / 2] = mul2(pair(sr[k >> 5][k & 31], sr[k >> 5][(k + 1) & 31]), s4.x);
-                    sv[k / 2 + 1] = mul2(pair(sr[k >> 5][(k + 2) & 31], sr[k >> 5][(k + 3) & 31]), s4.y);
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t sr[32];
+                    ld32(t_s + 64u * b + 32u * h, sr);
+                    ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        const ulonglong2 s4 = lds_2x2(sc + 4u * (32 * h + k));
+                        sv[16 * h + k / 2] = mul2(pair(sr[k], sr[k + 1]), s4.x);
+                        sv[16 * h + k / 2 + 1] = mul2(pair(sr[k + 2], sr[k + 3]), s4.y);
+                    }
                 }
-                if (kvalid < kKeys) {
+                if constexpr (kTail) {
 #pragma unroll
                     for (int k = 0; k < kKeys; k += 2) {
                         if (k >= kvalid)
@@ -578,9 +610,9 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
                 l = l * corr + ((lo_of(ls[0]) + hi_of(ls[0])) + (lo_of(ls[1]) + hi_of(ls[1])));
                 // the group's previous P V has landed (each of its phases is waited
                 // for in turn: a parity tells two neighbouring phases apart, no more)
-                if (i > 1 && !mbar_wait_w(bar + kBarPvDone + 8u * g, (m_it - 1) & 1, abort_flag, hdr, kSitePvDone)) {
+                if (i > 1 && !wait_w<false>(bar + kBarPvDone + 8u * g, (m_it - 1) & 1, abort_flag, hdr, kSitePvDone)) {
                     ok = false;
-                    break;
+                    return;
                 }
                 if (i > 1 && __any_sync(0xFFFFFFFFu, grow)) {
                     // rescale this warp's O rows
@@ -601,12 +633,18 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
                 tc_fence_before();
                 mbar_arrive(bar + kBarPFull + 16u * g + 8u * b);
                 m_used = m_new;
+            };
+            for (int i = g; ok && i < n; i += 2, ++m_it) {
+                if (x.keys - (x.c_lo + i) * kKeys >= kKeys)
+                    one(i, std::false_type());
+                else
+                    one(i, std::true_type());
             }
             chunk += max(0, n);
             // the group's last P V of the unit has landed
             const bool mine = n > g;
             if (ok && mine)
-                ok = mbar_wait_w(bar + kBarPvDone + 8u * g, (m_it - 1) & 1, abort_flag, hdr, kSitePvDone);
+                ok = wait_w<false>(bar + kBarPvDone + 8u * g, (m_it - 1) & 1, abort_flag, hdr, kSitePvDone);
             tc_fence_after();
             if (w.split == 1) {
                 // ---- merge of the two groups: each thread finishes the 8-channel
@@ -672,7 +710,7 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
             tc_fence_before();
             for (int i = 0; i < s; ++i)
                 mbar_arrive_peer(map_peer(bar + kBarReady, (uint32_t)(w.base + i)));
-            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar + kBarReady, 0, abort_flag, hdr, kSiteReady));
+            ok = ok && wait_w<true>(bar + kBarReady, 0, abort_flag, hdr, kSiteReady);
             if (!ok)
                 continue;
             {
@@ -694,7 +732,7 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
                 st_peer_f32x2(map_peer(sb + L::kOffMl + slot * 8u, (uint32_t)(w.base + owner)), m_used, mine ? l : -1.0f);
                 mbar_arrive_peer(map_peer(bar + kBarPush, (uint32_t)(w.base + owner)));   // releases the pushes
             }
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar + kBarPush, 0, abort_flag, hdr, kSitePush))) {
+            if (!wait_w<true>(bar + kBarPush, 0, abort_flag, hdr, kSitePush)) {
                 ok = false;
                 continue;
             }
