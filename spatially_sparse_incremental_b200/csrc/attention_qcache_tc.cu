@@ -13,15 +13,16 @@
 //     into bf16 rows of 128 bytes with the 128-byte swizzle (K-major for the
 //     first product, MN-major for the second), and the chunk's scales;
 //   * warp 8 issues S = Q K^T (M 128, N 64) and O += P V (M 128, K 64);
-//   * warps 0 .. 3 and 4 .. 7 are two softmax groups that take every other
-//     chunk, one query row a thread: running maximum and sum (float32),
+//   * warps 0 .. 3 and 4 .. 7 are two softmax groups, one query row a thread,
+//     that take every other chunk, or (more units than CTAs) a block of 128
+//     queries each, so that a chunk is staged once for 256 queries: running maximum and sum (float32),
 //     P = 2^(s - max) * value scale as bf16 over the chunk's own S columns, the
 //     O row in tensor memory rescaled only when the maximum has grown by more
 //     than 8 (base 2).  Each group has two S buffers, so the scores of its next
 //     chunk are there when it has finished one; with one group waiting the
 //     other keeps the exponentials busy.
-// The groups' rows (O, max, sum) are merged through shared memory at the end
-// of a unit.  Where units are fewer than half the CTAs, the CTAs of a cluster
+// Rows (O, max, sum) of groups that share a block are merged through shared
+// memory at the end of a unit.  Where units are fewer than half the CTAs, the CTAs of a cluster
 // also split the keys and push their rows to the row's owner through
 // distributed shared memory.
 #include <algorithm>
@@ -55,11 +56,12 @@ template <int KD>
 struct Lay {
     static constexpr int kAtoms = KD / 64;                            // 64-channel blocks of 128-byte rows
     static constexpr int kStages = KD == 64 ? 6 : 3;                  // chunk ring
-    static constexpr int kAhead = KD == 64 ? 4 : 2;                   // chunks whose S may be issued before their P V:
-                                                                      // fewer than the ring's, whose next is being staged
+    static constexpr int kAhead = KD == 64 ? 4 : 2;                   // S products issued before the P V of the first:
+                                                                      // fewer chunks than the ring's, whose next is being staged
     static constexpr uint32_t kQAtom = kRows * 128, kKvAtom = kKeys * 128;
     static constexpr uint32_t kOffQ = 0;
-    static constexpr uint32_t kOffX = kAtoms * kQAtom;                // rows exchanged by the two groups
+    static constexpr uint32_t kOffX = kAtoms * kQAtom;                // rows exchanged by the two groups of a block,
+    static constexpr uint32_t kOffQ2 = kOffX;                         // or the second block's queries
     static constexpr uint32_t kOffK = kOffX + kRows * KD * 4;         // [stage][K atoms, V atoms]
     static constexpr uint32_t kKvStage = 2 * kAtoms * kKvAtom;
     static constexpr uint32_t kOffSc = kOffK + kStages * kKvStage;    // [stage][64 key scales, 64 value scales]
@@ -279,17 +281,18 @@ __device__ __forceinline__ bool wait_w(uint32_t b, uint32_t parity, volatile int
 
 // A unit and the chunks of it that one CTA takes.
 struct Unit {
-    int qb, head, n, keys, c_lo, c_hi;
+    int slot0, head, n, keys, c_lo, c_hi;
 };
 
 struct Work {
     int qblocks, slots, units, split, per, u_first, u_step, rank_split, base;
+    int pairs;   // the two softmax groups take a query block each (else they share one)
 };
 
 __device__ __forceinline__ Unit unit_at(const AttnQParams &p, const Work &w, int u)
 {
     Unit x;
-    x.qb = u % w.qblocks;
+    x.slot0 = (u % w.qblocks) * (kRows << w.pairs);
     const int rest = u / w.qblocks;
     x.head = rest % p.heads;
     x.n = rest / p.heads;
@@ -327,13 +330,17 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
     Work w;
     w.slots = query_slots(p);
     w.qblocks = (w.slots + kRows - 1) / kRows;
+    // one block of 128 queries fills a CTA when there are CTAs for all of them;
+    // otherwise two blocks share each chunk's staging
+    w.pairs = (int64_t)w.qblocks * p.N * p.heads > (int64_t)gridDim.x;
+    w.qblocks = (w.qblocks + w.pairs) >> w.pairs;
     w.units = w.qblocks * p.N * p.heads;
     {
         // the key split: the same on every CTA (it depends on the list's
         // length and the cache's keys); a split unit is its CTAs' only one
         const int nch = (p.keys + kKeys - 1) / kKeys;
         w.split = kCluster;
-        while (w.split > 1 && ((int64_t)w.units * w.split > (int64_t)gridDim.x || nch < 4 * w.split))
+        while (w.split > 1 && (w.pairs || (int64_t)w.units * w.split > (int64_t)gridDim.x || nch < 4 * w.split))
             w.split >>= 1;
         w.per = kCluster / w.split;
         const int rank = (int)cluster_rank(), sub = rank / w.split;
@@ -408,12 +415,13 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
                 fetch(0, std::integral_constant<int, 0>());
                 if (kSets > 1 && n > 1)
                     fetch(1, std::integral_constant<int, kSets - 1>());
-                // the unit's queries: row t, zeros for padding slots and channels
+                // the unit's queries, a row a thread, zeros for padding slots and channels
                 if (nu > 0 && !wait_w<false>(bar + kBarQEmpty, (nu - 1) & 1, abort_flag, hdr, kSiteQEmpty))
                     break;
-                if (t < kRows) {
-                    const int row = t, slot = x.qb * kRows + row;
+                for (int row = t; row < kRows << w.pairs; row += kStage) {
+                    const int slot = x.slot0 + row;
                     const int64_t pix = slot < w.slots ? query_pixel(p, x.n, slot) : -1;
+                    const uint32_t dst = sb + (row < kRows ? L::kOffQ : L::kOffQ2);
 #pragma unroll 1
                     for (int g0 = 0; g0 < nkv; g0 += 4) {
                         uint4 q[4];
@@ -426,7 +434,7 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
 #pragma unroll
                         for (int g = 0; g < 4; ++g)
                             if (g0 + g < nkv)
-                                sts128(sb + L::kOffQ + place(L::kQAtom, row, g0 + g), q[g]);
+                                sts128(dst + place(L::kQAtom, row & (kRows - 1), g0 + g), q[g]);
                     }
                 }
                 fence_async_smem();
@@ -465,58 +473,60 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
             const int dv0 = min(args.dvp, 64), dv1 = args.dvp - dv0;
             const uint32_t id_o0 = idesc_bf16(dv0) | (1u << 16), id_o1 = idesc_bf16(dv1) | (1u << 16);   // B (V) MN-major
             const int ks = args.dhp / 16;
-            int s_it = 0, pv_it = 0, nu = 0;      // chunks whose S / P V has been issued
-            int ns[2] = {0, 0}, np[2] = {0, 0};   // of each softmax group
+            int chunk = 0, nu = 0;                // chunks, units of the CTA so far
+            int ns[2] = {0, 0}, np[2] = {0, 0};   // S and P V products of each softmax group so far
             bool ok = true;
             for (int u = w.u_first; ok && u < w.units; u += w.u_step) {
                 const Unit x = unit_at(p, w, u);
-                const int n = x.c_hi - x.c_lo;
-                if (n <= 0)
+                // job j: group j mod 2 on chunk j, or on chunk j / 2 when the
+                // groups take a block each
+                const int jobs = (x.c_hi - x.c_lo) << w.pairs;
+                if (jobs <= 0)
                     continue;
                 if (!wait_w<false>(bar + kBarQFull, nu & 1, abort_flag, hdr, kSiteQFull))
                     break;
                 ++nu;
-                auto issue_s = [&](int i) -> bool {
-                    const int st = s_it % L::kStages, g = i & 1, b = ns[g] & 1;
-                    if (!wait_w<false>(bar + kBarKvFull + 8u * st, (s_it / L::kStages) & 1, abort_flag, hdr, kSiteKvFull))
+                auto issue_s = [&](int j) -> bool {
+                    const int ci = chunk + (j >> w.pairs), st = ci % L::kStages, g = j & 1, b = ns[g] & 1;
+                    if (!wait_w<false>(bar + kBarKvFull + 8u * st, (ci / L::kStages) & 1, abort_flag, hdr, kSiteKvFull))
                         return false;
                     tc_fence_after();
                     const uint32_t kb = sb + L::kOffK + (uint32_t)st * L::kKvStage;
+                    const uint32_t qb = sb + (w.pairs && g ? L::kOffQ2 : L::kOffQ);
                     for (int kk = 0; kk < ks; ++kk)
-                        mma_ss_w(tmem + 128u * g + 64u * b, desc_sw128(sb + L::kOffQ + (kk >> 2) * L::kQAtom) + 2u * (kk & 3),
+                        mma_ss_w(tmem + 128u * g + 64u * b, desc_sw128(qb + (kk >> 2) * L::kQAtom) + 2u * (kk & 3),
                                  desc_sw128(kb + (kk >> 2) * L::kKvAtom) + 2u * (kk & 3), id_s, kk > 0);
                     tc_commit_w(bar + kBarSFull + 16u * g + 8u * b);
                     ++ns[g];
-                    ++s_it;
-                    if (i + 1 == n)
+                    if (j + 1 == jobs)
                         tc_commit_w(bar + kBarQEmpty);
                     return true;
                 };
-                constexpr int kAhead = L::kAhead;
-                for (int i = 0; ok && i < min(kAhead, n); ++i)
-                    ok = issue_s(i);
-                for (int i = 0; ok && i < n; ++i) {
-                    const int g = i & 1, b = np[g] & 1;
+                for (int j = 0; ok && j < min(L::kAhead, jobs); ++j)
+                    ok = issue_s(j);
+                for (int j = 0; ok && j < jobs; ++j) {
+                    const int g = j & 1, b = np[g] & 1;
                     if (!wait_w<false>(bar + kBarPFull + 16u * g + 8u * b, (np[g] >> 1) & 1, abort_flag, hdr, kSitePFull)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const int st = pv_it % L::kStages;
+                    const int st = (chunk + (j >> w.pairs)) % L::kStages;
                     const uint32_t vb = sb + L::kOffK + (uint32_t)st * L::kKvStage + L::kAtoms * L::kKvAtom;
                     const uint32_t d = tmem + kTmemO + 128u * g, pa = tmem + 128u * g + 64u * b;
                     for (int kk = 0; kk < kKeys / 16; ++kk)
-                        mma_ts_w(d, pa + 8u * kk, desc_sw128(vb + kk * 2048), id_o0, i > 1 || kk > 0);
+                        mma_ts_w(d, pa + 8u * kk, desc_sw128(vb + kk * 2048), id_o0, j > 1 || kk > 0);
                     if (dv1 > 0)
                         for (int kk = 0; kk < kKeys / 16; ++kk)
-                            mma_ts_w(d + 64u, pa + 8u * kk, desc_sw128(vb + L::kKvAtom + kk * 2048), id_o1, i > 1 || kk > 0);
+                            mma_ts_w(d + 64u, pa + 8u * kk, desc_sw128(vb + L::kKvAtom + kk * 2048), id_o1, j > 1 || kk > 0);
                     tc_commit_w(bar + kBarPvDone + 8u * g);
-                    tc_commit_w(bar + kBarKvEmpty + 8u * st);
+                    if (!w.pairs || g == 1)
+                        tc_commit_w(bar + kBarKvEmpty + 8u * st);
                     ++np[g];
-                    ++pv_it;
-                    if (i + kAhead < n)
-                        ok = issue_s(i + kAhead);
+                    if (j + L::kAhead < jobs)
+                        ok = issue_s(j + L::kAhead);
                 }
+                chunk += x.c_hi - x.c_lo;
             }
             if (!ok) {
                 // the products in flight finish before this CTA's memory is given up
@@ -539,16 +549,16 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
         bool ok = true;
         for (int u = w.u_first; u < w.units; u += w.u_step) {
             const Unit x = unit_at(p, w, u);
-            const int n = x.c_hi - x.c_lo;
+            const int n = (x.c_hi - x.c_lo) << w.pairs;   // jobs, those of parity g are this group's
             float m_used = -INFINITY, l = 0.0f;
-            // one chunk; kTail: the item's last, with keys to mask
+            // one job; kTail: its chunk is the item's last, with keys to mask
             auto one = [&](int i, auto tail) {
                 constexpr bool kTail = decltype(tail)::value;
-                const int kvalid = x.keys - (x.c_lo + i) * kKeys;
+                const int kvalid = x.keys - (x.c_lo + (i >> w.pairs)) * kKeys;
                 const int b = m_it & 1;
                 // (the staged scales are seen through the stage's own barrier; its
                 // next phase waits for this chunk's P V)
-                const int ci = chunk + i;
+                const int ci = chunk + (i >> w.pairs);
                 if (!wait_w<false>(bar + kBarKvFull + 8u * (ci % L::kStages), (ci / L::kStages) & 1, abort_flag, hdr, kSiteKvFull) ||
                     !wait_w<false>(bar + kBarSFull + 16u * g + 8u * b, (m_it >> 1) & 1, abort_flag, hdr, kSiteSFull)) {
                     ok = false;
@@ -635,17 +645,43 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
                 m_used = m_new;
             };
             for (int i = g; ok && i < n; i += 2, ++m_it) {
-                if (x.keys - (x.c_lo + i) * kKeys >= kKeys)
+                if (x.keys - (x.c_lo + (i >> w.pairs)) * kKeys >= kKeys)
                     one(i, std::false_type());
                 else
                     one(i, std::true_type());
             }
-            chunk += max(0, n);
+            chunk += x.c_hi - x.c_lo;
             // the group's last P V of the unit has landed
             const bool mine = n > g;
             if (ok && mine)
                 ok = wait_w<false>(bar + kBarPvDone + 8u * g, (m_it - 1) & 1, abort_flag, hdr, kSitePvDone);
             tc_fence_after();
+            if (w.pairs) {
+                // ---- the group's block of queries: its rows are finished
+                const int slot = x.slot0 + g * kRows + r;
+                const int64_t pix = slot < w.slots ? query_pixel(p, x.n, slot) : -1;
+                if (!ok)
+                    continue;
+                const float inv = mine ? 1.0f / l : 0.0f;   // (no key at all: zeros)
+#pragma unroll
+                for (int pc = 0; pc < KD / 16; ++pc) {
+                    if (pc * 16 < args.dvp) {
+                        float v[16];
+                        if (mine)
+                            tmem_ld16(t_o + 16u * pc, v);
+#pragma unroll
+                        for (int q = 0; q < 16; ++q)
+                            v[q] = mine ? v[q] : 0.0f;
+                        __nv_bfloat16 *dst = p.o + pix * p.Dv + x.head * p.dvh + 16 * pc;
+                        if (pix >= 0)
+                            store8(dst, v, inv);
+                        if (pix >= 0 && 2 * pc + 1 < ng)
+                            store8(dst + 8, v + 8, inv);
+                    }
+                }
+                tc_fence_before();
+                continue;
+            }
             if (w.split == 1) {
                 // ---- merge of the two groups: each thread finishes the 8-channel
                 // groups of its parity of its row, from the other's copy of them
@@ -674,7 +710,7 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
                     tc_fence_before();
                 }
                 soft_sync();
-                const int slot = x.qb * kRows + r;
+                const int slot = x.slot0 + r;
                 const int64_t pix = slot < w.slots ? query_pixel(p, x.n, slot) : -1;
                 if (ok && pix >= 0) {
                     const float2 ml = lds_f2(sb + L::kOffMl + (uint32_t)((1 - g) * kRows + r) * 8u);
@@ -738,7 +774,7 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
             }
             for (int item = (int)threadIdx.x; item < rows * ng; item += kSoft) {
                 const int j = item % rows, gi = item / rows;
-                const int slot = x.qb * kRows + w.rank_split * rows + j;
+                const int slot = x.slot0 + w.rank_split * rows + j;
                 const int64_t pix = slot < w.slots ? query_pixel(p, x.n, slot) : -1;
                 if (pix < 0)
                     continue;
