@@ -225,6 +225,42 @@ struct Stager {
     }
 };
 
+// The scores of a chunk over one 64-channel block: `steps` (1 .. 4) steps of 16
+// channels (32 bytes along the swizzled rows of both operands), from one
+// elected lane.
+__device__ __forceinline__ void mma_s_w(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, int steps)
+{
+    asm volatile(
+        "{\n .reg .pred p, e, t, e1, e2, e3;\n .reg .b32 l;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"
+        " elect.sync l|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
+        " setp.gt.and.s32 e1, %5, 1, e;\n setp.gt.and.s32 e2, %5, 2, e;\n setp.gt.and.s32 e3, %5, 3, e;\n"
+        " add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"
+        " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+        " @e1 tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n"
+        " @e2 tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n"
+        " @e3 tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(steps)
+        : "memory");
+}
+
+// O (+)= P V over a chunk's 64 keys for one 64-channel block of V: four steps
+// of 16 keys (8 columns of P in tensor memory, 2 KB of V), from one elected lane.
+__device__ __forceinline__ void mma_pv_w(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n .reg .pred p, e, t;\n .reg .b32 l, a1, a2, a3;\n .reg .b64 b1, b2, b3;\n"
+        " elect.sync l|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
+        " add.u32 a1, %1, 8;\n add.u32 a2, %1, 16;\n add.u32 a3, %1, 24;\n"
+        " add.s64 b1, %2, 128;\n add.s64 b2, %2, 256;\n add.s64 b3, %2, 384;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Pairs of float32.
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; }
 __device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
@@ -472,9 +508,12 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
             const uint32_t id_s = idesc_bf16(kKeys);
             const int dv0 = min(args.dvp, 64), dv1 = args.dvp - dv0;
             const uint32_t id_o0 = idesc_bf16(dv0) | (1u << 16), id_o1 = idesc_bf16(dv1) | (1u << 16);   // B (V) MN-major
-            const int ks = args.dhp / 16;
-            int chunk = 0, nu = 0;                // chunks, units of the CTA so far
-            int ns[2] = {0, 0}, np[2] = {0, 0};   // S and P V products of each softmax group so far
+            const int ks0 = min(args.dhp, 64) / 16, ks1 = args.dhp / 16 - ks0;   // 16-channel steps of each block
+            const uint64_t qd = desc_sw128(sb + L::kOffQ), q2d = desc_sw128(sb + (w.pairs ? L::kOffQ2 : L::kOffQ));
+            const uint64_t kd = desc_sw128(sb + L::kOffK), vd = desc_sw128(sb + L::kOffK + L::kAtoms * L::kKvAtom);
+            int s_st = 0, v_st = 0, nu = 0;   // stage of the next S's chunk, of the next P V's; units so far
+            uint32_t s_ph = 0;
+            uint32_t s_n[2] = {0, 0}, p_n[2] = {0, 0};   // S and P V products of each group so far
             bool ok = true;
             for (int u = w.u_first; ok && u < w.units; u += w.u_step) {
                 const Unit x = unit_at(p, w, u);
@@ -486,47 +525,60 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
                 if (!wait_w<false>(bar + kBarQFull, nu & 1, abort_flag, hdr, kSiteQFull))
                     break;
                 ++nu;
-                auto issue_s = [&](int j) -> bool {
-                    const int ci = chunk + (j >> w.pairs), st = ci % L::kStages, g = j & 1, b = ns[g] & 1;
-                    if (!wait_w<false>(bar + kBarKvFull + 8u * st, (ci / L::kStages) & 1, abort_flag, hdr, kSiteKvFull))
+                // (the groups' loops are written out: their counters stay in registers)
+                auto issue_s = [&](int j, auto group) -> bool {
+                    constexpr int g = decltype(group)::value;
+                    const uint32_t b = s_n[g]++ & 1;
+                    if (!wait_w<false>(bar + kBarKvFull + 8u * s_st, s_ph, abort_flag, hdr, kSiteKvFull))
                         return false;
                     tc_fence_after();
-                    const uint32_t kb = sb + L::kOffK + (uint32_t)st * L::kKvStage;
-                    const uint32_t qb = sb + (w.pairs && g ? L::kOffQ2 : L::kOffQ);
-                    for (int kk = 0; kk < ks; ++kk)
-                        mma_ss_w(tmem + 128u * g + 64u * b, desc_sw128(qb + (kk >> 2) * L::kQAtom) + 2u * (kk & 3),
-                                 desc_sw128(kb + (kk >> 2) * L::kKvAtom) + 2u * (kk & 3), id_s, kk > 0);
+                    const uint32_t d = tmem + 128u * g + 64u * b;
+                    const uint64_t ad = g ? q2d : qd, bd = kd + (uint64_t)((uint32_t)s_st * (L::kKvStage >> 4));
+                    mma_s_w(d, ad, bd, id_s, 0, ks0);
+                    if (KD > 64 && ks1 > 0)
+                        mma_s_w(d, ad + (L::kQAtom >> 4), bd + (L::kKvAtom >> 4), id_s, 1, ks1);
                     tc_commit_w(bar + kBarSFull + 16u * g + 8u * b);
-                    ++ns[g];
                     if (j + 1 == jobs)
                         tc_commit_w(bar + kBarQEmpty);
+                    if (!w.pairs || g == 1) {
+                        if (++s_st == L::kStages) {
+                            s_st = 0;
+                            s_ph ^= 1;
+                        }
+                    }
                     return true;
                 };
-                for (int j = 0; ok && j < min(L::kAhead, jobs); ++j)
-                    ok = issue_s(j);
-                for (int j = 0; ok && j < jobs; ++j) {
-                    const int g = j & 1, b = np[g] & 1;
-                    if (!wait_w<false>(bar + kBarPFull + 16u * g + 8u * b, (np[g] >> 1) & 1, abort_flag, hdr, kSitePFull)) {
-                        ok = false;
-                        break;
-                    }
+                auto issue_pv = [&](int j, auto group) -> bool {
+                    constexpr int g = decltype(group)::value;
+                    const uint32_t n = p_n[g]++, b = n & 1;
+                    if (!wait_w<false>(bar + kBarPFull + 16u * g + 8u * b, (n >> 1) & 1, abort_flag, hdr, kSitePFull))
+                        return false;
                     tc_fence_after();
-                    const int st = (chunk + (j >> w.pairs)) % L::kStages;
-                    const uint32_t vb = sb + L::kOffK + (uint32_t)st * L::kKvStage + L::kAtoms * L::kKvAtom;
                     const uint32_t d = tmem + kTmemO + 128u * g, pa = tmem + 128u * g + 64u * b;
-                    for (int kk = 0; kk < kKeys / 16; ++kk)
-                        mma_ts_w(d, pa + 8u * kk, desc_sw128(vb + kk * 2048), id_o0, j > 1 || kk > 0);
-                    if (dv1 > 0)
-                        for (int kk = 0; kk < kKeys / 16; ++kk)
-                            mma_ts_w(d + 64u, pa + 8u * kk, desc_sw128(vb + L::kKvAtom + kk * 2048), id_o1, j > 1 || kk > 0);
+                    const uint64_t bd = vd + (uint64_t)((uint32_t)v_st * (L::kKvStage >> 4));
+                    mma_pv_w(d, pa, bd, id_o0, j > 1);
+                    if (KD > 64 && dv1 > 0)
+                        mma_pv_w(d + 64u, pa, bd + (L::kKvAtom >> 4), id_o1, j > 1);
                     tc_commit_w(bar + kBarPvDone + 8u * g);
-                    if (!w.pairs || g == 1)
-                        tc_commit_w(bar + kBarKvEmpty + 8u * st);
-                    ++np[g];
-                    if (j + L::kAhead < jobs)
-                        ok = issue_s(j + L::kAhead);
+                    if (!w.pairs || g == 1) {
+                        tc_commit_w(bar + kBarKvEmpty + 8u * v_st);
+                        if (++v_st == L::kStages)
+                            v_st = 0;
+                    }
+                    return true;
+                };
+                using G0 = std::integral_constant<int, 0>;
+                using G1 = std::integral_constant<int, 1>;
+                for (int j = 0; ok && j < min(L::kAhead, jobs); j += 2) {
+                    ok = issue_s(j, G0());
+                    if (ok && j + 1 < jobs)
+                        ok = issue_s(j + 1, G1());
                 }
-                chunk += x.c_hi - x.c_lo;
+                for (int j = 0; ok && j < jobs; j += 2) {
+                    ok = issue_pv(j, G0()) && (j + L::kAhead >= jobs || issue_s(j + L::kAhead, G0()));
+                    if (ok && j + 1 < jobs)
+                        ok = issue_pv(j + 1, G1()) && (j + 1 + L::kAhead >= jobs || issue_s(j + 1 + L::kAhead, G1()));
+                }
             }
             if (!ok) {
                 // the products in flight finish before this CTA's memory is given up
