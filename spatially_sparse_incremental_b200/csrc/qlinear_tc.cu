@@ -43,7 +43,7 @@ constexpr int kCluster = 4;
 constexpr int kMaxStages = 9;
 
 constexpr uint32_t kRing = 196608;       // 4 stages of 128 + 256 rows, more of narrower ones
-constexpr uint32_t kOffRecv = kRing;     // sums pushed by the other CTAs of a split unit
+constexpr uint32_t kOffRecv = kRing;     // sums pushed by the other CTAs of a split unit, or the output tiles of the warps
 constexpr uint32_t kRecvBytes = (kCluster - 1) * kRows * (kSplitBn / kCluster) * 4;
 constexpr uint32_t kOffCol = kOffRecv + kRecvBytes;          // per accumulator: column scales and biases
 constexpr uint32_t kOffTok = kOffCol + 2 * 2 * kMaxBn * 4;   // swapped units: the columns' pixels
@@ -57,6 +57,7 @@ constexpr uint32_t kBarDrain = kBarRecv + 8;
 constexpr uint32_t kTmemSlot = kBarDrain + 8;
 constexpr uint32_t kAbort = kTmemSlot + 4;
 constexpr uint32_t kSmem = kOffBar + 256 + 1024;             // + alignment slack
+static_assert(kEpiWarps * 2048 <= kRecvBytes, "output tiles");
 static_assert(kAbort + 4 <= 256, "barrier block");
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
@@ -176,12 +177,10 @@ __device__ __forceinline__ void put1(const QLinearParams &p, int64_t e, float v)
     }
 }
 
-// 16 sums of one token from column c on: scales and biases from shared memory
-// (col: 16-byte rows of kMaxBn scales, then kMaxBn biases).
-__device__ __forceinline__ void finish16(const Args &a, const int (&acc)[16], uint32_t col, float sa, int64_t pix, int c)
+// 16 sums of one token, scaled and biased: scales and biases from shared
+// memory (col: kMaxBn scales, then kMaxBn biases).
+__device__ __forceinline__ void scale16(const int *acc, uint32_t col, float sa, float *v)
 {
-    const QLinearParams &p = a.q;
-    float v[16];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const float4 s = lds_f32x4(col + 16u * q), b = lds_f32x4(col + 4u * kMaxBn + 16u * q);
@@ -190,43 +189,78 @@ __device__ __forceinline__ void finish16(const Args &a, const int (&acc)[16], ui
         v[4 * q + 2] = qlinear_value(acc[4 * q + 2], sa, s.z) + b.z;
         v[4 * q + 3] = qlinear_value(acc[4 * q + 3], sa, s.w) + b.w;
     }
-    const int64_t e = pix * p.Co + c;
-    if (!a.vec || c + 16 > p.Co) {
+}
+
+__device__ __forceinline__ void sts_u4(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 lds_u4(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// The outputs of a warp's 32 tokens (pix: this lane's, negative: none) over the
+// 64 bytes of columns from c on (32 bf16 or 16 float32), v being this lane's
+// token's.  A thread's own row would leave as 16-byte pieces of 32 different
+// lines an instruction; through `tile` (2 KB of shared memory of the warp) four
+// lanes store the 64 bytes of a row together, and read the residual so.  The
+// 16-byte pieces of row r lie at piece ^ ((r / 2) mod 4): no bank conflicts
+// either way.
+template <int kE>   // bytes of an output element
+__device__ __forceinline__ void put64(const QLinearParams &p, float *v, int64_t pix, int c, uint32_t tile, int lane)
+{
+    const uint32_t own = tile + 64u * lane, sw = (uint32_t)(lane >> 1) & 3u;
+    if (p.residual) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-            if (c + k < p.Co)
-                put1(p, e + k, v[k]);
-        return;
-    }
-    if (p.dtype == SIGE_BF16) {
+        for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2), k = lane & 3;
+            const int64_t px = __shfl_sync(0xFFFFFFFFu, pix, r);
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (px >= 0)
+                x = ld_nc16(p.residual + (px * p.Co + c) * kE + 16 * k);
+            sts_u4(tile + 64u * r + (((uint32_t)k ^ ((uint32_t)(r >> 1) & 3u)) << 4), x);
+        }
+        __syncwarp();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (p.residual) {
-                const uint4 r = ld_nc16(p.residual + e * 2 + 16 * h);
-                const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+        for (int k = 0; k < 4; ++k) {
+            const uint4 x = lds_u4(own + (((uint32_t)k ^ sw) << 4));
+            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    v[8 * h + 2 * k] += bf16_lo(w[k]);
-                    v[8 * h + 2 * k + 1] += bf16_hi(w[k]);
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (kE == 2) {
+                    v[8 * k + 2 * e] += bf16_lo(u[e]);
+                    v[8 * k + 2 * e + 1] += bf16_hi(u[e]);
+                } else {
+                    v[4 * k + e] += __uint_as_float(u[e]);
                 }
             }
-            const float *u = v + 8 * h;
-            *reinterpret_cast<uint4 *>(p.y + e * 2 + 16 * h) =
-                make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(u[4], u[5]), pack_bf16x2(u[6], u[7]));
-        }
-    } else {
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            if (p.residual) {
-                const uint4 r = ld_nc16(p.residual + e * 4 + 16 * h);
-                v[4 * h] += __uint_as_float(r.x);
-                v[4 * h + 1] += __uint_as_float(r.y);
-                v[4 * h + 2] += __uint_as_float(r.z);
-                v[4 * h + 3] += __uint_as_float(r.w);
-            }
-            *reinterpret_cast<float4 *>(p.y + e * 4 + 16 * h) = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
         }
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint4 x;
+        if constexpr (kE == 2) {
+            const float *u = v + 8 * k;
+            x = make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(u[4], u[5]), pack_bf16x2(u[6], u[7]));
+        } else {
+            x = make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]),
+                           __float_as_uint(v[4 * k + 3]));
+        }
+        sts_u4(own + (((uint32_t)k ^ sw) << 4), x);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2), k = lane & 3;
+        const int64_t px = __shfl_sync(0xFFFFFFFFu, pix, r);
+        const uint4 x = lds_u4(tile + 64u * r + (((uint32_t)k ^ ((uint32_t)(r >> 1) & 3u)) << 4));
+        if (px >= 0)
+            *reinterpret_cast<uint4 *>(p.y + (px * p.Co + c) * kE + 16 * k) = x;
+    }
+    __syncwarp();
 }
 
 } // namespace qt
@@ -398,6 +432,7 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
         const int r = (warp & 3) * 32 + lane;              // row of the unit = tensor-memory lane
         const int half = (warp - 2) >> 2;
         const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t tile = sb + kOffRecv + (uint32_t)(warp - 2) * 2048u;   // (a split unit receives there instead)
         int nu = 0;
         bool ok = true;
         for (uint32_t u = u_first; u < plan.units; u += u_step, ++nu) {
@@ -474,7 +509,22 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                     continue;
                 }
             }
-            for (int g = 16 * half; g < cw; g += 32) {
+            int g0 = 0;   // columns finished in groups of 32
+            if (split_n == 1 && !plan.swap && args.vec && p.dtype == SIGE_BF16) {
+                for (; g0 + 32 <= cw && cb * plan.bn + g0 + 32 <= p.Co; g0 += 32) {
+                    if (((g0 >> 5) & 1) != half)
+                        continue;
+                    int acc[2][16];
+                    ld_cols(t_acc + (uint32_t)g0, acc[0]);
+                    ld_cols(t_acc + (uint32_t)g0 + 16u, acc[1]);
+                    ld_done();
+                    float v[32];
+                    scale16(acc[0], col + 4u * (uint32_t)g0, rs, v);
+                    scale16(acc[1], col + 4u * (uint32_t)(g0 + 16), rs, v + 16);
+                    put64<2>(p, v, pix, cb * plan.bn + g0, tile, lane);
+                }
+            }
+            for (int g = g0 + 16 * half; g < cw; g += 32) {
                 int acc[16];
                 ld_cols(t_acc + (uint32_t)(col0 + g), acc);
                 ld_done();
@@ -498,8 +548,19 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                                 put1(p, (int64_t)t * p.Co + chan, qlinear_value(acc[k], colp[col0 + g + k], rs) + rbias);
                         }
                     }
-                } else if (pix >= 0) {
-                    finish16(args, acc, col + 4u * (uint32_t)(col0 + g), rs, pix, cb * plan.bn + col0 + g);
+                } else {
+                    // (a part of 16 columns, or a row's ragged or unaligned end)
+                    const int c = cb * plan.bn + col0 + g;
+                    float v[16];
+                    scale16(acc, col + 4u * (uint32_t)(col0 + g), rs, v);
+                    if (split_n == 1 && args.vec && p.dtype == SIGE_F32 && c + 16 <= p.Co) {
+                        put64<4>(p, v, pix, c, tile, lane);
+                    } else if (pix >= 0) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            if (c + k < p.Co)
+                                put1(p, pix * p.Co + c + k, v[k]);
+                    }
                 }
             }
             tc_fence_before();
