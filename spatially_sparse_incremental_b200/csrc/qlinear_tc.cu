@@ -13,8 +13,9 @@
 // the device knows for a tile list, so every CTA derives them at its start.
 //   * warp 0 loads the operands by TMA into a ring of stages, 128-byte rows
 //     with the 128-byte swizzle (the K-major operands of the MMA): weights and
-//     whole maps by boxes, the tokens of a tile list by tile::gather4, four
-//     rows an instruction and lane, straight from the cache;
+//     whole maps by boxes of rows, the tokens of a tile list straight from the
+//     cache, a 4 x 4 or 8 x 8 tile a box or (other tiles) four tokens a
+//     tile::gather4, one copy a lane;
 //   * warp 1 issues the MMAs into one of two accumulators of up to 256
 //     columns, so that the next unit's products run under this one's epilogue;
 //   * warps 2 .. 9 (two warps to each quarter of the tensor memory's lanes,
@@ -108,11 +109,32 @@ __device__ __forceinline__ uint32_t idesc_s8(int n)
     return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_s8_w(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+// The `steps` (1 .. 4) products of a stage, 32 channels each (32 bytes along the
+// swizzled rows), and the commit that releases the stage, from one elected lane
+// of the converged warp.
+__device__ __forceinline__ void mma_s8_commit_w(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                                int steps, uint32_t bar)
 {
-    asm volatile("{\n .reg .pred p, e;\n .reg .b32 l;\n elect.sync l|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-                 " @e tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+    asm volatile(
+        "{\n .reg .pred p, e, t, e1, e2, e3;\n .reg .b32 l;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"
+        " elect.sync l|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
+        " setp.gt.and.s32 e1, %5, 1, e;\n setp.gt.and.s32 e2, %5, 2, e;\n setp.gt.and.s32 e3, %5, 3, e;\n"
+        " add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"
+        " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
+        " @e tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n"
+        " @e1 tcgen05.mma.cta_group::1.kind::i8 [%0], a1, b1, %3, t;\n"
+        " @e2 tcgen05.mma.cta_group::1.kind::i8 [%0], a2, b2, %3, t;\n"
+        " @e3 tcgen05.mma.cta_group::1.kind::i8 [%0], a3, b3, %3, t;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(steps), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2, int c3)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
                  : "memory");
 }
 
@@ -161,6 +183,7 @@ __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n
 struct Args {
     QLinearParams q;
     int vec;       // y and the residual take 16-byte accesses of whole groups of columns
+    int tile_rows; // tokens of a tile that one box copies, 0: four tokens a copy
 };
 
 // One output element.
@@ -269,7 +292,7 @@ using namespace qt;
 
 __global__ void __launch_bounds__(qt::kThreads, 1)
     k_qlinear_tc(const __grid_constant__ qt::Args args, const __grid_constant__ CUtensorMap tw,
-                 const __grid_constant__ CUtensorMap tbox, const __grid_constant__ CUtensorMap trow)
+                 const __grid_constant__ CUtensorMap tw32, const __grid_constant__ CUtensorMap tbox)
 {
     extern __shared__ __align__(1024) uint8_t qt_raw[];
     const QLinearParams &p = args.q;
@@ -297,7 +320,8 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
     }
     if (warp == 0 && lane == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tw)) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(p.px.idx ? &trow : &tbox)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tw32)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tbox)) : "memory");
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(bar + kTmemSlot),
@@ -330,22 +354,52 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
     const uint32_t stage_bytes = (uint32_t)(kRows + plan.bn) * kChunk;
     if (warp == 0) {
         // ---- operands
+        const bool lists = p.px.idx != nullptr;
+        const bool box = !plan.swap && !lists;      // 128 tokens in a row
+        const bool tiles = lists && args.tile_rows; // whole tiles by boxes
+        // weight rows by boxes of 128 or 32, one a lane
+        const int wrows = plan.swap ? kRows : plan.bn;
+        const bool wide = wrows >= kRows;
+        const int nw = wide ? wrows / kRows : wrows / 32;
+        const CUtensorMap *wmap = wide ? &tw : &tw32;
+        const uint32_t woff = (plan.swap ? 0u : (uint32_t)(kRows * kChunk)) + (uint32_t)(lane * (wide ? kRows : 32)) * kChunk;
+        const uint32_t toff = plan.swap ? (uint32_t)(kRows * kChunk) : 0u;
+        const int per_copy = box ? kRows : tiles ? args.tile_rows : 4;   // tokens a copy, one copy a lane
+        const uint32_t tdst0 = toff + (uint32_t)(lane * (tiles ? args.tile_rows : 4)) * kChunk;
         int it = 0, st = 0;
         uint32_t ph = 1;
         bool ok = true;
         for (uint32_t u = u_first; ok && u < plan.units; u += u_step) {
             const uint32_t rb = u / plan.cblocks;
             const int cb = (int)(u - rb * plan.cblocks);
-            // this lane's four tokens of the unit (a padding slot reads row 0,
-            // and its products are not written)
-            int rows[4] = {0, 0, 0, 0};
-            const bool box = !plan.swap && !p.px.idx;
-            if (!box) {
+            const int wrow = (plan.swap ? (int)rb * kRows : cb * plan.bn) + lane * (wide ? kRows : 32);
+            // the copies that hold a token: what lies in the other rows of a stage
+            // enters only products that are not written
+            const uint32_t left = plan.slots - (plan.swap ? 0 : rb * kRows);
+            const int nt = box ? 1 : (int)((min(left, (uint32_t)kRows) + per_copy - 1) / per_copy);
+            const uint32_t bytes = (uint32_t)(wrows + nt * per_copy) * kChunk;
+            // this lane's four tokens of the unit, or its tile (a clipped slot
+            // reads the first token's row or tile)
+            int t0 = 0, t1 = 0, t2 = 0, t3 = 0;
+            if (tiles) {
+                const uint32_t s0 = (plan.swap ? 0 : rb * kRows) + (uint32_t)(lane * args.tile_rows);
+                if (lane < nt) {
+                    const int64_t px = pixel_of(p.px, s0);
+                    if (px >= 0) {
+                        const uint32_t tn = udiv(s0, p.px.dbb), t = udiv(tn, p.px.dN);
+                        const int2 org = __ldg(reinterpret_cast<const int2 *>(p.px.idx) + t);
+                        t0 = org.y;
+                        t1 = org.x;
+                        t2 = (int)(tn - t * (uint32_t)p.px.N);
+                    }
+                }
+            } else if (!box) {
                 const uint32_t s0 = (plan.swap ? 0 : rb * kRows) + 4 * lane;
+                int rows[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (s0 + k < plan.slots)
-                        rows[k] = (int)max((int64_t)0, pixel_of(p.px, s0 + k));
+                    rows[k] = s0 + k < plan.slots ? (int)max((int64_t)0, pixel_of(p.px, s0 + k)) : 0;
+                t0 = rows[0]; t1 = rows[1]; t2 = rows[2]; t3 = rows[3];
             }
             for (int c = c_lo; c < c_hi; ++c, ++it) {
                 if (it >= plan.stages && !mbar_wait_w(bar + kBarEmpty + 8u * st, ph, abort_flag, hdr, kSiteEmpty)) {
@@ -353,21 +407,20 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                     break;
                 }
                 const uint32_t full = bar + kBarFull + 8u * st;
-                const uint32_t rdst = sb + (uint32_t)st * stage_bytes, cdst = rdst + kRows * kChunk;
-                const uint32_t tdst = plan.swap ? cdst : rdst, wdst = plan.swap ? rdst : cdst;
-                const int wrows = plan.swap ? kRows : plan.bn;
-                const int w0 = plan.swap ? (int)rb * kRows : cb * plan.bn;
-                if (lane == 0) {
-                    mbar_expect_tx(full, stage_bytes);
-                    for (int i = 0; i < wrows; i += 32)
-                        tma_load_2d(wdst + (uint32_t)i * kChunk, &tw, full, c * kChunk, w0 + i);
-                    if (box)
-                        tma_load_2d(tdst, &tbox, full, c * kChunk, (int)rb * kRows);
-                }
+                const uint32_t dst = sb + (uint32_t)st * stage_bytes;
+                if (lane == 0)
+                    mbar_expect_tx(full, bytes);
                 __syncwarp();
-                if (!box && 4 * lane < (plan.swap ? plan.bn : kRows))
-                    tma_gather4(tdst + (uint32_t)lane * 4 * kChunk, &trow, full, c * kChunk, rows[0], rows[1], rows[2],
-                                rows[3]);
+                if (lane < nw)
+                    tma_load_2d(dst + woff, wmap, full, c * kChunk, wrow);
+                if (lane < nt) {
+                    if (box)
+                        tma_load_2d(dst, &tbox, full, c * kChunk, (int)rb * kRows);
+                    else if (tiles)
+                        tma_load_4d(dst + tdst0, &tbox, full, c * kChunk, t0, t1, t2);
+                    else
+                        tma_gather4(dst + tdst0, &tbox, full, c * kChunk, t0, t1, t2, t3);
+                }
                 __syncwarp();
                 if (++st == plan.stages) {
                     st = 0;
@@ -388,6 +441,8 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
     } else if (warp == 1) {
         // ---- products
         const uint32_t id = idesc_s8(plan.bn);
+        const uint64_t ring = desc_sw128(sb);
+        const int last_steps = (p.C - (plan.nch - 1) * kChunk + 31) / 32;   // of the last chunk's 32-channel steps
         int st = 0, nu = 0;
         uint32_t ph = 0;
         bool ok = true;
@@ -405,12 +460,9 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                const uint64_t ad = desc_sw128(sb + (uint32_t)st * stage_bytes);
-                const uint64_t bd = desc_sw128(sb + (uint32_t)st * stage_bytes + kRows * kChunk);
-                const int left = p.C - c * kChunk, steps = left >= kChunk ? 4 : (left + 31) / 32;
-                for (int k = 0; k < steps; ++k)
-                    mma_s8_w(d, ad + 2u * k, bd + 2u * k, id, c > c_lo || k > 0);
-                tc_commit_w(bar + kBarEmpty + 8u * st);
+                const uint64_t ad = ring + (uint64_t)((uint32_t)st * (stage_bytes >> 4));
+                mma_s8_commit_w(d, ad, ad + ((kRows * kChunk) >> 4), id, c > c_lo,
+                                c + 1 < plan.nch ? 4 : last_steps, bar + kBarEmpty + 8u * st);
                 if (++st == plan.stages) {
                     st = 0;
                     ph ^= 1;
@@ -584,6 +636,7 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
 
 // ------------------------------------------------------------------ host
 
+// 128-byte columns of a matrix of `rows` rows of C codes, box_rows rows a copy.
 static bool encode_rows(CUtensorMap *map, const void *base, int64_t rows, int C, int box_rows, CUtensorMapL2promotion l2,
                         PFN_cuTensorMapEncodeTiled_v12000 encode)
 {
@@ -593,6 +646,19 @@ static bool encode_rows(CUtensorMap *map, const void *base, int64_t rows, int C,
     cuuint32_t es[2] = {1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, l2,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The token map [N][H][W][C], one b x b tile a copy (zeros outside the map).
+static bool encode_tiles(CUtensorMap *map, const QLinearParams &p, PFN_cuTensorMapEncodeTiled_v12000 encode)
+{
+    const cuuint64_t C = (cuuint64_t)p.C, W = (cuuint64_t)p.px.W, H = (cuuint64_t)p.px.H;
+    cuuint64_t dims[4] = {C, W, H, (cuuint64_t)p.px.N};
+    cuuint64_t strides[3] = {C, C * W, C * W * H};
+    cuuint32_t box[4] = {(cuuint32_t)qt::kChunk, (cuuint32_t)p.px.b, (cuuint32_t)p.px.b, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t *>(p.a), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -608,10 +674,25 @@ int launch_qlinear_tc(const QLinearParams &p, cudaStream_t stream)
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
         return SIGE_ERR_CUDA;
-    CUtensorMap tw, tbox, trow;
-    if (!encode || !encode_rows(&tw, p.w, p.Co, p.C, 32, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, encode) ||
-        !encode_rows(&tbox, p.a, p.rows, p.C, qt::kRows, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, encode) ||
-        !encode_rows(&trow, p.a, p.rows, p.C, 1, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, encode))
+    if (!encode)
+        return SIGE_ERR_CUDA;
+    // how the tokens are copied: 128 in a row for a whole map; tiles of 4 x 4 or
+    // 8 x 8 (a divisor of 128 tokens, whole 1 KB swizzle atoms) by boxes, which
+    // took 8.4 -> %s us off ...; four tokens a copy otherwise
+    qt::Args a{};
+    CUtensorMap tw, tw32, tbox;
+    bool good = encode_rows(&tw, p.w, p.Co, p.C, qt::kRows, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, encode) &&
+                encode_rows(&tw32, p.w, p.Co, p.C, 32, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, encode);
+    if (p.px.idx && (p.px.b == 4 || p.px.b == 8)) {
+        a.tile_rows = p.px.b * p.px.b;
+        good = good && encode_tiles(&tbox, p, encode);
+    } else {
+        // (the few tokens of a swapped unit are gathered from a whole map, too)
+        const bool rows128 = !p.px.idx && p.slots > qt::kSwapTokens;
+        good = good && encode_rows(&tbox, p.a, p.rows, p.C, rows128 ? qt::kRows : 1,
+                                   rows128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B, encode);
+    }
+    if (!good)
         return SIGE_ERR_CUDA;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -643,7 +724,6 @@ int launch_qlinear_tc(const QLinearParams &p, cudaStream_t stream)
         clusters_of[dev].store(ncl, std::memory_order_release);
     }
     prefer_max_shared(k_qlinear_tc);
-    qt::Args a{};
     a.q = p;
     const int esz = p.dtype == SIGE_BF16 ? 2 : 4;
     a.vec = (int64_t)p.Co * esz % 16 == 0 && aligned_to(p.y, 16) && aligned_to(p.residual, 16);
@@ -659,7 +739,7 @@ int launch_qlinear_tc(const QLinearParams &p, cudaStream_t stream)
         // no more clusters than the narrowest units of a full list can use
         cfg.gridDim = dim3((unsigned)(qt::kCluster * std::max<int64_t>(1, std::min<int64_t>(ncl, narrowest))));
     }
-    if (cudaLaunchKernelEx(&cfg, k_qlinear_tc, a, tw, tbox, trow) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, k_qlinear_tc, a, tw, tw32, tbox) != cudaSuccess) {
         cudaGetLastError();
         return SIGE_ERR_CUDA;
     }
