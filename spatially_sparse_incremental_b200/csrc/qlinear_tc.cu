@@ -44,7 +44,7 @@ constexpr int kCluster = 4;
 constexpr int kMaxStages = 9;
 
 constexpr uint32_t kRing = 196608;       // 4 stages of 128 + 256 rows, more of narrower ones
-constexpr uint32_t kOffRecv = kRing;     // sums pushed by the other CTAs of a split unit, or the output tiles of the warps
+constexpr uint32_t kOffRecv = kRing;     // sums pushed by the other CTAs of a split unit
 constexpr uint32_t kRecvBytes = (kCluster - 1) * kRows * (kSplitBn / kCluster) * 4;
 constexpr uint32_t kOffCol = kOffRecv + kRecvBytes;          // per accumulator: column scales and biases
 constexpr uint32_t kOffTok = kOffCol + 2 * 2 * kMaxBn * 4;   // swapped units: the columns' pixels
@@ -58,7 +58,6 @@ constexpr uint32_t kBarDrain = kBarRecv + 8;
 constexpr uint32_t kTmemSlot = kBarDrain + 8;
 constexpr uint32_t kAbort = kTmemSlot + 4;
 constexpr uint32_t kSmem = kOffBar + 256 + 1024;             // + alignment slack
-static_assert(kEpiWarps * 2048 <= kRecvBytes, "output tiles");
 static_assert(kAbort + 4 <= 256, "barrier block");
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
@@ -70,7 +69,40 @@ struct Plan {
     uint32_t slots, rblocks, cblocks, units;
 };
 
+__host__ __device__ inline int least(int a, int b) { return a < b ? a : b; }
+
+// How a product of many tokens is cut: candidate i < 8 is units of 32 (i + 1)
+// columns, then 64 columns with K split 2 and 4 ways and 32 columns split 2
+// ways (16 columns or more for each CTA to finish).
+constexpr int kCuts = 11;
+__host__ __device__ inline void cut_at(int i, int *bn, int *split)
+{
+    *bn = i < 8 ? 32 * (i + 1) : i == 10 ? 32 : 64;
+    *split = i < 8 ? 1 : i == 9 ? 4 : 2;
+}
+
+// Estimated cycles of a cut: rounds of units, each the longer of its chunks
+// (the operands' way into shared memory at about 60 bytes a cycle measured
+// longer than the products, 2 bn cycles; 250 for the issue of a small one) and
+// its outputs (about 12 cycles a column); a fill and a drain; the exchange of a
+// split.  0xFFFFFFFF: not possible.
+__host__ __device__ inline uint32_t cut_cost(int i, uint32_t rblocks, int Co, int nch, int grid, int cluster)
+{
+    int bn, split;
+    cut_at(i, &bn, &split);
+    const uint32_t units = rblocks * (((uint32_t)Co + bn - 1) / bn);
+    if (split > cluster || (split > 1 && (units * (uint32_t)split > (uint32_t)grid || nch < 2 * split)))
+        return 0xFFFFFFFFu;
+    const uint32_t rounds = (units * (uint32_t)split + grid - 1) / grid;
+    uint32_t chunk = (uint32_t)(kRows + bn) * 2u + (uint32_t)(kRows + bn) / 8u;
+    chunk = chunk < 250u ? 250u : chunk;
+    const uint32_t mul = (uint32_t)((nch + split - 1) / split) * chunk, out = 12u * (uint32_t)bn;
+    const float c = (float)rounds * (float)(mul > out ? mul : out) + (float)(1000u + out / split + (split > 1 ? 2500u : 0u));
+    return c < 2e9f ? (uint32_t)c : 2000000000u;
+}
+
 // The launch's work for `slots` tokens on `grid` CTAs in clusters of `cluster`.
+// On the device the whole warp calls it: a lane prices each cut.
 __host__ __device__ inline Plan make_plan(uint32_t slots, int Co, int C, int grid, int cluster)
 {
     Plan q;
@@ -79,24 +111,31 @@ __host__ __device__ inline Plan make_plan(uint32_t slots, int Co, int C, int gri
     q.swap = slots <= kSwapTokens;
     if (q.swap) {
         // wide enough that every CTA of a split unit finishes 16 columns
-        const int least = cluster < 4 || q.nch < 4 ? 16 : q.nch < 8 ? 32 : 64;
+        const int wide = cluster < 4 || q.nch < 4 ? 16 : q.nch < 8 ? 32 : 64;
         q.bn = slots > 48 ? 64 : slots > 32 ? 48 : slots > 16 ? 32 : 16;
-        q.bn = q.bn > least ? q.bn : least;
+        q.bn = q.bn > wide ? q.bn : wide;
         q.rblocks = ((uint32_t)Co + kRows - 1) / kRows;
         q.cblocks = slots > 0;
+        q.units = q.rblocks * q.cblocks;
+        q.split = cluster;
+        while (q.split > 1 && (q.units * (uint32_t)q.split > (uint32_t)grid || q.nch < 2 * q.split || q.bn % (16 * q.split)))
+            q.split >>= 1;
     } else {
-        // the widest unit (fewest operand reads) that still gives every CTA one
         q.rblocks = (slots + kRows - 1) / kRows;
-        int sh = 8;
-        while (sh > 5 && (q.rblocks * (((uint32_t)Co + (1u << sh) - 1) >> sh) < (uint32_t)grid || (1 << (sh - 1)) >= Co))
-            --sh;
-        q.bn = 1 << sh;
-        q.cblocks = ((uint32_t)Co + (1u << sh) - 1) >> sh;
+#ifdef __CUDA_ARCH__
+        const int lane = (int)(threadIdx.x & 31);
+        const uint32_t mine = cut_cost(least(lane, kCuts - 1), q.rblocks, Co, q.nch, grid, cluster);
+        const int best = __ffs(__ballot_sync(0xFFFFFFFFu, mine == __reduce_min_sync(0xFFFFFFFFu, mine))) - 1;
+#else
+        int best = 0;
+        for (int i = 1; i < kCuts; ++i)
+            if (cut_cost(i, q.rblocks, Co, q.nch, grid, cluster) < cut_cost(best, q.rblocks, Co, q.nch, grid, cluster))
+                best = i;
+#endif
+        cut_at(best, &q.bn, &q.split);
+        q.cblocks = ((uint32_t)Co + q.bn - 1) / q.bn;
+        q.units = q.rblocks * q.cblocks;
     }
-    q.units = q.rblocks * q.cblocks;
-    q.split = q.bn <= kSplitBn ? cluster : 1;
-    while (q.split > 1 && (q.units * (uint32_t)q.split > (uint32_t)grid || q.nch < 2 * q.split || q.bn % (16 * q.split)))
-        q.split >>= 1;
     q.stages = q.bn > 128 ? 4 : q.bn > 64 ? 6 : q.bn > 32 ? 8 : 9;
     return q;
 }
@@ -127,6 +166,22 @@ __device__ __forceinline__ void mma_s8_commit_w(uint32_t d, uint64_t a, uint64_t
         " @e3 tcgen05.mma.cta_group::1.kind::i8 [%0], a3, b3, %3, t;\n"
         " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n}\n" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(steps), "r"(bar)
+        : "memory");
+}
+
+// A whole stage from two boxes (128 bytes of K from byte x on, rows ya and yb)
+// and the bytes its barrier waits for, from one elected lane of the converged
+// warp.
+__device__ __forceinline__ void tma_stage_w(uint32_t da, const CUtensorMap *ma, int ya, uint32_t db, const CUtensorMap *mb,
+                                            int yb, uint32_t bar, uint32_t bytes, int x)
+{
+    asm volatile(
+        "{\n .reg .pred e;\n .reg .b32 l;\n elect.sync l|e, 0xffffffff;\n"
+        " @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%6], %7;\n"
+        " @e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%8, %2}], [%6];\n"
+        " @e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%3], [%4, {%8, %5}], [%6];\n}\n"
+        ::"r"(da), "l"(reinterpret_cast<uint64_t>(ma)), "r"(ya), "r"(db), "l"(reinterpret_cast<uint64_t>(mb)), "r"(yb),
+        "r"(bar), "r"(bytes), "r"(x)
         : "memory");
 }
 
@@ -182,8 +237,9 @@ __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n
 
 struct Args {
     QLinearParams q;
-    int vec;       // y and the residual take 16-byte accesses of whole groups of columns
+    int vec;       // y and the residual take 32-byte accesses of 16 columns
     int tile_rows; // tokens of a tile that one box copies, 0: four tokens a copy
+    Plan plan;     // of a whole map (a list's is made on the device)
 };
 
 // One output element.
@@ -214,76 +270,68 @@ __device__ __forceinline__ void scale16(const int *acc, uint32_t col, float sa, 
     }
 }
 
-__device__ __forceinline__ void sts_u4(uint32_t addr, uint4 v)
+// 32 bytes (a whole memory sector).
+__device__ __forceinline__ void st_v8(void *dst, const uint32_t *v)
 {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
-__device__ __forceinline__ uint4 lds_u4(uint32_t addr)
+__device__ __forceinline__ void ld_v8(const void *src, uint32_t *v)
 {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-    return v;
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(src));
 }
 
-// The outputs of a warp's 32 tokens (pix: this lane's, negative: none) over the
-// 64 bytes of columns from c on (32 bf16 or 16 float32), v being this lane's
-// token's.  A thread's own row would leave as 16-byte pieces of 32 different
-// lines an instruction; through `tile` (2 KB of shared memory of the warp) four
-// lanes store the 64 bytes of a row together, and read the residual so.  The
-// 16-byte pieces of row r lie at piece ^ ((r / 2) mod 4): no bank conflicts
-// either way.
-template <int kE>   // bytes of an output element
-__device__ __forceinline__ void put64(const QLinearParams &p, float *v, int64_t pix, int c, uint32_t tile, int lane)
+// 16 outputs of one token (y and the residual at element e, 32-byte aligned
+// rows): a thread writes whole sectors of its own row.
+__device__ __forceinline__ void put16(const QLinearParams &p, int64_t e, float *v)
 {
-    const uint32_t own = tile + 64u * lane, sw = (uint32_t)(lane >> 1) & 3u;
-    if (p.residual) {
+    if (p.dtype == SIGE_BF16) {
+        uint32_t w[8];
+        if (p.residual) {
+            ld_v8(p.residual + e * 2, w);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 8 * i + (lane >> 2), k = lane & 3;
-            const int64_t px = __shfl_sync(0xFFFFFFFFu, pix, r);
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (px >= 0)
-                x = ld_nc16(p.residual + (px * p.Co + c) * kE + 16 * k);
-            sts_u4(tile + 64u * r + (((uint32_t)k ^ ((uint32_t)(r >> 1) & 3u)) << 4), x);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint4 x = lds_u4(own + (((uint32_t)k ^ sw) << 4));
-            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (kE == 2) {
-                    v[8 * k + 2 * e] += bf16_lo(u[e]);
-                    v[8 * k + 2 * e + 1] += bf16_hi(u[e]);
-                } else {
-                    v[4 * k + e] += __uint_as_float(u[e]);
-                }
+            for (int k = 0; k < 8; ++k) {
+                v[2 * k] += bf16_lo(w[k]);
+                v[2 * k + 1] += bf16_hi(w[k]);
             }
         }
-    }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        uint4 x;
-        if constexpr (kE == 2) {
-            const float *u = v + 8 * k;
-            x = make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(u[4], u[5]), pack_bf16x2(u[6], u[7]));
-        } else {
-            x = make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]),
-                           __float_as_uint(v[4 * k + 3]));
+        for (int k = 0; k < 8; ++k)
+            w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+        st_v8(p.y + e * 2, w);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t w[8];
+            if (p.residual) {
+                ld_v8(p.residual + e * 4 + 32 * h, w);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    v[8 * h + k] += __uint_as_float(w[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                w[k] = __float_as_uint(v[8 * h + k]);
+            st_v8(p.y + e * 4 + 32 * h, w);
         }
-        sts_u4(own + (((uint32_t)k ^ sw) << 4), x);
     }
-    __syncwarp();
+}
+
+// 16 columns from c on of one token (pix): put16 where whole sectors allow it.
+__device__ __forceinline__ void put_cols(const Args &a, float *v, int64_t pix, int c)
+{
+    const QLinearParams &p = a.q;
+    if (a.vec && c + 16 <= p.Co) {
+        put16(p, pix * p.Co + c, v);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + (lane >> 2), k = lane & 3;
-        const int64_t px = __shfl_sync(0xFFFFFFFFu, pix, r);
-        const uint4 x = lds_u4(tile + 64u * r + (((uint32_t)k ^ ((uint32_t)(r >> 1) & 3u)) << 4));
-        if (px >= 0)
-            *reinterpret_cast<uint4 *>(p.y + (px * p.Co + c) * kE + 16 * k) = x;
+        for (int k = 0; k < 16; ++k)
+            if (c + k < p.Co)
+                put1(p, pix * p.Co + c + k, v[k]);
     }
-    __syncwarp();
 }
 
 } // namespace qt
@@ -292,7 +340,8 @@ using namespace qt;
 
 __global__ void __launch_bounds__(qt::kThreads, 1)
     k_qlinear_tc(const __grid_constant__ qt::Args args, const __grid_constant__ CUtensorMap tw,
-                 const __grid_constant__ CUtensorMap tw32, const __grid_constant__ CUtensorMap tbox)
+                 const __grid_constant__ CUtensorMap tw64, const __grid_constant__ CUtensorMap tw32,
+                 const __grid_constant__ CUtensorMap tbox)
 {
     extern __shared__ __align__(1024) uint8_t qt_raw[];
     const QLinearParams &p = args.q;
@@ -320,7 +369,6 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
     }
     if (warp == 0 && lane == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tw)) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tw32)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tbox)) : "memory");
     }
     if (warp == 1) {
@@ -329,7 +377,7 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     pdl_wait();
-    const Plan plan = make_plan((uint32_t)pixel_slots(p.px), p.Co, p.C, (int)gridDim.x, (int)csize);
+    const Plan plan = p.px.idx ? make_plan((uint32_t)pixel_slots(p.px), p.Co, p.C, (int)gridDim.x, (int)csize) : args.plan;
     const int split_n = plan.split;
     const int per = (int)csize / split_n;                  // units a cluster takes at a time
     const int rank = csize > 1 ? (int)cluster_rank() : 0;
@@ -338,8 +386,8 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
     const uint32_t u_step = (gridDim.x / csize) * (uint32_t)per;
     const int c_lo = split * plan.nch / split_n, c_hi = (split + 1) * plan.nch / split_n;   // never empty
     if (threadIdx.x == 0) {
-        // rows pushed by the other CTAs of the unit (each by 128 threads a half)
-        mbar_init(bar + kBarRecv, (uint32_t)max(1, (split_n - 1) * kEpiThreads));
+        // pushed by the warps of the unit's other CTAs
+        mbar_init(bar + kBarRecv, (uint32_t)max(1, (split_n - 1) * kEpiWarps));
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     tc_fence_before();
@@ -355,46 +403,42 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
     if (warp == 0) {
         // ---- operands
         const bool lists = p.px.idx != nullptr;
-        const bool box = !plan.swap && !lists;      // 128 tokens in a row
-        const bool tiles = lists && args.tile_rows; // whole tiles by boxes
-        // weight rows by boxes of 128 or 32, one a lane
+        const bool tiles = lists && args.tile_rows;   // whole tiles by boxes
+        // weight rows: one box for a whole map; for a list (whose bn the host
+        // does not know) boxes of 128, 64 and 32, one a lane
         const int wrows = plan.swap ? kRows : plan.bn;
-        const bool wide = wrows >= kRows;
-        const int nw = wide ? wrows / kRows : wrows / 32;
-        const CUtensorMap *wmap = wide ? &tw : &tw32;
-        const uint32_t woff = (plan.swap ? 0u : (uint32_t)(kRows * kChunk)) + (uint32_t)(lane * (wide ? kRows : 32)) * kChunk;
-        const uint32_t toff = plan.swap ? (uint32_t)(kRows * kChunk) : 0u;
-        const int per_copy = box ? kRows : tiles ? args.tile_rows : 4;   // tokens a copy, one copy a lane
-        const uint32_t tdst0 = toff + (uint32_t)(lane * (tiles ? args.tile_rows : 4)) * kChunk;
+        const int n128 = wrows >> 7, n64 = (wrows >> 6) & 1, nw = n128 + n64 + ((wrows >> 5) & 1);
+        const CUtensorMap *wmap = lane < n128 ? &tw : lane < n128 + n64 ? &tw64 : &tw32;
+        const int wofs = lane < n128 ? 128 * lane : lane < n128 + n64 ? 128 * n128 : 128 * n128 + 64 * n64;
+        const uint32_t wdst = plan.swap ? 0u : (uint32_t)(kRows * kChunk);
+        const uint32_t tdst = plan.swap ? (uint32_t)(kRows * kChunk) : 0u;
+        const int per_copy = tiles ? args.tile_rows : 4;   // tokens a copy of a list, one copy a lane
         int it = 0, st = 0;
         uint32_t ph = 1;
         bool ok = true;
         for (uint32_t u = u_first; ok && u < plan.units; u += u_step) {
             const uint32_t rb = u / plan.cblocks;
             const int cb = (int)(u - rb * plan.cblocks);
-            const int wrow = (plan.swap ? (int)rb * kRows : cb * plan.bn) + lane * (wide ? kRows : 32);
-            // the copies that hold a token: what lies in the other rows of a stage
-            // enters only products that are not written
-            const uint32_t left = plan.slots - (plan.swap ? 0 : rb * kRows);
-            const int nt = box ? 1 : (int)((min(left, (uint32_t)kRows) + per_copy - 1) / per_copy);
-            const uint32_t bytes = (uint32_t)(wrows + nt * per_copy) * kChunk;
+            const int wrow = plan.swap ? (int)rb * kRows : cb * plan.bn;
+            const uint32_t s_first = plan.swap ? 0 : rb * kRows;
+            // the copies that hold a token of the list: what lies in the other
+            // rows of a stage enters only products that are not written
+            const int nt = lists ? (int)((min(plan.slots - s_first, (uint32_t)kRows) + per_copy - 1) / per_copy) : 0;
+            const uint32_t bytes = lists ? (uint32_t)(wrows + nt * per_copy) * kChunk : stage_bytes;
             // this lane's four tokens of the unit, or its tile (a clipped slot
             // reads the first token's row or tile)
             int t0 = 0, t1 = 0, t2 = 0, t3 = 0;
             if (tiles) {
-                const uint32_t s0 = (plan.swap ? 0 : rb * kRows) + (uint32_t)(lane * args.tile_rows);
-                if (lane < nt) {
-                    const int64_t px = pixel_of(p.px, s0);
-                    if (px >= 0) {
-                        const uint32_t tn = udiv(s0, p.px.dbb), t = udiv(tn, p.px.dN);
-                        const int2 org = __ldg(reinterpret_cast<const int2 *>(p.px.idx) + t);
-                        t0 = org.y;
-                        t1 = org.x;
-                        t2 = (int)(tn - t * (uint32_t)p.px.N);
-                    }
+                const uint32_t s0 = s_first + (uint32_t)(lane * args.tile_rows);
+                if (lane < nt && pixel_of(p.px, s0) >= 0) {
+                    const uint32_t tn = udiv(s0, p.px.dbb), t = udiv(tn, p.px.dN);
+                    const int2 org = __ldg(reinterpret_cast<const int2 *>(p.px.idx) + t);
+                    t0 = org.y;
+                    t1 = org.x;
+                    t2 = (int)(tn - t * (uint32_t)p.px.N);
                 }
-            } else if (!box) {
-                const uint32_t s0 = (plan.swap ? 0 : rb * kRows) + 4 * lane;
+            } else if (lists) {
+                const uint32_t s0 = s_first + 4 * lane;
                 int rows[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -408,20 +452,23 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                 }
                 const uint32_t full = bar + kBarFull + 8u * st;
                 const uint32_t dst = sb + (uint32_t)st * stage_bytes;
-                if (lane == 0)
-                    mbar_expect_tx(full, bytes);
-                __syncwarp();
-                if (lane < nw)
-                    tma_load_2d(dst + woff, wmap, full, c * kChunk, wrow);
-                if (lane < nt) {
-                    if (box)
-                        tma_load_2d(dst, &tbox, full, c * kChunk, (int)rb * kRows);
-                    else if (tiles)
-                        tma_load_4d(dst + tdst0, &tbox, full, c * kChunk, t0, t1, t2);
-                    else
-                        tma_gather4(dst + tdst0, &tbox, full, c * kChunk, t0, t1, t2, t3);
+                if (!lists) {
+                    tma_stage_w(dst + wdst, &tw, wrow, dst + tdst, &tbox, (int)s_first, full, bytes, c * kChunk);
+                } else {
+                    if (lane == 0)
+                        mbar_expect_tx(full, bytes);
+                    __syncwarp();
+                    if (lane < nw)
+                        tma_load_2d(dst + wdst + (uint32_t)wofs * kChunk, wmap, full, c * kChunk, wrow + wofs);
+                    if (lane < nt) {
+                        const uint32_t d = dst + tdst + (uint32_t)(lane * per_copy) * kChunk;
+                        if (tiles)
+                            tma_load_4d(d, &tbox, full, c * kChunk, t0, t1, t2);
+                        else
+                            tma_gather4(d, &tbox, full, c * kChunk, t0, t1, t2, t3);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
                 if (++st == plan.stages) {
                     st = 0;
                     ph ^= 1;
@@ -484,7 +531,6 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
         const int r = (warp & 3) * 32 + lane;              // row of the unit = tensor-memory lane
         const int half = (warp - 2) >> 2;
         const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t tile = sb + kOffRecv + (uint32_t)(warp - 2) * 2048u;   // (a split unit receives there instead)
         int nu = 0;
         bool ok = true;
         for (uint32_t u = u_first; u < plan.units; u += u_step, ++nu) {
@@ -540,9 +586,12 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                 }
                 // push the other slices to their owners: 16 columns at a time,
                 // [sender][4 columns][row] of 16 bytes
+                // (a slice without tokens of a swapped unit is nobody's)
                 for (int o = 1; o < split_n; ++o) {
-                    const int to = (split + o) % split_n;
-                    const int from = (split - to + split_n) % split_n - 1;   // this CTA among the owner's senders
+                    const int to = (split + o) & (split_n - 1);
+                    if (plan.swap && to * cw >= (int)plan.slots)
+                        continue;
+                    const int from = ((split - to) & (split_n - 1)) - 1;   // this CTA among the owner's senders
                     for (int g = 16 * half; g < cw; g += 32) {
                         int acc[16];
                         ld_cols(t_acc + (uint32_t)(to * cw + g), acc);
@@ -554,29 +603,56 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                             st_peer_s32x4(dst + (uint32_t)q * kRows * 16, acc[4 * q], acc[4 * q + 1], acc[4 * q + 2],
                                           acc[4 * q + 3]);
                     }
-                    mbar_arrive_peer(map_peer(bar + kBarRecv, (uint32_t)(sub * split_n + to)));
+                    __syncwarp();   // the warp's pushes, then one arrival for them
+                    if (lane == 0)
+                        mbar_arrive_peer(map_peer(bar + kBarRecv, (uint32_t)(sub * split_n + to)));
                 }
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar + kBarRecv, 0, abort_flag, hdr, kSiteRecv))) {
+                if ((!plan.swap || col0 < (int)plan.slots) &&
+                    !__all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar + kBarRecv, 0, abort_flag, hdr, kSiteRecv))) {
                     ok = false;
                     continue;
                 }
             }
-            int g0 = 0;   // columns finished in groups of 32
-            if (split_n == 1 && !plan.swap && args.vec && p.dtype == SIGE_BF16) {
-                for (; g0 + 32 <= cw && cb * plan.bn + g0 + 32 <= p.Co; g0 += 32) {
-                    if (((g0 >> 5) & 1) != half)
-                        continue;
-                    int acc[2][16];
-                    ld_cols(t_acc + (uint32_t)g0, acc[0]);
-                    ld_cols(t_acc + (uint32_t)g0 + 16u, acc[1]);
+            if (split_n == 1 && !plan.swap) {
+                // 32 columns at a time, the next ones on their way
+                int acc[2][32];
+                auto load = [&](int g, int (&r)[32]) {
+                    ld_cols(t_acc + (uint32_t)g, *reinterpret_cast<int (*)[16]>(r));
+                    ld_cols(t_acc + (uint32_t)g + 16u, *reinterpret_cast<int (*)[16]>(r + 16));
+                };
+                auto finish = [&](int g, int (&r)[32]) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float v[16];
+                        scale16(r + 16 * h, col + 4u * (uint32_t)(g + 16 * h), rs, v);
+                        if (pix >= 0)
+                            put_cols(args, v, pix, cb * plan.bn + g + 16 * h);
+                    }
+                };
+                int g = 32 * half;
+                if (g < cw) {
+                    load(g, acc[0]);
                     ld_done();
-                    float v[32];
-                    scale16(acc[0], col + 4u * (uint32_t)g0, rs, v);
-                    scale16(acc[1], col + 4u * (uint32_t)(g0 + 16), rs, v + 16);
-                    put64<2>(p, v, pix, cb * plan.bn + g0, tile, lane);
+                    while (true) {
+                        if (g + 64 < cw)
+                            load(g + 64, acc[1]);
+                        finish(g, acc[0]);
+                        if ((g += 64) >= cw)
+                            break;
+                        ld_done();
+                        if (g + 64 < cw)
+                            load(g + 64, acc[0]);
+                        finish(g, acc[1]);
+                        if ((g += 64) >= cw)
+                            break;
+                        ld_done();
+                    }
                 }
+                tc_fence_before();
+                mbar_arrive(bar + kBarAccEmpty + 8u * ab);
+                continue;
             }
-            for (int g = g0 + 16 * half; g < cw; g += 32) {
+            for (int g = 16 * half; g < cw && (!plan.swap || col0 + g < (int)plan.slots); g += 32) {
                 int acc[16];
                 ld_cols(t_acc + (uint32_t)(col0 + g), acc);
                 ld_done();
@@ -592,27 +668,21 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                     }
                 }
                 if (plan.swap) {
+                    const int nt = min(16, (int)plan.slots - col0 - g);
                     if (chan >= 0) {
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            const int t = tokp[col0 + g + k];
-                            if (t >= 0)
-                                put1(p, (int64_t)t * p.Co + chan, qlinear_value(acc[k], colp[col0 + g + k], rs) + rbias);
+                            if (k < nt) {
+                                const int t = tokp[col0 + g + k];
+                                if (t >= 0)
+                                    put1(p, (int64_t)t * p.Co + chan, qlinear_value(acc[k], colp[col0 + g + k], rs) + rbias);
+                            }
                         }
                     }
-                } else {
-                    // (a part of 16 columns, or a row's ragged or unaligned end)
-                    const int c = cb * plan.bn + col0 + g;
+                } else if (pix >= 0) {
                     float v[16];
                     scale16(acc, col + 4u * (uint32_t)(col0 + g), rs, v);
-                    if (split_n == 1 && args.vec && p.dtype == SIGE_F32 && c + 16 <= p.Co) {
-                        put64<4>(p, v, pix, c, tile, lane);
-                    } else if (pix >= 0) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            if (c + k < p.Co)
-                                put1(p, pix * p.Co + c + k, v[k]);
-                    }
+                    put_cols(args, v, pix, cb * plan.bn + col0 + g);
                 }
             }
             tc_fence_before();
@@ -676,24 +746,7 @@ int launch_qlinear_tc(const QLinearParams &p, cudaStream_t stream)
         return SIGE_ERR_CUDA;
     if (!encode)
         return SIGE_ERR_CUDA;
-    // how the tokens are copied: 128 in a row for a whole map; tiles of 4 x 4 or
-    // 8 x 8 (a divisor of 128 tokens, whole 1 KB swizzle atoms) by boxes, which
-    // took 8.4 -> %s us off ...; four tokens a copy otherwise
     qt::Args a{};
-    CUtensorMap tw, tw32, tbox;
-    bool good = encode_rows(&tw, p.w, p.Co, p.C, qt::kRows, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, encode) &&
-                encode_rows(&tw32, p.w, p.Co, p.C, 32, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, encode);
-    if (p.px.idx && (p.px.b == 4 || p.px.b == 8)) {
-        a.tile_rows = p.px.b * p.px.b;
-        good = good && encode_tiles(&tbox, p, encode);
-    } else {
-        // (the few tokens of a swapped unit are gathered from a whole map, too)
-        const bool rows128 = !p.px.idx && p.slots > qt::kSwapTokens;
-        good = good && encode_rows(&tbox, p.a, p.rows, p.C, rows128 ? qt::kRows : 1,
-                                   rows128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B, encode);
-    }
-    if (!good)
-        return SIGE_ERR_CUDA;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -726,20 +779,48 @@ int launch_qlinear_tc(const QLinearParams &p, cudaStream_t stream)
     prefer_max_shared(k_qlinear_tc);
     a.q = p;
     const int esz = p.dtype == SIGE_BF16 ? 2 : 4;
-    a.vec = (int64_t)p.Co * esz % 16 == 0 && aligned_to(p.y, 16) && aligned_to(p.residual, 16);
+    a.vec = (int64_t)p.Co * esz % 32 == 0 && aligned_to(p.y, 32) && aligned_to(p.residual, 32);
     // a whole map of enough units needs no cluster (every SM takes part); a
     // list's length is known on the device only
     const int sms = device_sm_count();
-    const bool solo = !p.px.idx && qt::make_plan((uint32_t)p.slots, p.Co, p.C, sms, qt::kCluster).split == 1;
-    cfg.numAttrs = solo ? 1 : 2;
-    if (solo) {
-        const qt::Plan plan = qt::make_plan((uint32_t)p.slots, p.Co, p.C, sms, 1);
-        cfg.gridDim = dim3((unsigned)std::min<int64_t>(sms, plan.units));
+    const int most = qt::kCluster * ncl;
+    bool solo = false;
+    if (!p.px.idx) {
+        a.plan = qt::make_plan((uint32_t)p.slots, p.Co, p.C, most, qt::kCluster);
+        solo = a.plan.split == 1;
+        if (solo)
+            a.plan = qt::make_plan((uint32_t)p.slots, p.Co, p.C, sms, 1);
+        cfg.gridDim = dim3(solo ? (unsigned)std::min<int64_t>(sms, a.plan.units)
+                                : (a.plan.units * a.plan.split + qt::kCluster - 1) / qt::kCluster * qt::kCluster);
     } else {
         // no more clusters than the narrowest units of a full list can use
         cfg.gridDim = dim3((unsigned)(qt::kCluster * std::max<int64_t>(1, std::min<int64_t>(ncl, narrowest))));
     }
-    if (cudaLaunchKernelEx(&cfg, k_qlinear_tc, a, tw, tw32, tbox) != cudaSuccess) {
+    cfg.numAttrs = solo ? 1 : 2;
+    // how the operands are copied.  A whole map: one box of weight rows and one
+    // of tokens a stage.  A list: tiles of 4 x 4 or 8 x 8 (a divisor of 128
+    // tokens) by a box each, 5.7 us where four tokens a copy took 8.8 (25 tiles
+    // of 4 x 4, C 320 -> 320); four tokens a copy otherwise.
+    CUtensorMap tw, tw64, tw32, tbox;
+    const CUtensorMapL2promotion l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+    bool good;
+    if (!p.px.idx) {
+        good = encode_rows(&tw, p.w, p.Co, p.C, a.plan.swap ? qt::kRows : a.plan.bn, l2, encode) &&
+               encode_rows(&tbox, p.a, p.rows, p.C, a.plan.swap ? a.plan.bn : qt::kRows, l2, encode);
+        tw64 = tw32 = tw;
+    } else {
+        good = encode_rows(&tw, p.w, p.Co, p.C, 128, l2, encode) && encode_rows(&tw64, p.w, p.Co, p.C, 64, l2, encode) &&
+               encode_rows(&tw32, p.w, p.Co, p.C, 32, l2, encode);
+        if (p.px.b == 4 || p.px.b == 8) {
+            a.tile_rows = p.px.b * p.px.b;
+            good = good && encode_tiles(&tbox, p, encode);
+        } else {
+            good = good && encode_rows(&tbox, p.a, p.rows, p.C, 1, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, encode);
+        }
+    }
+    if (!good)
+        return SIGE_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, k_qlinear_tc, a, tw, tw64, tw32, tbox) != cudaSuccess) {
         cudaGetLastError();
         return SIGE_ERR_CUDA;
     }
