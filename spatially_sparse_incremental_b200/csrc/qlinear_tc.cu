@@ -44,7 +44,7 @@ constexpr int kCluster = 4;
 constexpr int kMaxStages = 9;
 
 constexpr uint32_t kRing = 196608;       // 4 stages of 128 + 256 rows, more of narrower ones
-constexpr uint32_t kOffRecv = kRing;     // sums pushed by the other CTAs of a split unit
+constexpr uint32_t kOffRecv = kRing;     // sums pushed by the other CTAs of a split unit, or the output tiles of the warps
 constexpr uint32_t kRecvBytes = (kCluster - 1) * kRows * (kSplitBn / kCluster) * 4;
 constexpr uint32_t kOffCol = kOffRecv + kRecvBytes;          // per accumulator: column scales and biases
 constexpr uint32_t kOffTok = kOffCol + 2 * 2 * kMaxBn * 4;   // swapped units: the columns' pixels
@@ -58,6 +58,7 @@ constexpr uint32_t kBarDrain = kBarRecv + 8;
 constexpr uint32_t kTmemSlot = kBarDrain + 8;
 constexpr uint32_t kAbort = kTmemSlot + 4;
 constexpr uint32_t kSmem = kOffBar + 256 + 1024;             // + alignment slack
+static_assert(kEpiWarps * 2048 <= kRecvBytes, "output tiles");
 static_assert(kAbort + 4 <= 256, "barrier block");
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
@@ -238,22 +239,26 @@ __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n
 struct Args {
     QLinearParams q;
     int vec;       // y and the residual take 32-byte accesses of 16 columns
+    int tma_out;   // the outputs of a whole map leave by TMA
     int tile_rows; // tokens of a tile that one box copies, 0: four tokens a copy
     Plan plan;     // of a whole map (a list's is made on the device)
 };
 
+__device__ __forceinline__ float residual1(const QLinearParams &p, int64_t e)
+{
+    return p.dtype == SIGE_BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.residual)[e])
+                                : reinterpret_cast<const float *>(p.residual)[e];
+}
+
 // One output element.
 __device__ __forceinline__ void put1(const QLinearParams &p, int64_t e, float v)
 {
-    if (p.dtype == SIGE_BF16) {
-        if (p.residual)
-            v += __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.residual)[e]);
+    if (p.residual)
+        v += residual1(p, e);
+    if (p.dtype == SIGE_BF16)
         reinterpret_cast<__nv_bfloat16 *>(p.y)[e] = __float2bfloat16_rn(v);
-    } else {
-        if (p.residual)
-            v += reinterpret_cast<const float *>(p.residual)[e];
+    else
         reinterpret_cast<float *>(p.y)[e] = v;
-    }
 }
 
 // 16 sums of one token, scaled and biased: scales and biases from shared
@@ -284,20 +289,73 @@ __device__ __forceinline__ void ld_v8(const void *src, uint32_t *v)
                  : "l"(src));
 }
 
+// The outputs of a whole map leave through shared memory and TMA: v holds 64
+// bytes of columns (32 bf16 or 16 float32) of this lane's row, tile 2 KB of the
+// warp, the rows' 16-byte pieces at piece ^ ((row / 2) mod 4) (the 64-byte
+// swizzle of the output map, and no bank conflicts).  Storing them from the
+// registers, 32 bytes of 32 different lines an instruction, bounded a call of
+// wide outputs (16384 x 640 x 5120: 73 us, 45 us without the stores).
+template <int kE>   // bytes of an output element
+__device__ __forceinline__ void put_tile(const float *v, uint32_t tile, const CUtensorMap *map, int col, int row, int lane)
+{
+    // the previous tile has been read
+    if (lane == 0)
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+    const uint32_t own = tile + 64u * lane, sw = (uint32_t)(lane >> 1) & 3u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint4 x;
+        if constexpr (kE == 2) {
+            const float *u = v + 8 * k;
+            x = make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(u[4], u[5]), pack_bf16x2(u[6], u[7]));
+        } else {
+            x = make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]),
+                           __float_as_uint(v[4 * k + 3]));
+        }
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(own + (((uint32_t)k ^ sw) << 4)), "r"(x.x), "r"(x.y),
+                     "r"(x.z), "r"(x.w)
+                     : "memory");
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0)
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];\n"
+                     "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+                     "r"(tile), "r"(col), "r"(row)
+                     : "memory");
+}
+
+// + residual, for 16 columns of one token from element e on (32-byte aligned).
+__device__ __forceinline__ void add_residual16(const QLinearParams &p, int64_t e, float *v)
+{
+    uint32_t w[8];
+    if (p.dtype == SIGE_BF16) {
+        ld_v8(p.residual + e * 2, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            v[2 * k] += bf16_lo(w[k]);
+            v[2 * k + 1] += bf16_hi(w[k]);
+        }
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            ld_v8(p.residual + e * 4 + 32 * h, w);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[8 * h + k] += __uint_as_float(w[k]);
+        }
+    }
+}
+
 // 16 outputs of one token (y and the residual at element e, 32-byte aligned
 // rows): a thread writes whole sectors of its own row.
 __device__ __forceinline__ void put16(const QLinearParams &p, int64_t e, float *v)
 {
+    if (p.residual)
+        add_residual16(p, e, v);
+    uint32_t w[8];
     if (p.dtype == SIGE_BF16) {
-        uint32_t w[8];
-        if (p.residual) {
-            ld_v8(p.residual + e * 2, w);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                v[2 * k] += bf16_lo(w[k]);
-                v[2 * k + 1] += bf16_hi(w[k]);
-            }
-        }
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
@@ -305,13 +363,6 @@ __device__ __forceinline__ void put16(const QLinearParams &p, int64_t e, float *
     } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            uint32_t w[8];
-            if (p.residual) {
-                ld_v8(p.residual + e * 4 + 32 * h, w);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    v[8 * h + k] += __uint_as_float(w[k]);
-            }
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 w[k] = __float_as_uint(v[8 * h + k]);
@@ -341,7 +392,7 @@ using namespace qt;
 __global__ void __launch_bounds__(qt::kThreads, 1)
     k_qlinear_tc(const __grid_constant__ qt::Args args, const __grid_constant__ CUtensorMap tw,
                  const __grid_constant__ CUtensorMap tw64, const __grid_constant__ CUtensorMap tw32,
-                 const __grid_constant__ CUtensorMap tbox)
+                 const __grid_constant__ CUtensorMap tbox, const __grid_constant__ CUtensorMap ty)
 {
     extern __shared__ __align__(1024) uint8_t qt_raw[];
     const QLinearParams &p = args.q;
@@ -531,6 +582,7 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
         const int r = (warp & 3) * 32 + lane;              // row of the unit = tensor-memory lane
         const int half = (warp - 2) >> 2;
         const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t tile = sb + kOffRecv + (uint32_t)(warp - 2) * 2048u;   // (a split unit receives there instead)
         int nu = 0;
         bool ok = true;
         for (uint32_t u = u_first; u < plan.units; u += u_step, ++nu) {
@@ -620,14 +672,35 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                     ld_cols(t_acc + (uint32_t)g, *reinterpret_cast<int (*)[16]>(r));
                     ld_cols(t_acc + (uint32_t)g + 16u, *reinterpret_cast<int (*)[16]>(r + 16));
                 };
-                auto finish = [&](int g, int (&r)[32]) {
+                auto finish = [&](int g, int (&q)[32]) {
+                    const int c = cb * plan.bn + g, row = (int)rb * kRows + (warp & 3) * 32;
+                    float v[32];
+                    scale16(q, col + 4u * (uint32_t)g, rs, v);
+                    scale16(q + 16, col + 4u * (uint32_t)(g + 16), rs, v + 16);
+                    if (!args.tma_out) {
+                        if (pix >= 0) {
+                            put_cols(args, v, pix, c);
+                            put_cols(args, v + 16, pix, c + 16);
+                        }
+                        return;
+                    }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        float v[16];
-                        scale16(r + 16 * h, col + 4u * (uint32_t)(g + 16 * h), rs, v);
-                        if (pix >= 0)
-                            put_cols(args, v, pix, cb * plan.bn + g + 16 * h);
+                        if (p.residual && pix >= 0) {
+                            if (args.vec && c + 16 * h + 16 <= p.Co) {
+                                add_residual16(p, pix * p.Co + c + 16 * h, v + 16 * h);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 16; ++k)
+                                    if (c + 16 * h + k < p.Co)
+                                        v[16 * h + k] += residual1(p, pix * p.Co + c + 16 * h + k);
+                            }
+                        }
+                        if (p.dtype == SIGE_F32 && c + 16 * h < p.Co)
+                            put_tile<4>(v + 16 * h, tile, &ty, c + 16 * h, row, lane);
                     }
+                    if (p.dtype == SIGE_BF16 && c < p.Co)
+                        put_tile<2>(v, tile, &ty, c, row, lane);
                 };
                 int g = 32 * half;
                 if (g < cw) {
@@ -689,6 +762,9 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
             mbar_arrive(bar + kBarAccEmpty + 8u * ab);
         }
     }
+    if (warp >= 2 && lane == 0)
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // the outputs have left shared memory
+    __syncwarp();
     if (csize > 1 && !joined)
         cluster_wait();
     tc_fence_before();
@@ -729,6 +805,18 @@ static bool encode_tiles(CUtensorMap *map, const QLinearParams &p, PFN_cuTensorM
     cuuint32_t es[4] = {1, 1, 1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t *>(p.a), dims, strides, box, es,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The output [rows][Co], 64 bytes of columns x 32 rows a copy.
+static bool encode_out(CUtensorMap *map, const QLinearParams &p, int esz, PFN_cuTensorMapEncodeTiled_v12000 encode)
+{
+    cuuint64_t dims[2] = {(cuuint64_t)p.Co, (cuuint64_t)p.rows};
+    cuuint64_t strides[1] = {(cuuint64_t)p.Co * esz};
+    cuuint32_t box[2] = {(cuuint32_t)(64 / esz), 32};
+    cuuint32_t es[2] = {1, 1};
+    return encode(map, esz == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p.y, dims, strides,
+                  box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -801,13 +889,15 @@ int launch_qlinear_tc(const QLinearParams &p, cudaStream_t stream)
     // of tokens a stage.  A list: tiles of 4 x 4 or 8 x 8 (a divisor of 128
     // tokens) by a box each, 5.7 us where four tokens a copy took 8.8 (25 tiles
     // of 4 x 4, C 320 -> 320); four tokens a copy otherwise.
-    CUtensorMap tw, tw64, tw32, tbox;
+    CUtensorMap tw, tw64, tw32, tbox, ty{};
     const CUtensorMapL2promotion l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
     bool good;
     if (!p.px.idx) {
         good = encode_rows(&tw, p.w, p.Co, p.C, a.plan.swap ? qt::kRows : a.plan.bn, l2, encode) &&
                encode_rows(&tbox, p.a, p.rows, p.C, a.plan.swap ? a.plan.bn : qt::kRows, l2, encode);
         tw64 = tw32 = tw;
+        a.tma_out = !a.plan.swap && a.plan.split == 1 && (int64_t)p.Co * esz % 16 == 0 && aligned_to(p.y, 16) &&
+                    encode_out(&ty, p, esz, encode);
     } else {
         good = encode_rows(&tw, p.w, p.Co, p.C, 128, l2, encode) && encode_rows(&tw64, p.w, p.Co, p.C, 64, l2, encode) &&
                encode_rows(&tw32, p.w, p.Co, p.C, 32, l2, encode);
@@ -820,7 +910,7 @@ int launch_qlinear_tc(const QLinearParams &p, cudaStream_t stream)
     }
     if (!good)
         return SIGE_ERR_CUDA;
-    if (cudaLaunchKernelEx(&cfg, k_qlinear_tc, a, tw, tw64, tw32, tbox) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, k_qlinear_tc, a, tw, tw64, tw32, tbox, ty) != cudaSuccess) {
         cudaGetLastError();
         return SIGE_ERR_CUDA;
     }
