@@ -44,7 +44,8 @@ constexpr int kCluster = 4;
 constexpr int kMaxStages = 9;
 
 constexpr uint32_t kRing = 196608;       // 4 stages of 128 + 256 rows, more of narrower ones
-constexpr uint32_t kOffRecv = kRing;     // sums pushed by the other CTAs of a split unit, or the output tiles of the warps
+constexpr uint32_t kOffRecv = kRing;     // sums pushed by the other CTAs of a split unit (k_qlinear_whole: the
+                                         // output tiles of the warps)
 constexpr uint32_t kRecvBytes = (kCluster - 1) * kRows * (kSplitBn / kCluster) * 4;
 constexpr uint32_t kOffCol = kOffRecv + kRecvBytes;          // per accumulator: column scales and biases
 constexpr uint32_t kOffTok = kOffCol + 2 * 2 * kMaxBn * 4;   // swapped units: the columns' pixels
@@ -236,10 +237,29 @@ __device__ __forceinline__ float4 lds_f32x4(uint32_t addr)
 }
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); }
 
+// After a wait that expired: the copies in flight (the last of `it` issued) land,
+// and the products in flight finish, before the CTA's memory is given up; both
+// bounded.
+__device__ __noinline__ void drain_copies(uint32_t bar, int it, int stages)
+{
+    for (int i = 0; i < min(it, stages); ++i) {
+        const int k = it - 1 - i, s = k % stages;
+        const long long t0 = clock64();
+        while (!mbar_try(bar + kBarFull + 8u * s, (k / stages) & 1) && clock64() - t0 < kWaitCycles / 64)
+            ;
+    }
+}
+__device__ __noinline__ void drain_products(uint32_t bar)
+{
+    tc_commit_w(bar + kBarDrain);
+    const long long t0 = clock64();
+    while (!mbar_try(bar + kBarDrain, 0) && clock64() - t0 < kWaitCycles / 64)
+        ;
+}
+
 struct Args {
     QLinearParams q;
     int vec;       // y and the residual take 32-byte accesses of 16 columns
-    int tma_out;   // the outputs of a whole map leave by TMA
     int tile_rows; // tokens of a tile that one box copies, 0: four tokens a copy
     Plan plan;     // of a whole map (a list's is made on the device)
 };
@@ -392,7 +412,7 @@ using namespace qt;
 __global__ void __launch_bounds__(qt::kThreads, 1)
     k_qlinear_tc(const __grid_constant__ qt::Args args, const __grid_constant__ CUtensorMap tw,
                  const __grid_constant__ CUtensorMap tw64, const __grid_constant__ CUtensorMap tw32,
-                 const __grid_constant__ CUtensorMap tbox, const __grid_constant__ CUtensorMap ty)
+                 const __grid_constant__ CUtensorMap tbox)
 {
     extern __shared__ __align__(1024) uint8_t qt_raw[];
     const QLinearParams &p = args.q;
@@ -413,7 +433,7 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar + kBarAccFull + 8u * i, 1);
-            mbar_init(bar + kBarAccEmpty + 8u * i, kEpiThreads);
+            mbar_init(bar + kBarAccEmpty + 8u * i, kEpiWarps);
         }
         mbar_init(bar + kBarDrain, 1);
         *abort_flag = 0;
@@ -526,15 +546,8 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                 }
             }
         }
-        if (!ok) {
-            // the copies in flight land before this CTA's memory is given up
-            for (int i = 0; i < min(it, plan.stages); ++i) {
-                const int k = it - 1 - i, s = k % plan.stages;
-                const long long t0 = clock64();
-                while (!mbar_try(bar + kBarFull + 8u * s, (k / plan.stages) & 1) && clock64() - t0 < kWaitCycles / 64)
-                    ;
-            }
-        }
+        if (!ok)
+            drain_copies(bar, it, plan.stages);
         __syncwarp();
     } else if (warp == 1) {
         // ---- products
@@ -569,12 +582,8 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
             if (ok)
                 tc_commit_w(bar + kBarAccFull + 8u * ab);
         }
-        if (!ok) {
-            tc_commit_w(bar + kBarDrain);
-            const long long t0 = clock64();
-            while (!mbar_try(bar + kBarDrain, 0) && clock64() - t0 < kWaitCycles / 64)
-                ;
-        }
+        if (!ok)
+            drain_products(bar);
         __syncwarp();
     } else {
         // ---- outputs
@@ -582,7 +591,6 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
         const int r = (warp & 3) * 32 + lane;              // row of the unit = tensor-memory lane
         const int half = (warp - 2) >> 2;
         const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t tile = sb + kOffRecv + (uint32_t)(warp - 2) * 2048u;   // (a split unit receives there instead)
         int nu = 0;
         bool ok = true;
         for (uint32_t u = u_first; u < plan.units; u += u_step, ++nu) {
@@ -673,34 +681,13 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                     ld_cols(t_acc + (uint32_t)g + 16u, *reinterpret_cast<int (*)[16]>(r + 16));
                 };
                 auto finish = [&](int g, int (&q)[32]) {
-                    const int c = cb * plan.bn + g, row = (int)rb * kRows + (warp & 3) * 32;
-                    float v[32];
-                    scale16(q, col + 4u * (uint32_t)g, rs, v);
-                    scale16(q + 16, col + 4u * (uint32_t)(g + 16), rs, v + 16);
-                    if (!args.tma_out) {
-                        if (pix >= 0) {
-                            put_cols(args, v, pix, c);
-                            put_cols(args, v + 16, pix, c + 16);
-                        }
-                        return;
-                    }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        if (p.residual && pix >= 0) {
-                            if (args.vec && c + 16 * h + 16 <= p.Co) {
-                                add_residual16(p, pix * p.Co + c + 16 * h, v + 16 * h);
-                            } else {
-#pragma unroll
-                                for (int k = 0; k < 16; ++k)
-                                    if (c + 16 * h + k < p.Co)
-                                        v[16 * h + k] += residual1(p, pix * p.Co + c + 16 * h + k);
-                            }
-                        }
-                        if (p.dtype == SIGE_F32 && c + 16 * h < p.Co)
-                            put_tile<4>(v + 16 * h, tile, &ty, c + 16 * h, row, lane);
+                        float v[16];
+                        scale16(q + 16 * h, col + 4u * (uint32_t)(g + 16 * h), rs, v);
+                        if (pix >= 0)
+                            put_cols(args, v, pix, cb * plan.bn + g + 16 * h);
                     }
-                    if (p.dtype == SIGE_BF16 && c < p.Co)
-                        put_tile<2>(v, tile, &ty, c, row, lane);
                 };
                 int g = 32 * half;
                 if (g < cw) {
@@ -722,7 +709,9 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(bar + kBarAccEmpty + 8u * ab);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar + kBarAccEmpty + 8u * ab);
                 continue;
             }
             for (int g = 16 * half; g < cw && (!plan.swap || col0 + g < (int)plan.slots); g += 32) {
@@ -759,12 +748,11 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                 }
             }
             tc_fence_before();
-            mbar_arrive(bar + kBarAccEmpty + 8u * ab);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar + kBarAccEmpty + 8u * ab);
         }
     }
-    if (warp >= 2 && lane == 0)
-        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // the outputs have left shared memory
-    __syncwarp();
     if (csize > 1 && !joined)
         cluster_wait();
     tc_fence_before();
@@ -777,6 +765,213 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
     if (csize > 1) {
         cluster_arrive();
         cluster_wait();
+    }
+}
+
+// The same for a whole map whose units are neither swapped nor split and whose
+// outputs TMA can store: the loops that bound the large products, with nothing
+// else in them (the general kernel's outputs, with every case in one loop, ran
+// at about half their rate).  kE: bytes of an output element.
+template <int kE>
+__global__ void __launch_bounds__(qt::kThreads, 1)
+    k_qlinear_whole(const __grid_constant__ qt::Args args, const __grid_constant__ CUtensorMap tw,
+                    const __grid_constant__ CUtensorMap tbox, const __grid_constant__ CUtensorMap ty)
+{
+    extern __shared__ __align__(1024) uint8_t qt_raw[];
+    const QLinearParams &p = args.q;
+    const Plan &plan = args.plan;
+    const uint32_t raw = smem_u32(qt_raw);
+    const uint32_t sb = (raw + 1023u) & ~1023u;
+    uint8_t *smem = qt_raw + (sb - raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t bar = sb + kOffBar;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffBar + kAbort);
+    WsHeader *hdr = p.hdr;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kMaxStages; ++i) {
+            mbar_init(bar + kBarFull + 8u * i, 1);
+            mbar_init(bar + kBarEmpty + 8u * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar + kBarAccFull + 8u * i, 1);
+            mbar_init(bar + kBarAccEmpty + 8u * i, kEpiWarps);
+        }
+        mbar_init(bar + kBarDrain, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0 && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tw)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tbox)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&ty)) : "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(bar + kTmemSlot),
+                     "r"(2 * kMaxBn));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + kOffBar + kTmemSlot);
+    pdl_wait();
+
+    const uint32_t stage_bytes = (uint32_t)(kRows + plan.bn) * kChunk;
+    if (warp == 0) {
+        // ---- operands
+        int it = 0, st = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        for (uint32_t u = blockIdx.x; ok && u < plan.units; u += gridDim.x) {
+            const uint32_t rb = u / plan.cblocks;
+            const int cb = (int)(u - rb * plan.cblocks);
+            for (int c = 0; c < plan.nch; ++c, ++it) {
+                if (it >= plan.stages && !mbar_wait_w(bar + kBarEmpty + 8u * st, ph, abort_flag, hdr, kSiteEmpty)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = sb + (uint32_t)st * stage_bytes;
+                tma_stage_w(dst + kRows * kChunk, &tw, cb * plan.bn, dst, &tbox, (int)rb * kRows, bar + kBarFull + 8u * st,
+                            stage_bytes, c * kChunk);
+                if (++st == plan.stages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        if (!ok)
+            drain_copies(bar, it, plan.stages);
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---- products
+        const uint32_t id = idesc_s8(plan.bn);
+        const uint64_t ring = desc_sw128(sb);
+        const int last_steps = (p.C - (plan.nch - 1) * kChunk + 31) / 32;
+        int st = 0, nu = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (uint32_t u = blockIdx.x; ok && u < plan.units; u += gridDim.x, ++nu) {
+            const int ab = nu & 1;
+            if (nu >= 2 && !mbar_wait_w(bar + kBarAccEmpty + 8u * ab, ((nu >> 1) & 1) ^ 1, abort_flag, hdr, kSiteAccEmpty)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            for (int c = 0; c < plan.nch; ++c) {
+                if (!mbar_wait_w(bar + kBarFull + 8u * st, ph, abort_flag, hdr, kSiteFull)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t ad = ring + (uint64_t)((uint32_t)st * (stage_bytes >> 4));
+                mma_s8_commit_w(tmem + (uint32_t)ab * kMaxBn, ad, ad + ((kRows * kChunk) >> 4), id, c > 0,
+                                c + 1 < plan.nch ? 4 : last_steps, bar + kBarEmpty + 8u * st);
+                if (++st == plan.stages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+            if (ok)
+                tc_commit_w(bar + kBarAccFull + 8u * ab);
+        }
+        if (!ok)
+            drain_products(bar);
+        __syncwarp();
+    } else {
+        // ---- outputs: a warp's rows are its quarter of the tensor memory's
+        // lanes, its columns every other group of 64 bytes
+        constexpr int kCols = 64 / kE;
+        const int et = (int)threadIdx.x - 64, r = (warp & 3) * 32 + lane, half = (warp - 2) >> 2;
+        const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t tile = sb + kOffRecv + (uint32_t)(warp - 2) * 2048u;
+        float *colp = reinterpret_cast<float *>(smem + kOffCol);
+        // a unit's scales (thread: a column's, and its row's) are on their way
+        // under the unit before
+        float n_sw = 0.0f, n_bias = 0.0f, n_sa = 0.0f;
+        auto fetch = [&](uint32_t u) {
+            const uint32_t rb = u / plan.cblocks;
+            const int c = (int)(u - rb * plan.cblocks) * plan.bn + et;
+            const bool in = et < plan.bn && c < p.Co;
+            const int64_t row = (int64_t)rb * kRows + r;
+            n_sw = in ? __ldg(p.sw + c) : 0.0f;
+            n_bias = in && p.bias ? __ldg(p.bias + c) : 0.0f;
+            n_sa = row < p.rows ? __ldg(p.sa + row) : 0.0f;
+        };
+        if (blockIdx.x < plan.units)
+            fetch(blockIdx.x);
+        int nu = 0;
+        bool ok = true;
+        for (uint32_t u = blockIdx.x; u < plan.units; u += gridDim.x, ++nu) {
+            const int ab = nu & 1;
+            const uint32_t rb = u / plan.cblocks;
+            const int c0 = (int)(u - rb * plan.cblocks) * plan.bn;
+            const uint32_t col = sb + kOffCol + (uint32_t)ab * 2 * kMaxBn * 4;
+            colp[ab * 2 * kMaxBn + et] = n_sw;
+            colp[ab * 2 * kMaxBn + kMaxBn + et] = n_bias;
+            const float sa = n_sa;
+            const int row0 = (int)rb * kRows + (warp & 3) * 32;
+            const int64_t e0 = ((int64_t)row0 + lane) * p.Co + c0;
+            const bool has_res = p.residual && row0 + lane < p.rows;
+            uint32_t res[16];
+            auto residual = [&](int g) {   // this row's 64 bytes from column g of the unit on
+                if (has_res && c0 + g < p.Co) {
+                    ld_v8(p.residual + (e0 + g) * kE, res);
+                    if (c0 + g + kCols / 2 < p.Co)
+                        ld_v8(p.residual + (e0 + g) * kE + 32, res + 8);
+                }
+            };
+            residual(half * kCols);
+            if (u + gridDim.x < plan.units)
+                fetch(u + gridDim.x);
+            epi_sync();   // (every warp of every unit comes here: a wait that expired keeps a warp in the loop)
+            if (ok)
+                ok = mbar_wait_w(bar + kBarAccFull + 8u * ab, (nu >> 1) & 1, abort_flag, hdr, kSiteAccFull);
+            if (!ok)
+                continue;
+            tc_fence_after();
+            const uint32_t t_acc = t_row + (uint32_t)ab * kMaxBn;
+#pragma unroll 1
+            for (int g = half * kCols; g < plan.bn && c0 + g < p.Co; g += 2 * kCols) {
+                int acc[kCols];
+                float v[kCols];
+#pragma unroll
+                for (int q = 0; q < kCols; q += 16)
+                    ld_cols(t_acc + (uint32_t)(g + q), *reinterpret_cast<int (*)[16]>(acc + q));
+                ld_done();
+#pragma unroll
+                for (int q = 0; q < kCols; q += 16)
+                    scale16(acc + q, col + 4u * (uint32_t)(g + q), sa, v + q);
+                if (p.residual) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        if constexpr (kE == 2) {
+                            v[2 * k] += bf16_lo(res[k]);
+                            v[2 * k + 1] += bf16_hi(res[k]);
+                        } else {
+                            v[k] += __uint_as_float(res[k]);
+                        }
+                    }
+                    if (g + 2 * kCols < plan.bn)
+                        residual(g + 2 * kCols);
+                }
+                if (row0 < p.rows)
+                    put_tile<kE>(v, tile, &ty, c0 + g, row0, lane);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar + kBarAccEmpty + 8u * ab);
+        }
+        if (lane == 0)
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // the outputs have left shared memory
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * kMaxBn));
     }
 }
 
@@ -850,7 +1045,9 @@ int launch_qlinear_tc(const QLinearParams &p, cudaStream_t stream)
     static std::atomic<int> clusters_of[64];   // co-resident clusters, per device
     int ncl = clusters_of[dev].load(std::memory_order_acquire);
     if (ncl == 0) {
-        if (cudaFuncSetAttribute(k_qlinear_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)qt::kSmem) != cudaSuccess) {
+        if (cudaFuncSetAttribute(k_qlinear_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)qt::kSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(k_qlinear_whole<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)qt::kSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(k_qlinear_whole<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)qt::kSmem) != cudaSuccess) {
             cudaGetLastError();
             return SIGE_ERR_CUDA;
         }
@@ -872,7 +1069,7 @@ int launch_qlinear_tc(const QLinearParams &p, cudaStream_t stream)
     // list's length is known on the device only
     const int sms = device_sm_count();
     const int most = qt::kCluster * ncl;
-    bool solo = false;
+    bool solo = false, whole = false;
     if (!p.px.idx) {
         a.plan = qt::make_plan((uint32_t)p.slots, p.Co, p.C, most, qt::kCluster);
         solo = a.plan.split == 1;
@@ -896,8 +1093,7 @@ int launch_qlinear_tc(const QLinearParams &p, cudaStream_t stream)
         good = encode_rows(&tw, p.w, p.Co, p.C, a.plan.swap ? qt::kRows : a.plan.bn, l2, encode) &&
                encode_rows(&tbox, p.a, p.rows, p.C, a.plan.swap ? a.plan.bn : qt::kRows, l2, encode);
         tw64 = tw32 = tw;
-        a.tma_out = !a.plan.swap && a.plan.split == 1 && (int64_t)p.Co * esz % 16 == 0 && aligned_to(p.y, 16) &&
-                    encode_out(&ty, p, esz, encode);
+        whole = solo && !a.plan.swap && a.vec && encode_out(&ty, p, esz, encode);
     } else {
         good = encode_rows(&tw, p.w, p.Co, p.C, 128, l2, encode) && encode_rows(&tw64, p.w, p.Co, p.C, 64, l2, encode) &&
                encode_rows(&tw32, p.w, p.Co, p.C, 32, l2, encode);
@@ -910,7 +1106,10 @@ int launch_qlinear_tc(const QLinearParams &p, cudaStream_t stream)
     }
     if (!good)
         return SIGE_ERR_CUDA;
-    if (cudaLaunchKernelEx(&cfg, k_qlinear_tc, a, tw, tw64, tw32, tbox, ty) != cudaSuccess) {
+    const cudaError_t err = !whole      ? cudaLaunchKernelEx(&cfg, k_qlinear_tc, a, tw, tw64, tw32, tbox)
+                            : esz == 2 ? cudaLaunchKernelEx(&cfg, k_qlinear_whole<2>, a, tw, tbox, ty)
+                                       : cudaLaunchKernelEx(&cfg, k_qlinear_whole<4>, a, tw, tbox, ty);
+    if (err != cudaSuccess) {
         cudaGetLastError();
         return SIGE_ERR_CUDA;
     }
