@@ -6,25 +6,25 @@
 // the score before the softmax (key scale), to the weight after it (value
 // scale); the only rounding of an operand is that of weight * scale to bf16.
 //
-// Work unit: 128 query slots of one (batch item, head), the keys in chunks of
-// 64.  Roles of a CTA's 16 warps:
-//   * warps 9 .. 15 stage the operands: the unit's queries once, and for each
-//     chunk the codes (global loads of 8 codes a lane, one chunk ahead), turned
+// Work unit: one or two blocks of 128 query slots of one (batch item, head), the
+// keys in chunks of 64.  Roles of a CTA's warps:
+//   * seven warps stage the operands: the unit's queries once, and for each
+//     chunk the codes (global loads of 8 codes a lane, two chunks ahead), turned
 //     into bf16 rows of 128 bytes with the 128-byte swizzle (K-major for the
 //     first product, MN-major for the second), and the chunk's scales;
-//   * warp 8 issues S = Q K^T (M 128, N 64) and O += P V (M 128, K 64);
-//   * warps 0 .. 3 and 4 .. 7 are two softmax groups, one query row a thread,
-//     that take every other chunk, or (more units than CTAs) a block of 128
-//     queries each, so that a chunk is staged once for 256 queries: running maximum and sum (float32),
-//     P = 2^(s - max) * value scale as bf16 over the chunk's own S columns, the
-//     O row in tensor memory rescaled only when the maximum has grown by more
-//     than 8 (base 2).  Each group has two S buffers, so the scores of its next
-//     chunk are there when it has finished one; with one group waiting the
-//     other keeps the exponentials busy.
-// Rows (O, max, sum) of groups that share a block are merged through shared
-// memory at the end of a unit.  Where units are fewer than half the CTAs, the CTAs of a cluster
-// also split the keys and push their rows to the row's owner through
-// distributed shared memory.
+//   * one warp issues S = Q K^T (M 128, N 64) and O += P V (M 128, K 64);
+//   * four groups of four warps (heads up to 64; two groups for wider ones) do
+//     the softmax, one query row a thread, taking (block, chunk) jobs in turn:
+//     running maximum and sum (float32), P = 2^(s - max) * value scale as bf16
+//     over the chunk's own S columns, the O row in tensor memory rescaled only
+//     when the maximum has grown by more than 8 (base 2).  A thread reads its
+//     scores twice, 32 at a time (once for the maximum, once for the weights):
+//     few registers, so that four warps a scheduler cover each other's waits.
+// With more units than CTAs a unit is two blocks, so that a chunk is staged once
+// for 256 queries.  Rows (O, max, sum) of groups that share a block are merged
+// through shared memory at the end of a unit.  Where units are fewer than half
+// the CTAs, the CTAs of a cluster also split the keys and push their rows to
+// the row's owner through distributed shared memory.
 #include <algorithm>
 #include <atomic>
 #include <math.h>
@@ -39,60 +39,66 @@ namespace at {
 using namespace attn;
 
 constexpr int kRows = 128;
-constexpr int kKeys = 64;           // keys of a chunk
 constexpr int kGroup = 128;         // threads of a softmax group
-constexpr int kSoft = 2 * kGroup;
-constexpr int kStage = 224;         // staging threads
-// Registers: 512 threads are launched with 128 each; the softmax groups take
-// 152, the warpgroup of the MMA warp and the other staging one 104 (2 x 152 +
-// 2 x 104 = 4 x 128).
-constexpr int kSoftRegs = 152, kStageRegs = 104;
-constexpr int kThreads = kSoft + 32 + kStage;
+constexpr int kStage = 192;         // staging threads
 constexpr int kCluster = 4;
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 3;
 
-// Shared memory for heads of up to KD (64 or 128) channels.
+// Shared and tensor memory for heads of up to KD (64 or 128) channels.
 template <int KD>
 struct Lay {
+    static constexpr int kKeys = KD == 64 ? 128 : 64;                 // keys of a chunk
+    static constexpr int kSoft = 2 * kGroup, kMmaWarp = kSoft / 32, kThreads = kSoft + 64 + kStage;
     static constexpr int kAtoms = KD / 64;                            // 64-channel blocks of 128-byte rows
-    static constexpr int kStages = KD == 64 ? 6 : 3;                  // chunk ring
-    static constexpr int kAhead = KD == 64 ? 4 : 2;                   // S products issued before the P V of the first:
-                                                                      // fewer chunks than the ring's, whose next is being staged
+    static constexpr int kStages = 3;                                 // chunk ring
     static constexpr uint32_t kQAtom = kRows * 128, kKvAtom = kKeys * 128;
-    static constexpr uint32_t kOffQ = 0;
-    static constexpr uint32_t kOffX = kAtoms * kQAtom;                // rows exchanged by the two groups of a block,
-    static constexpr uint32_t kOffQ2 = kOffX;                         // or the second block's queries
-    static constexpr uint32_t kOffK = kOffX + kRows * KD * 4;         // [stage][K atoms, V atoms]
+    static constexpr uint32_t kOffQ = 0;                              // queries, a second block's at kOffQ2
+    static constexpr uint32_t kOffQ2 = kAtoms * kQAtom;
+    // rows exchanged by the groups of a block, half a row a softmax thread (over
+    // the second block's queries: units of one block only)
+    static constexpr uint32_t kOffX = kOffQ2;
+    static constexpr uint32_t kOffK = kOffX + kSoft * (KD / 2) * 4;   // [stage][K atoms, V atoms]
     static constexpr uint32_t kKvStage = 2 * kAtoms * kKvAtom;
-    static constexpr uint32_t kOffSc = kOffK + kStages * kKvStage;    // [stage][64 key scales, 64 value scales]
-    static constexpr uint32_t kOffMl = kOffSc + kStages * 512;        // [256] (max, sum)
-    static constexpr uint32_t kOffBar = kOffMl + 2048;
+    static constexpr uint32_t kScStage = 2 * kKeys * 4;
+    static constexpr uint32_t kOffSc = kOffK + kStages * kKvStage;    // [stage][key scales, value scales]
+    static constexpr uint32_t kOffMl = kOffSc + kStages * kScStage;   // (max, sum) of a softmax thread's row
+    static constexpr uint32_t kOffBar = kOffMl + kSoft * 8;
     static constexpr uint32_t kBytes = kOffBar + 256 + 1024;          // + alignment slack
     // rows pushed by the CTAs of a split unit, over the exchange rows and the
-    // ring (both idle by then): 256 rows of KD floats
+    // ring (both idle by then): kSoft rows of KD floats
     static constexpr uint32_t kOffPush = kOffX;
-    static_assert(kOffPush + 256 * KD * 4 <= kOffSc, "pushed rows");
+    static_assert(kOffPush + kSoft * KD * 4 <= kOffSc, "pushed rows");
+    static_assert(kOffQ2 + kAtoms * kQAtom <= kOffK && kOffK % 1024 == 0, "second block's queries");
     static_assert(kBytes <= 227 * 1024, "shared memory");
+    // Tensor memory, 512 columns.  Heads up to 64: a group's S (128 columns), its
+    // P apart (64), so that the next S comes while the weights are still being
+    // made; O (64).  Wider heads: two buffers of 64 columns a group, P over S; O
+    // (128).
+    static constexpr bool kApart = KD == 64;
+    static constexpr int kBufs = kApart ? 1 : 2;
+    static __device__ __forceinline__ uint32_t tmem_s(uint32_t g, uint32_t b) { return kApart ? 128u * g : 64u * (2 * g + b); }
+    static __device__ __forceinline__ uint32_t tmem_p(uint32_t g, uint32_t b) { return kApart ? 256u + 64u * g : tmem_s(g, b); }
+    static __device__ __forceinline__ uint32_t tmem_o(uint32_t g) { return kApart ? 384u + 64u * g : 256u + 128u * g; }
 };
 
 constexpr uint32_t kBarKvFull = 0;      // + 8 stage
-constexpr uint32_t kBarKvEmpty = 48;    // + 8 stage
-constexpr uint32_t kBarSFull = 96;      // + 16 group + 8 buffer
-constexpr uint32_t kBarPFull = 128;     // + 16 group + 8 buffer
-constexpr uint32_t kBarPvDone = 160;    // + 8 group
+constexpr uint32_t kBarKvEmpty = 32;    // + 8 stage
+constexpr uint32_t kBarSFull = 64;      // + 8 buffer (group by group)
+constexpr uint32_t kBarSFree = 96;      // + 8 group: its S has been read (P apart)
+constexpr uint32_t kBarPFull = 112;     // + 8 buffer
+constexpr uint32_t kBarPvDone = 144;    // + 8 buffer: the P V of its last job has landed
 constexpr uint32_t kBarQFull = 176;
 constexpr uint32_t kBarQEmpty = 184;
 constexpr uint32_t kBarReady = 192;     // every CTA of a split unit has finished its products
 constexpr uint32_t kBarPush = 200;      // the rows this CTA owns have been pushed
-constexpr uint32_t kBarDrain = 208;
-constexpr uint32_t kTmemSlot = 216;
-constexpr uint32_t kAbort = 220;
-constexpr uint32_t kTmemCols = 512;     // S / P: four buffers of 64 columns, O: 256 + 128 group
-constexpr uint32_t kTmemO = 256;
+constexpr uint32_t kBarDrain = 208;     // + 8 for the P V warp
+constexpr uint32_t kTmemSlot = 224;
+constexpr uint32_t kAbort = 228;
+constexpr uint32_t kTmemCols = 512;
 
 // wait sites (the detail of a recorded SIGE_ERR_TIMEOUT)
 constexpr int kSiteKvEmpty = 401, kSiteKvFull = 402, kSiteQEmpty = 403, kSitePFull = 404, kSiteQFull = 405,
-              kSiteSFull = 406, kSitePvDone = 407, kSiteReady = 408, kSitePush = 409;
+              kSiteSFull = 406, kSitePvDone = 407, kSiteReady = 408, kSitePush = 409, kSiteFree = 410;
 
 struct Args {
     AttnQParams a;
@@ -154,7 +160,7 @@ __device__ __forceinline__ uint32_t place(uint32_t atom, int j, int v)
 // vector i being (key j, vector v) number t + kStage i of the chunk, v fastest.
 // Where they lie in the chunk and in shared memory is worked out once; kSets
 // register sets hold the codes on their way.
-template <int N, int kSets>
+template <int N, int kSets, int kKeys>
 struct Stager {
     uint32_t src[N];      // byte offset from the chunk's first key
     uint32_t to[N];       // offset in the staged rows | key << 16 (kKeys: no such vector, kZero: zeros for padded channels)
@@ -271,6 +277,12 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 {
     uint64_t d;
@@ -288,7 +300,19 @@ __device__ __forceinline__ void sts_f4(uint32_t addr, const float *v)
 {
     asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
 }
+template <int kSoft>
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory"); }
+
+// 16 columns of this warp's 32 tensor-memory lanes.
+__device__ __forceinline__ void st16u(uint32_t taddr, const uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
 
 // Bounded waits by every lane of a warp, inline (a call would keep the
 // compiler from splitting the registers between the roles): false, in all
@@ -322,9 +346,10 @@ struct Unit {
 
 struct Work {
     int qblocks, slots, units, split, per, u_first, u_step, rank_split, base;
-    int pairs;   // the two softmax groups take a query block each (else they share one)
+    int pairs;   // 1: units of two query blocks
 };
 
+template <int kKeys>
 __device__ __forceinline__ Unit unit_at(const AttnQParams &p, const Work &w, int u)
 {
     Unit x;
@@ -344,9 +369,10 @@ __device__ __forceinline__ Unit unit_at(const AttnQParams &p, const Work &w, int
 using namespace at;
 
 template <int KD>
-__global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid_constant__ at::Args args)
+__global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(const __grid_constant__ at::Args args)
 {
     using L = Lay<KD>;
+    constexpr int kKeys = L::kKeys;
     extern __shared__ __align__(1024) uint8_t at_raw[];
     const AttnQParams &p = args.a;
     const uint32_t raw = smem_u32(at_raw);
@@ -357,7 +383,7 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kOffBar + kAbort);
     WsHeader *hdr = p.hdr;
 
-    if (warp == 8) {
+    if (warp == L::kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(bar + kTmemSlot),
                      "r"(kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -392,16 +418,19 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar + kBarSFull + 8u * i, 1);
-            mbar_init(bar + kBarPFull + 8u * i, kGroup);
+            mbar_init(bar + kBarPFull + 8u * i, kGroup / 32);
+            mbar_init(bar + kBarPvDone + 8u * i, 1);
         }
-        mbar_init(bar + kBarPvDone, 1);
-        mbar_init(bar + kBarPvDone + 8u, 1);
+        mbar_init(bar + kBarSFree, kGroup / 32);
+        mbar_init(bar + kBarSFree + 8u, kGroup / 32);
         mbar_init(bar + kBarQFull, kStage);
         mbar_init(bar + kBarQEmpty, 1);
-        mbar_init(bar + kBarReady, (uint32_t)(kSoft * w.split));
-        // 2 s parts of each of the CTA's 128 / s rows
-        mbar_init(bar + kBarPush, (uint32_t)kSoft);
+        // one arrival a warp: of every softmax warp of the unit's CTAs; of the
+        // warps whose rows this CTA owns (kGroups s parts of 128 / s rows)
+        mbar_init(bar + kBarReady, (uint32_t)(L::kSoft / 32 * w.split));
+        mbar_init(bar + kBarPush, (uint32_t)L::kSoft / 32);
         mbar_init(bar + kBarDrain, 1);
+        mbar_init(bar + kBarDrain + 8u, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -412,22 +441,21 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
     cluster_arrive();   // the peers' barriers are initialised before the first remote arrival
     bool joined = false;
 
-    if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kStageRegs));
-        if (warp > 8) {
+    if (warp >= L::kMmaWarp) {
+        if (warp > L::kMmaWarp + 1) {
             // ---- staging
-            const int t = (int)threadIdx.x - (kSoft + 32);
+            const int t = (int)threadIdx.x - (L::kSoft + 64);
             const int nk = p.dh >> 3, nkv = args.dhp >> 3;   // 8-channel vectors of a query row; padded to 16 channels
             constexpr int kPer = (kKeys * KD / 8 + kStage - 1) / kStage;   // vectors of K, and of V, a thread
             constexpr int kSets = 2;   // chunks on their way while one is converted
-            Stager<kPer, kSets> K, V;
+            Stager<kPer, kSets, kKeys> K, V;
             K.init(t, nkv, args.dkv, nk, p.D, p.kfmt, L::kKvAtom);
             V.init(t, p.dvh >> 3, args.dvv, p.dvh >> 3, p.Dv, p.vfmt, L::kKvAtom);
             int it = 0, st = 0, nu = 0;
             uint32_t ph = 1;
             bool ok = true;
             for (int u = w.u_first; ok && u < w.units; u += w.u_step) {
-                const Unit x = unit_at(p, w, u);
+                const Unit x = unit_at<kKeys>(p, w, u);
                 const int n = x.c_hi - x.c_lo;
                 if (n <= 0)
                     continue;
@@ -437,16 +465,20 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
                 const float *ks = p.ks + row0 * p.kng + x.head * p.dh / p.kgroup;
                 const float *vs = p.vs + row0 * p.vng + x.head * p.dvh / p.vgroup;
                 const int left = x.keys - x.c_lo * kKeys;   // keys from the first chunk on
-                float sr[kSets];
+                constexpr int kSc = (2 * kKeys + kStage - 1) / kStage;
+                float sr[kSets][kSc];
                 auto fetch = [&](int i, auto set) {
                     constexpr int s = decltype(set)::value;
                     const int nkeys = left - i * kKeys;
                     K.template fetch<s>(nkeys);
                     V.template fetch<s>(nkeys);
-                    const int key = t & (kKeys - 1), row = i * kKeys + key;
-                    sr[s] = 0.0f;
-                    if (t < 2 * kKeys && key < nkeys)
-                        sr[s] = t < kKeys ? __ldg(ks + (int64_t)row * p.kng) * args.sc : __ldg(vs + (int64_t)row * p.vng);
+#pragma unroll
+                    for (int e = 0; e < kSc; ++e) {
+                        const int k = t + e * kStage, key = k & (kKeys - 1), row = i * kKeys + key;
+                        sr[s][e] = 0.0f;
+                        if (k < 2 * kKeys && key < nkeys)
+                            sr[s][e] = k < kKeys ? __ldg(ks + (int64_t)row * p.kng) * args.sc : __ldg(vs + (int64_t)row * p.vng);
+                    }
                 };
                 fetch(0, std::integral_constant<int, 0>());
                 if (kSets > 1 && n > 1)
@@ -483,8 +515,10 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
                     const uint32_t kb = sb + L::kOffK + (uint32_t)st * L::kKvStage;
                     K.template store<s>(kb);
                     V.template store<s>(kb + L::kAtoms * L::kKvAtom);
-                    if (t < 2 * kKeys)
-                        sts_f1(sb + L::kOffSc + (uint32_t)st * 512u + (uint32_t)t * 4u, sr[s]);
+#pragma unroll
+                    for (int e = 0; e < kSc; ++e)
+                        if (t + e * kStage < 2 * kKeys)
+                            sts_f1(sb + L::kOffSc + (uint32_t)st * L::kScStage + (uint32_t)(t + e * kStage) * 4u, sr[s][e]);
                     fence_async_smem();
                     mbar_arrive(bar + kBarKvFull + 8u * st);
                     if (i + kSets < n)
@@ -504,199 +538,209 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
             }
             __syncwarp();
         } else {
-            // ---- products
+            // ---- products: one warp the scores, one the weighted values (one warp
+            // for both took about 1300 cycles a job, more than a softmax group)
+            const bool scores = warp == L::kMmaWarp;
             const uint32_t id_s = idesc_bf16(kKeys);
             const int dv0 = min(args.dvp, 64), dv1 = args.dvp - dv0;
             const uint32_t id_o0 = idesc_bf16(dv0) | (1u << 16), id_o1 = idesc_bf16(dv1) | (1u << 16);   // B (V) MN-major
             const int ks0 = min(args.dhp, 64) / 16, ks1 = args.dhp / 16 - ks0;   // 16-channel steps of each block
             const uint64_t qd = desc_sw128(sb + L::kOffQ), q2d = desc_sw128(sb + (w.pairs ? L::kOffQ2 : L::kOffQ));
             const uint64_t kd = desc_sw128(sb + L::kOffK), vd = desc_sw128(sb + L::kOffK + L::kAtoms * L::kKvAtom);
-            int s_st = 0, v_st = 0, nu = 0;   // stage of the next S's chunk, of the next P V's; units so far
-            uint32_t s_ph = 0;
-            uint32_t s_n[2] = {0, 0}, p_n[2] = {0, 0};   // S and P V products of each group so far
+            int st = 0, nu = 0;   // stage of the next job's chunk; units so far
+            uint32_t ph = 0;
+            // jobs of each group so far, mod 4, a byte each.  (The loops are one for
+            // all groups: the warps of an SM share a small instruction cache, and
+            // these instructions are on the path of every job.)
+            uint32_t done = 0;
             bool ok = true;
             for (int u = w.u_first; ok && u < w.units; u += w.u_step) {
-                const Unit x = unit_at(p, w, u);
-                // job j: group j mod 2 on chunk j, or on chunk j / 2 when the
-                // groups take a block each
+                const Unit x = unit_at<kKeys>(p, w, u);
+                // job j of the unit: group j mod 2; chunk j, or chunk j / 2 of block
+                // j mod 2
                 const int jobs = (x.c_hi - x.c_lo) << w.pairs;
                 if (jobs <= 0)
                     continue;
-                if (!wait_w<false>(bar + kBarQFull, nu & 1, abort_flag, hdr, kSiteQFull))
+                if (scores && !wait_w<false>(bar + kBarQFull, nu & 1, abort_flag, hdr, kSiteQFull)) {
+                    ok = false;
                     break;
-                ++nu;
-                // (the groups' loops are written out: their counters stay in registers)
-                auto issue_s = [&](int j, auto group) -> bool {
-                    constexpr int g = decltype(group)::value;
-                    const uint32_t b = s_n[g]++ & 1;
-                    if (!wait_w<false>(bar + kBarKvFull + 8u * s_st, s_ph, abort_flag, hdr, kSiteKvFull))
-                        return false;
-                    tc_fence_after();
-                    const uint32_t d = tmem + 128u * g + 64u * b;
-                    const uint64_t ad = g ? q2d : qd, bd = kd + (uint64_t)((uint32_t)s_st * (L::kKvStage >> 4));
-                    mma_s_w(d, ad, bd, id_s, 0, ks0);
-                    if (KD > 64 && ks1 > 0)
-                        mma_s_w(d, ad + (L::kQAtom >> 4), bd + (L::kKvAtom >> 4), id_s, 1, ks1);
-                    tc_commit_w(bar + kBarSFull + 16u * g + 8u * b);
-                    if (j + 1 == jobs)
-                        tc_commit_w(bar + kBarQEmpty);
-                    if (!w.pairs || g == 1) {
-                        if (++s_st == L::kStages) {
-                            s_st = 0;
-                            s_ph ^= 1;
-                        }
-                    }
-                    return true;
-                };
-                auto issue_pv = [&](int j, auto group) -> bool {
-                    constexpr int g = decltype(group)::value;
-                    const uint32_t n = p_n[g]++, b = n & 1;
-                    if (!wait_w<false>(bar + kBarPFull + 16u * g + 8u * b, (n >> 1) & 1, abort_flag, hdr, kSitePFull))
-                        return false;
-                    tc_fence_after();
-                    const uint32_t d = tmem + kTmemO + 128u * g, pa = tmem + 128u * g + 64u * b;
-                    const uint64_t bd = vd + (uint64_t)((uint32_t)v_st * (L::kKvStage >> 4));
-                    mma_pv_w(d, pa, bd, id_o0, j > 1);
-                    if (KD > 64 && dv1 > 0)
-                        mma_pv_w(d + 64u, pa, bd + (L::kKvAtom >> 4), id_o1, j > 1);
-                    tc_commit_w(bar + kBarPvDone + 8u * g);
-                    if (!w.pairs || g == 1) {
-                        tc_commit_w(bar + kBarKvEmpty + 8u * v_st);
-                        if (++v_st == L::kStages)
-                            v_st = 0;
-                    }
-                    return true;
-                };
-                using G0 = std::integral_constant<int, 0>;
-                using G1 = std::integral_constant<int, 1>;
-                for (int j = 0; ok && j < min(L::kAhead, jobs); j += 2) {
-                    ok = issue_s(j, G0());
-                    if (ok && j + 1 < jobs)
-                        ok = issue_s(j + 1, G1());
                 }
-                for (int j = 0; ok && j < jobs; j += 2) {
-                    ok = issue_pv(j, G0()) && (j + L::kAhead >= jobs || issue_s(j + L::kAhead, G0()));
-                    if (ok && j + 1 < jobs)
-                        ok = issue_pv(j + 1, G1()) && (j + 1 + L::kAhead >= jobs || issue_s(j + 1 + L::kAhead, G1()));
+                ++nu;
+#pragma unroll 1
+                for (int j = 0; j < jobs; ++j) {
+                    const uint32_t g = (uint32_t)j & 1u, n = (done >> (8 * g)) & 3u;
+                    const uint32_t b = n & (L::kBufs - 1), buf = L::kBufs * g + b, par = (n / L::kBufs) & 1u;
+                    done = (done + (1u << (8 * g))) & 0x03030303u;
+                    if (scores) {
+                        // (the group has read its last S, or the P V of the
+                        // buffer's last job has landed)
+                        if (!wait_w<false>(bar + kBarKvFull + 8u * st, ph, abort_flag, hdr, kSiteKvFull) ||
+                            !wait_w<false>(bar + (L::kApart ? kBarSFree + 8u * g : kBarPvDone + 8u * buf), par ^ 1u, abort_flag,
+                                           hdr, kSiteFree)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t ad = g ? q2d : qd, bd = kd + (uint64_t)((uint32_t)st * (L::kKvStage >> 4));
+                        const uint32_t d = tmem + L::tmem_s(g, b);
+                        mma_s_w(d, ad, bd, id_s, 0, ks0);
+                        if (KD > 64 && ks1 > 0)
+                            mma_s_w(d, ad + (L::kQAtom >> 4), bd + (L::kKvAtom >> 4), id_s, 1, ks1);
+                        tc_commit_w(bar + kBarSFull + 8u * buf);
+                        if (j + 1 == jobs)
+                            tc_commit_w(bar + kBarQEmpty);
+                    } else {
+                        if (!wait_w<false>(bar + kBarPFull + 8u * buf, par, abort_flag, hdr, kSitePFull)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t d = tmem + L::tmem_o(g), pa = tmem + L::tmem_p(g, b);
+                        const uint64_t bd = vd + (uint64_t)((uint32_t)st * (L::kKvStage >> 4));
+#pragma unroll
+                        for (int k = 0; k < kKeys / 64; ++k) {
+                            mma_pv_w(d, pa + 32u * k, bd + 512u * k, id_o0, j >= 2 || k > 0);
+                            if (KD > 64 && dv1 > 0)
+                                mma_pv_w(d + 64u, pa + 32u * k, bd + (L::kKvAtom >> 4) + 512u * k, id_o1, j >= 2 || k > 0);
+                        }
+                        tc_commit_w(bar + kBarPvDone + 8u * buf);
+                        if (!w.pairs || g)
+                            tc_commit_w(bar + kBarKvEmpty + 8u * st);
+                    }
+                    if (!w.pairs || g) {
+                        ph ^= st + 1 == L::kStages;
+                        st = st + 1 == L::kStages ? 0 : st + 1;
+                    }
                 }
             }
             if (!ok) {
                 // the products in flight finish before this CTA's memory is given up
-                tc_commit_w(bar + kBarDrain);
+                const uint32_t drain = bar + kBarDrain + (scores ? 0u : 8u);
+                tc_commit_w(drain);
                 const long long t0 = clock64();
-                while (!mbar_try(bar + kBarDrain, 0) && clock64() - t0 < kWaitCycles / 64)
+                while (!mbar_try(drain, 0) && clock64() - t0 < kWaitCycles / 64)
                     ;
             }
             __syncwarp();
         }
     } else {
         // ---- softmax: thread = query row r of group g
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        constexpr int kG = 2, kSoft = L::kSoft;
         const int g = warp >> 2;
         const int r = (warp & 3) * 32 + lane;
         const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t t_s = t_row + 128u * g, t_o = t_row + kTmemO + 128u * g;
+        const uint32_t t_o = t_row + L::tmem_o(g);
         const int ng = p.dvh >> 3;             // 8-channel groups of an output row
-        int chunk = 0, m_it = 0;               // chunks of the CTA so far; of this group
+        int chunk = 0, m_it = 0;               // chunks of the CTA so far; jobs of this group
         bool ok = true;
         for (int u = w.u_first; u < w.units; u += w.u_step) {
-            const Unit x = unit_at(p, w, u);
-            const int n = (x.c_hi - x.c_lo) << w.pairs;   // jobs, those of parity g are this group's
+            const Unit x = unit_at<kKeys>(p, w, u);
+            const int n = (x.c_hi - x.c_lo) << w.pairs;   // jobs, every kG-th from g on this group's
             float m_used = -INFINITY, l = 0.0f;
             // one job; kTail: its chunk is the item's last, with keys to mask
             auto one = [&](int i, auto tail) {
                 constexpr bool kTail = decltype(tail)::value;
+                const int ci = chunk + (i >> w.pairs), b = m_it & (L::kBufs - 1);
                 const int kvalid = x.keys - (x.c_lo + (i >> w.pairs)) * kKeys;
-                const int b = m_it & 1;
                 // (the staged scales are seen through the stage's own barrier; its
                 // next phase waits for this chunk's P V)
-                const int ci = chunk + (i >> w.pairs);
                 if (!wait_w<false>(bar + kBarKvFull + 8u * (ci % L::kStages), (ci / L::kStages) & 1, abort_flag, hdr, kSiteKvFull) ||
-                    !wait_w<false>(bar + kBarSFull + 16u * g + 8u * b, (m_it >> 1) & 1, abort_flag, hdr, kSiteSFull)) {
+                    !wait_w<false>(bar + kBarSFull + 8u * (L::kBufs * g + b), (m_it / L::kBufs) & 1, abort_flag, hdr, kSiteSFull)) {
                     ok = false;
                     return;
                 }
                 tc_fence_after();
-                const uint32_t sc = sb + L::kOffSc + (uint32_t)(ci % L::kStages) * 512u;
-                // scores in pairs (the packed float32 instructions: half as many)
-                uint64_t sv[kKeys / 2];
+                const uint32_t sc = sb + L::kOffSc + (uint32_t)(ci % L::kStages) * L::kScStage;
+                const uint32_t t_s = t_row + L::tmem_s(g, b), t_p = t_row + L::tmem_p(g, b);
+                // (packed float32 instructions: half as many)
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
+#pragma unroll 1
+                for (int h = 0; h < kKeys / 32; ++h) {
                     uint32_t sr[32];
-                    ld32(t_s + 64u * b + 32u * h, sr);
+                    ld32(t_s + 32u * h, sr);
                     ld_wait();
 #pragma unroll
                     for (int k = 0; k < 32; k += 4) {
                         const ulonglong2 s4 = lds_2x2(sc + 4u * (32 * h + k));
-                        sv[16 * h + k / 2] = mul2(pair(sr[k], sr[k + 1]), s4.x);
-                        sv[16 * h + k / 2 + 1] = mul2(pair(sr[k + 2], sr[k + 3]), s4.y);
-                    }
-                }
-                if constexpr (kTail) {
+                        const uint64_t a = mul2(pair(sr[k], sr[k + 1]), s4.x), c = mul2(pair(sr[k + 2], sr[k + 3]), s4.y);
+                        const float v[4] = {lo_of(a), hi_of(a), lo_of(c), hi_of(c)};
 #pragma unroll
-                    for (int k = 0; k < kKeys; k += 2) {
-                        if (k >= kvalid)
-                            sv[k / 2] = 0xFF800000FF800000ull;   // two -inf
-                        else if (k + 1 >= kvalid)
-                            sv[k / 2] = (sv[k / 2] & 0xFFFFFFFFull) | 0xFF80000000000000ull;
+                        for (int e = 0; e < 4; ++e)
+                            if (!kTail || 32 * h + k + e < kvalid)
+                                mx[e] = fmaxf(mx[e], v[e]);
                     }
-                }
-#pragma unroll
-                for (int k = 0; k < kKeys / 2; ++k) {
-                    mx[(2 * k) & 3] = fmaxf(mx[(2 * k) & 3], lo_of(sv[k]));
-                    mx[(2 * k + 1) & 3] = fmaxf(mx[(2 * k + 1) & 3], hi_of(sv[k]));
                 }
                 const float t_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 // the exponent base moves only when the maximum has grown by
                 // more than 8 (weights <= 2^8 otherwise)
                 const bool grow = t_max > m_used + 8.0f;
                 const float m_new = grow ? t_max : m_used;
-                const float corr = ex2(m_used - m_new);   // 0 on the group's first chunk, 1 when kept
-                const uint64_t nm = pair(__float_as_uint(-m_new), __float_as_uint(-m_new));
-                uint64_t ls[2] = {0, 0};
-                uint32_t pk[32];
-#pragma unroll
-                for (int k = 0; k < kKeys; k += 4) {
-                    const ulonglong2 v4 = lds_2x2(sc + 256u + 4u * k);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint64_t d = add2(sv[k / 2 + h], nm);
-                        const uint64_t e = pair(__float_as_uint(ex2(lo_of(d))), __float_as_uint(ex2(hi_of(d))));
-                        ls[h] = add2(ls[h], e);
-                        const uint64_t q = mul2(e, h ? v4.y : v4.x);
-                        pk[k / 2 + h] = pack_bf16x2(lo_of(q), hi_of(q));
+                const float corr = ex2(m_used - m_new);   // 0 on the group's first job, 1 when kept
+                // the group's previous P V has landed: P may be written, O rescaled.
+                // (Each phase of the barrier is waited for in turn: a parity tells
+                // two neighbouring phases apart, no more.)
+                if (i >= kG) {
+                    const int pb = (m_it - 1) & (L::kBufs - 1);
+                    if (!wait_w<false>(bar + kBarPvDone + 8u * (L::kBufs * g + pb), ((m_it - 1) / L::kBufs) & 1, abort_flag, hdr,
+                                       kSitePvDone)) {
+                        ok = false;
+                        return;
                     }
-                }
-                st32(t_s + 64u * b, pk);   // over the scores just read
-                l = l * corr + ((lo_of(ls[0]) + hi_of(ls[0])) + (lo_of(ls[1]) + hi_of(ls[1])));
-                // the group's previous P V has landed (each of its phases is waited
-                // for in turn: a parity tells two neighbouring phases apart, no more)
-                if (i > 1 && !wait_w<false>(bar + kBarPvDone + 8u * g, (m_it - 1) & 1, abort_flag, hdr, kSitePvDone)) {
-                    ok = false;
-                    return;
-                }
-                if (i > 1 && __any_sync(0xFFFFFFFFu, grow)) {
-                    // rescale this warp's O rows
                     tc_fence_after();
-#pragma unroll
-                    for (int pc = 0; pc < KD / 16; ++pc) {
-                        if (pc * 16 < args.dvp) {
+                    if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll 1
+                        for (int pc = 0; pc < args.dvp; pc += 16) {
                             float v[16];
-                            tmem_ld16(t_o + 16u * pc, v);
+                            tmem_ld16(t_o + (uint32_t)pc, v);
 #pragma unroll
                             for (int q = 0; q < 16; ++q)
                                 v[q] *= corr;
-                            st16(t_o + 16u * pc, v);
+                            st16(t_o + (uint32_t)pc, v);
                         }
                     }
                 }
+                const uint64_t nm = pair(__float_as_uint(-m_new), __float_as_uint(-m_new));
+                uint64_t ls[2] = {0, 0};
+#pragma unroll 1
+                for (int h = 0; h < kKeys / 32; ++h) {
+                    uint32_t sr[32], pk[16];
+                    ld32(t_s + 32u * h, sr);
+                    ld_wait();
+                    if (L::kApart && h == kKeys / 32 - 1) {   // the next S may come
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(bar + kBarSFree + 8u * g);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        const ulonglong2 s4 = lds_2x2(sc + 4u * (32 * h + k)), v4 = lds_2x2(sc + 4u * (kKeys + 32 * h + k));
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            const int kk = 32 * h + k + 2 * f;
+                            const uint64_t d = fma2(pair(sr[k + 2 * f], sr[k + 2 * f + 1]), f ? s4.y : s4.x, nm);
+                            uint32_t e0 = __float_as_uint(ex2(lo_of(d))), e1 = __float_as_uint(ex2(hi_of(d)));
+                            if (kTail) {
+                                e0 = kk < kvalid ? e0 : 0;
+                                e1 = kk + 1 < kvalid ? e1 : 0;
+                            }
+                            const uint64_t e = pair(e0, e1);
+                            ls[f] = add2(ls[f], e);
+                            const uint64_t q = mul2(e, f ? v4.y : v4.x);
+                            pk[k / 2 + f] = pack_bf16x2(lo_of(q), hi_of(q));
+                        }
+                    }
+                    st16u(t_p + 16u * h, pk);   // (over scores that have been read, where P is not apart)
+                }
+                l = l * corr + ((lo_of(ls[0]) + hi_of(ls[0])) + (lo_of(ls[1]) + hi_of(ls[1])));
                 st_wait();
                 tc_fence_before();
-                mbar_arrive(bar + kBarPFull + 16u * g + 8u * b);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar + kBarPFull + 8u * (L::kBufs * g + b));
                 m_used = m_new;
             };
-            for (int i = g; ok && i < n; i += 2, ++m_it) {
+            for (int i = g; ok && i < n; i += kG, ++m_it) {
                 if (x.keys - (x.c_lo + (i >> w.pairs)) * kKeys >= kKeys)
                     one(i, std::false_type());
                 else
@@ -706,148 +750,142 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
             // the group's last P V of the unit has landed
             const bool mine = n > g;
             if (ok && mine)
-                ok = wait_w<false>(bar + kBarPvDone + 8u * g, (m_it - 1) & 1, abort_flag, hdr, kSitePvDone);
+                ok = wait_w<false>(bar + kBarPvDone + 8u * (L::kBufs * g + ((m_it - 1) & (L::kBufs - 1))), ((m_it - 1) / L::kBufs) & 1,
+                                   abort_flag, hdr, kSitePvDone);
             tc_fence_after();
-            if (w.pairs) {
-                // ---- the group's block of queries: its rows are finished
-                const int slot = x.slot0 + g * kRows + r;
-                const int64_t pix = slot < w.slots ? query_pixel(p, x.n, slot) : -1;
+            if (w.split > 1) {
+                // ---- merge of a split unit's kG s partial rows: each is pushed to
+                // the CTA that owns the row, over the memory of the ring, once
+                // every CTA of the unit has finished its products
+                const int s = w.split, rows = kRows / s;   // (32 or more: a warp's rows have one owner)
+                if (!joined) {
+                    cluster_wait();
+                    joined = true;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane < s)
+                    mbar_arrive_peer(map_peer(bar + kBarReady, (uint32_t)(w.base + lane)));
+                ok = wait_w<true>(bar + kBarReady, 0, abort_flag, hdr, kSiteReady) && ok;
                 if (!ok)
                     continue;
-                const float inv = mine ? 1.0f / l : 0.0f;   // (no key at all: zeros)
-#pragma unroll
-                for (int pc = 0; pc < KD / 16; ++pc) {
-                    if (pc * 16 < args.dvp) {
+                {
+                    const int owner = r / rows;
+                    const uint32_t slot = (uint32_t)((w.rank_split * kG + g) * rows + (r - owner * rows));   // of kSoft
+                    const uint32_t dst = map_peer(sb + L::kOffPush + slot * 16u, (uint32_t)(w.base + owner));
+#pragma unroll 1
+                    for (int pc = 0; pc < args.dvp; pc += 16) {
                         float v[16];
                         if (mine)
-                            tmem_ld16(t_o + 16u * pc, v);
+                            tmem_ld16(t_o + (uint32_t)pc, v);
 #pragma unroll
-                        for (int q = 0; q < 16; ++q)
-                            v[q] = mine ? v[q] : 0.0f;
-                        __nv_bfloat16 *dst = p.o + pix * p.Dv + x.head * p.dvh + 16 * pc;
-                        if (pix >= 0)
-                            store8(dst, v, inv);
-                        if (pix >= 0 && 2 * pc + 1 < ng)
-                            store8(dst + 8, v + 8, inv);
+                        for (int q = 0; q < 4; ++q)
+                            st_peer_f32x4(dst + (uint32_t)(pc / 4 + q) * (kSoft * 16u), mine ? v[4 * q] : 0.0f,
+                                          mine ? v[4 * q + 1] : 0.0f, mine ? v[4 * q + 2] : 0.0f, mine ? v[4 * q + 3] : 0.0f);
                     }
+                    st_peer_f32x2(map_peer(sb + L::kOffMl + slot * 8u, (uint32_t)(w.base + owner)), m_used, mine ? l : -1.0f);
+                    __syncwarp();   // the warp's pushes, then one arrival that releases them
+                    if (lane == 0)
+                        mbar_arrive_peer(map_peer(bar + kBarPush, (uint32_t)(w.base + owner)));
+                }
+                if (!wait_w<true>(bar + kBarPush, 0, abort_flag, hdr, kSitePush)) {
+                    ok = false;
+                    continue;
+                }
+                for (int item = (int)threadIdx.x; item < rows * ng; item += kSoft) {
+                    const int j = item % rows, gi = item / rows;
+                    const int slot = x.slot0 + w.rank_split * rows + j;
+                    const int64_t pix = slot < w.slots ? query_pixel(p, x.n, slot) : -1;
+                    if (pix < 0)
+                        continue;
+                    float mm = -INFINITY;
+                    for (int i = 0; i < kG * s; ++i)
+                        mm = fmaxf(mm, lds_f2(sb + L::kOffMl + (uint32_t)(i * rows + j) * 8u).x);
+                    float sum = 0.0f, acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                    for (int i = 0; i < kG * s; ++i) {
+                        const float2 ml = lds_f2(sb + L::kOffMl + (uint32_t)(i * rows + j) * 8u);
+                        if (ml.y == -1.0f)   // a part without a chunk
+                            continue;
+                        const float wt = ex2(ml.x - mm);
+                        sum = fmaf(ml.y, wt, sum);
+                        const uint32_t src = sb + L::kOffPush + (uint32_t)(i * rows + j) * 16u + (uint32_t)(2 * gi) * (kSoft * 16u);
+                        const float4 y0 = lds_f4(src), y1 = lds_f4(src + kSoft * 16u);
+                        acc[0] = fmaf(wt, y0.x, acc[0]); acc[1] = fmaf(wt, y0.y, acc[1]);
+                        acc[2] = fmaf(wt, y0.z, acc[2]); acc[3] = fmaf(wt, y0.w, acc[3]);
+                        acc[4] = fmaf(wt, y1.x, acc[4]); acc[5] = fmaf(wt, y1.y, acc[5]);
+                        acc[6] = fmaf(wt, y1.z, acc[6]); acc[7] = fmaf(wt, y1.w, acc[7]);
+                    }
+                    store8(p.o + pix * p.Dv + x.head * p.dvh + 8 * gi, acc, x.keys > 0 ? 1.0f / sum : 0.0f);
+                }
+                continue;
+            }
+            // ---- the unit's rows
+            const int slot = x.slot0 + (w.pairs ? (g & 1) * kRows : 0) + r;
+            const int64_t pix = slot < w.slots ? query_pixel(p, x.n, slot) : -1;
+            __nv_bfloat16 *dst = p.o + pix * p.Dv + x.head * p.dvh;
+            if (w.pairs) {   // a block each: nothing to merge
+                const float inv = mine ? 1.0f / l : 0.0f;   // (no key at all: zeros)
+#pragma unroll 1
+                for (int pc = 0; pc < args.dvp && ok; pc += 16) {
+                    float v[16];
+                    if (mine)
+                        tmem_ld16(t_o + (uint32_t)pc, v);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        v[q] = mine ? v[q] : 0.0f;
+                    if (pix >= 0)
+                        store8(dst + pc, v, inv);
+                    if (pix >= 0 && pc / 8 + 1 < ng)
+                        store8(dst + pc + 8, v + 8, inv);
                 }
                 tc_fence_before();
                 continue;
             }
-            if (w.split == 1) {
-                // ---- merge of the two groups: each thread finishes the 8-channel
-                // groups of its parity of its row, from the other's copy of them
-                soft_sync();   // the previous unit's rows have been read
-                float o[KD / 2];   // this thread's own groups
-                if (ok) {
+            // the two groups share the block: each keeps the 8-channel groups of
+            // its parity and merges them with the other's copy of them
+            float o[KD / 2];
+            const int tid = (int)threadIdx.x, pt = (g ^ 1) * kGroup + r;
+            soft_sync<kSoft>();   // the last unit's rows have been read
 #pragma unroll
-                    for (int pc = 0; pc < KD / 16; ++pc) {
-                        if (pc * 16 < args.dvp) {
-                            float v[16];
-                            if (mine)
-                                tmem_ld16(t_o + 16u * pc, v);
+            for (int k = 0; k < KD / 16; ++k) {
+                float v[16];
+                const bool in = ok && mine && 16 * k < args.dvp;
+                if (in)
+                    tmem_ld16(t_o + 16u * k, v);
+                const uint32_t at = sb + L::kOffX + (uint32_t)(2 * k * kSoft + tid) * 16u;
+                float m[8];
 #pragma unroll
-                            for (int q = 0; q < 8; ++q) {
-                                const float a = mine ? v[q] : 0.0f, c = mine ? v[8 + q] : 0.0f;
-                                o[8 * pc + q] = g == 0 ? a : c;   // even groups stay with group 0
-                                v[q] = g == 0 ? c : a;
-                            }
-                            const uint32_t dst = sb + L::kOffX + (uint32_t)((g * (KD / 16) + pc) * 2 * kRows + r) * 16u;
-                            sts_f4(dst, v);
-                            sts_f4(dst + kRows * 16u, v + 4);
-                        }
-                    }
-                    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sb + L::kOffMl + (uint32_t)(g * kRows + r) * 8u),
-                                 "f"(m_used), "f"(l) : "memory");
-                    tc_fence_before();
+                for (int q = 0; q < 8; ++q) {
+                    const float a = in ? v[q] : 0.0f, c = in ? v[8 + q] : 0.0f;
+                    m[q] = g ? a : c;
+                    o[8 * k + q] = g ? c : a;
                 }
-                soft_sync();
-                const int slot = x.slot0 + r;
-                const int64_t pix = slot < w.slots ? query_pixel(p, x.n, slot) : -1;
-                if (ok && pix >= 0) {
-                    const float2 ml = lds_f2(sb + L::kOffMl + (uint32_t)((1 - g) * kRows + r) * 8u);
-                    const float mm = fmaxf(m_used, ml.x);
-                    // a group without a chunk has weight 0 (and no key at all leaves zeros)
-                    const float wa = mine ? ex2(m_used - mm) : 0.0f, wb = n > 1 - g ? ex2(ml.x - mm) : 0.0f;
-                    const float inv = n > 0 ? 1.0f / (l * wa + ml.y * wb) : 0.0f;
-#pragma unroll
-                    for (int pc = 0; pc < KD / 16; ++pc) {
-                        const int gi = 2 * pc + g;
-                        if (gi < ng) {
-                            const uint32_t src = sb + L::kOffX + (uint32_t)(((1 - g) * (KD / 16) + pc) * 2 * kRows + r) * 16u;
-                            const float4 y0 = lds_f4(src), y1 = lds_f4(src + kRows * 16u);
-                            float *oo = o + 8 * pc;
-                            oo[0] = fmaf(y0.x, wb, oo[0] * wa); oo[1] = fmaf(y0.y, wb, oo[1] * wa);
-                            oo[2] = fmaf(y0.z, wb, oo[2] * wa); oo[3] = fmaf(y0.w, wb, oo[3] * wa);
-                            oo[4] = fmaf(y1.x, wb, oo[4] * wa); oo[5] = fmaf(y1.y, wb, oo[5] * wa);
-                            oo[6] = fmaf(y1.z, wb, oo[6] * wa); oo[7] = fmaf(y1.w, wb, oo[7] * wa);
-                            store8(p.o + pix * p.Dv + x.head * p.dvh + 8 * gi, oo, inv);
-                        }
-                    }
-                }
-                continue;
-            }
-            // ---- merge of a split unit's 2 s partial rows: each is pushed to the
-            // CTA that owns the row, over the memory of the ring, once every CTA
-            // of the unit has finished its products
-            const int s = w.split, rows = kRows / s;
-            if (!joined) {
-                cluster_wait();
-                joined = true;
+                sts_f4(at, m);
+                sts_f4(at + kSoft * 16u, m + 4);
             }
             tc_fence_before();
-            for (int i = 0; i < s; ++i)
-                mbar_arrive_peer(map_peer(bar + kBarReady, (uint32_t)(w.base + i)));
-            ok = ok && wait_w<true>(bar + kBarReady, 0, abort_flag, hdr, kSiteReady);
-            if (!ok)
-                continue;
-            {
-                const int owner = r / rows;
-                const uint32_t slot = (uint32_t)((w.rank_split * 2 + g) * rows + (r - owner * rows));   // of 256
-                const uint32_t dst = map_peer(sb + L::kOffPush + slot * 16u, (uint32_t)(w.base + owner));
+            // (a sum of -1: no key)
+            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sb + L::kOffMl + (uint32_t)tid * 8u), "f"(m_used),
+                         "f"(mine ? l : -1.0f) : "memory");
+            soft_sync<kSoft>();
+            const float2 ml = lds_f2(sb + L::kOffMl + (uint32_t)pt * 8u);
+            const bool other = ml.y != -1.0f;
+            const float mm = fmaxf(mine ? m_used : -INFINITY, other ? ml.x : -INFINITY);
+            const float wa = mine ? ex2(m_used - mm) : 0.0f, wb = other ? ex2(ml.x - mm) : 0.0f;
+            const float sum = (mine ? l * wa : 0.0f) + (other ? ml.y * wb : 0.0f);
+            const float inv = mine || other ? 1.0f / sum : 0.0f;   // (no key at all: zeros)
 #pragma unroll
-                for (int pc = 0; pc < KD / 16; ++pc) {
-                    if (pc * 16 < args.dvp) {
-                        float v[16];
-                        if (mine)
-                            tmem_ld16(t_o + 16u * pc, v);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            st_peer_f32x4(dst + (uint32_t)(4 * pc + q) * 4096u, mine ? v[4 * q] : 0.0f, mine ? v[4 * q + 1] : 0.0f,
-                                          mine ? v[4 * q + 2] : 0.0f, mine ? v[4 * q + 3] : 0.0f);
-                    }
+            for (int k = 0; k < KD / 16; ++k) {
+                if (ok && pix >= 0 && 2 * k + g < ng) {
+                    const uint32_t src = sb + L::kOffX + (uint32_t)(2 * k * kSoft + pt) * 16u;
+                    const float4 y0 = lds_f4(src), y1 = lds_f4(src + kSoft * 16u);
+                    float *oo = o + 8 * k;
+                    oo[0] = fmaf(y0.x, wb, oo[0] * wa); oo[1] = fmaf(y0.y, wb, oo[1] * wa);
+                    oo[2] = fmaf(y0.z, wb, oo[2] * wa); oo[3] = fmaf(y0.w, wb, oo[3] * wa);
+                    oo[4] = fmaf(y1.x, wb, oo[4] * wa); oo[5] = fmaf(y1.y, wb, oo[5] * wa);
+                    oo[6] = fmaf(y1.z, wb, oo[6] * wa); oo[7] = fmaf(y1.w, wb, oo[7] * wa);
+                    store8(dst + 8 * (2 * k + g), oo, inv);
                 }
-                st_peer_f32x2(map_peer(sb + L::kOffMl + slot * 8u, (uint32_t)(w.base + owner)), m_used, mine ? l : -1.0f);
-                mbar_arrive_peer(map_peer(bar + kBarPush, (uint32_t)(w.base + owner)));   // releases the pushes
-            }
-            if (!wait_w<true>(bar + kBarPush, 0, abort_flag, hdr, kSitePush)) {
-                ok = false;
-                continue;
-            }
-            for (int item = (int)threadIdx.x; item < rows * ng; item += kSoft) {
-                const int j = item % rows, gi = item / rows;
-                const int slot = x.slot0 + w.rank_split * rows + j;
-                const int64_t pix = slot < w.slots ? query_pixel(p, x.n, slot) : -1;
-                if (pix < 0)
-                    continue;
-                float mm = -INFINITY;
-                for (int i = 0; i < 2 * s; ++i)
-                    mm = fmaxf(mm, lds_f2(sb + L::kOffMl + (uint32_t)(i * rows + j) * 8u).x);
-                float sum = 0.0f, acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                for (int i = 0; i < 2 * s; ++i) {
-                    const float2 ml = lds_f2(sb + L::kOffMl + (uint32_t)(i * rows + j) * 8u);
-                    if (ml.y == -1.0f)   // a part without a chunk
-                        continue;
-                    const float wt = ex2(ml.x - mm);
-                    sum = fmaf(ml.y, wt, sum);
-                    const uint32_t src = sb + L::kOffPush + (uint32_t)(i * rows + j) * 16u + (uint32_t)(2 * gi) * 4096u;
-                    const float4 y0 = lds_f4(src), y1 = lds_f4(src + 4096u);
-                    acc[0] = fmaf(wt, y0.x, acc[0]); acc[1] = fmaf(wt, y0.y, acc[1]);
-                    acc[2] = fmaf(wt, y0.z, acc[2]); acc[3] = fmaf(wt, y0.w, acc[3]);
-                    acc[4] = fmaf(wt, y1.x, acc[4]); acc[5] = fmaf(wt, y1.y, acc[5]);
-                    acc[6] = fmaf(wt, y1.z, acc[6]); acc[7] = fmaf(wt, y1.w, acc[7]);
-                }
-                store8(p.o + pix * p.Dv + x.head * p.dvh + 8 * gi, acc, x.keys > 0 ? 1.0f / sum : 0.0f);
             }
         }
     }
@@ -855,7 +893,7 @@ __global__ void __launch_bounds__(at::kThreads, 1) k_attn_qcache_tc(const __grid
         cluster_wait();
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == L::kMmaWarp) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
     }
@@ -885,7 +923,7 @@ static int launch_kd(const at::Args &a, int64_t units_max, cudaStream_t stream)
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.blockDim = dim3(at::kThreads);
+    cfg.blockDim = dim3(at::Lay<KD>::kThreads);
     cfg.dynamicSmemBytes = at::Lay<KD>::kBytes;
     cfg.stream = stream;
     cfg.attrs = attr;
