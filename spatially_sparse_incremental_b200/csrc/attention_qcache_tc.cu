@@ -14,7 +14,7 @@
 //     first product, MN-major for the second), and the chunk's scales;
 //   * one warp issues S = Q K^T (M 128, N 64) and O += P V (M 128, K 64);
 //   * four groups of four warps (heads up to 64; two groups for wider ones) do
-//     the softmax, one query row a thread, taking (block, chunk) jobs in turn:
+//     the softmax, taking (block, chunk) jobs in turn:
 //     running maximum and sum (float32), P = 2^(s - max) * value scale as bf16
 //     over the chunk's own S columns, the O row in tensor memory rescaled only
 //     when the maximum has grown by more than 8 (base 2).  A thread reads its
@@ -43,6 +43,7 @@ constexpr int kGroup = 128;         // threads of a softmax group
 constexpr int kStage = 192;         // staging threads
 constexpr int kCluster = 4;
 constexpr int kMaxStages = 3;
+constexpr float kSlack = 40.0f;     // how far (base 2) a score may lie above the exponent base
 
 // Shared and tensor memory for heads of up to KD (64 or 128) channels.
 template <int KD>
@@ -289,10 +290,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-__device__ __forceinline__ ulonglong2 lds_2x2(uint32_t addr)
+__device__ __forceinline__ uint64_t lds_2(uint32_t addr)
 {
-    ulonglong2 v;
-    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(addr) : "memory");
+    uint64_t v;
+    asm volatile("ld.shared.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
     return v;
 }
 __device__ __forceinline__ void sts_f1(uint32_t addr, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory"); }
@@ -303,15 +304,34 @@ __device__ __forceinline__ void sts_f4(uint32_t addr, const float *v)
 template <int kSoft>
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory"); }
 
-// 16 columns of this warp's 32 tensor-memory lanes.
-__device__ __forceinline__ void st16u(uint32_t taddr, const uint32_t (&v)[16])
+// 16 tensor-memory lanes x 32 columns, spread over a warp as the accumulator
+// fragment of a matrix instruction: register 4 i + e of thread t is lane t / 4
+// (+ 8 for e = 2, 3), column 8 i + 2 (t mod 4) + (e mod 2).
+__device__ __forceinline__ void ld16x32(uint32_t taddr, uint32_t (&r)[16])
 {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-            taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// The same lanes x 16 columns: register 2 i + e is lane t / 4 + 8 e, column
+// 4 i + t mod 4 (pairs of bf16 of ld16x32's columns).
+__device__ __forceinline__ void st16x16(uint32_t taddr, const uint32_t *v)
+{
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// v[j] of a thread is that of row t / 4 + 8 j of the warp's 32: the value of row
+// `lane`.
+__device__ __forceinline__ float of_row(const float (&v)[4], int lane)
+{
+    const int src = (lane & 7) * 4;
+    const float a = __shfl_sync(0xFFFFFFFFu, v[0], src), b = __shfl_sync(0xFFFFFFFFu, v[1], src);
+    const float c = __shfl_sync(0xFFFFFFFFu, v[2], src), d = __shfl_sync(0xFFFFFFFFu, v[3], src);
+    return lane < 16 ? (lane < 8 ? a : b) : (lane < 24 ? c : d);
 }
 
 // Bounded waits by every lane of a warp, inline (a call would keep the
@@ -636,7 +656,14 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
         for (int u = w.u_first; u < w.units; u += w.u_step) {
             const Unit x = unit_at<kKeys>(p, w, u);
             const int n = (x.c_hi - x.c_lo) << w.pairs;   // jobs, every kG-th from g on this group's
-            float m_used = -INFINITY, l = 0.0f;
+            // of rows t / 4 + 8 j of the warp: the exponent base, and the sum over
+            // this thread's keys
+            float mq[4], lq[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                mq[j] = -INFINITY;
+                lq[j] = 0.0f;
+            }
             // one job; kTail: its chunk is the item's last, with keys to mask
             auto one = [&](int i, auto tail) {
                 constexpr bool kTail = decltype(tail)::value;
@@ -652,33 +679,73 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
                 tc_fence_after();
                 const uint32_t sc = sb + L::kOffSc + (uint32_t)(ci % L::kStages) * L::kScStage;
                 const uint32_t t_s = t_row + L::tmem_s(g, b), t_p = t_row + L::tmem_p(g, b);
-                // (packed float32 instructions: half as many)
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-                for (int h = 0; h < kKeys / 32; ++h) {
-                    uint32_t sr[32];
-                    ld32(t_s + 32u * h, sr);
-                    ld_wait();
+                // The scores are read in the fragment layout: a thread has a quarter
+                // of the keys for four rows, so it reads a quarter of the scales,
+                // once for the four.  (With a row a thread every lane reads every
+                // scale: 512 bytes a key pair and warp through shared memory, which
+                // bounded the kernel.)  Packed float32 instructions throughout.
+                const uint32_t sq = sc + 8u * (uint32_t)(lane & 3);
+                const int k0 = 2 * (lane & 3);
+                // One pass: the weights are formed with the exponent base of the
+                // group's jobs so far while the scores' maximum is found.  bf16 and
+                // float32 weights keep their precision up to 2^kSlack above the
+                // base, so the base moves (and the pass is run again) only when the
+                // maximum has grown by more than that, or for the group's first job.
+                float top[4];      // the job's largest score, less the base
+                uint64_t ls[4];    // sums of weights
+                auto pass = [&](auto first) {
+                    constexpr bool kFirst = decltype(first)::value;   // the maximum only, of the scores themselves
+                    uint64_t nm[4];
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        const ulonglong2 s4 = lds_2x2(sc + 4u * (32 * h + k));
-                        const uint64_t a = mul2(pair(sr[k], sr[k + 1]), s4.x), c = mul2(pair(sr[k + 2], sr[k + 3]), s4.y);
-                        const float v[4] = {lo_of(a), hi_of(a), lo_of(c), hi_of(c)};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (!kTail || 32 * h + k + e < kvalid)
-                                mx[e] = fmaxf(mx[e], v[e]);
+                    for (int j = 0; j < 4; ++j) {
+                        nm[j] = kFirst ? 0 : pair(__float_as_uint(-mq[j]), __float_as_uint(-mq[j]));
+                        top[j] = -INFINITY;
+                        ls[j] = 0;
                     }
-                }
-                const float t_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                // the exponent base moves only when the maximum has grown by
-                // more than 8 (weights <= 2^8 otherwise)
-                const bool grow = t_max > m_used + 8.0f;
-                const float m_new = grow ? t_max : m_used;
-                const float corr = ex2(m_used - m_new);   // 0 on the group's first job, 1 when kept
+#pragma unroll 1
+                    for (int h = 0; h < kKeys / 32; ++h) {
+                        uint32_t sr[2][16], pk[2][8];
+                        ld16x32(t_s + 32u * h, sr[0]);
+                        ld16x32(t_s + 32u * h + (16u << 16), sr[1]);
+                        ld_wait();
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint64_t s2 = lds_2(sq + 4u * (32 * h + 8 * q));
+                            const uint64_t v2 = kFirst ? 0 : lds_2(sq + 4u * (kKeys + 32 * h + 8 * q));
+                            const int kk = 32 * h + 8 * q + k0;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t *e = sr[j >> 1] + 4 * q + 2 * (j & 1);
+                                const uint64_t d = kFirst ? mul2(pair(e[0], e[1]), s2) : fma2(pair(e[0], e[1]), s2, nm[j]);
+                                float x0 = lo_of(d), x1 = hi_of(d);
+                                if (kTail) {   // (masked keys: weight 0)
+                                    x0 = kk < kvalid ? x0 : -INFINITY;
+                                    x1 = kk + 1 < kvalid ? x1 : -INFINITY;
+                                }
+                                top[j] = fmaxf(top[j], fmaxf(x0, x1));
+                                if constexpr (!kFirst) {
+                                    const uint64_t w2 = pair(__float_as_uint(ex2(x0)), __float_as_uint(ex2(x1)));
+                                    ls[j] = add2(ls[j], w2);
+                                    const uint64_t y = mul2(w2, v2);
+                                    pk[j >> 1][2 * q + (j & 1)] = pack_bf16x2(lo_of(y), hi_of(y));
+                                }
+                            }
+                        }
+                        if constexpr (!kFirst) {
+                            st16x16(t_p + 16u * h, pk[0]);
+                            st16x16(t_p + 16u * h + (16u << 16), pk[1]);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        top[j] = fmaxf(top[j], __shfl_xor_sync(0xFFFFFFFFu, top[j], 1));
+                        top[j] = fmaxf(top[j], __shfl_xor_sync(0xFFFFFFFFu, top[j], 2));
+                    }
+                };
                 // the group's previous P V has landed: P may be written, O rescaled.
                 // (Each phase of the barrier is waited for in turn: a parity tells
                 // two neighbouring phases apart, no more.)
+                bool again = i < kG;
                 if (i >= kG) {
                     const int pb = (m_it - 1) & (L::kBufs - 1);
                     if (!wait_w<false>(bar + kBarPvDone + 8u * (L::kBufs * g + pb), ((m_it - 1) / L::kBufs) & 1, abort_flag, hdr,
@@ -687,58 +754,63 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
                         return;
                     }
                     tc_fence_after();
+                    if constexpr (L::kApart) {
+                        pass(std::false_type());
+                        again = __any_sync(0xFFFFFFFFu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kSlack);
+                    } else {
+                        again = true;   // (P would lie over scores that are needed again: the maximum first)
+                    }
+                }
+                if (again) {
+                    if (i < kG || !L::kApart) {
+                        pass(std::true_type());
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            top[j] -= i < kG ? 0.0f : mq[j];
+                    }
+                    float corr[4];
+                    bool grow = false;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        // (a first job: from -inf to its maximum; a row whose scores
+                        // are all -inf or NaN keeps a base of -inf)
+                        const bool up = i < kG || top[j] > (L::kApart ? 0.0f : 8.0f);
+                        const float base = i < kG ? top[j] : mq[j] + top[j];
+                        corr[j] = up && i >= kG ? ex2(-top[j]) : 1.0f;
+                        if (up) {
+                            mq[j] = base;
+                            lq[j] *= corr[j];
+                            grow = grow || i >= kG;
+                        }
+                    }
                     if (__any_sync(0xFFFFFFFFu, grow)) {
+                        const float f = of_row(corr, lane);
 #pragma unroll 1
                         for (int pc = 0; pc < args.dvp; pc += 16) {
                             float v[16];
                             tmem_ld16(t_o + (uint32_t)pc, v);
 #pragma unroll
                             for (int q = 0; q < 16; ++q)
-                                v[q] *= corr;
+                                v[q] *= f;
                             st16(t_o + (uint32_t)pc, v);
                         }
                     }
+                    pass(std::false_type());
                 }
-                const uint64_t nm = pair(__float_as_uint(-m_new), __float_as_uint(-m_new));
-                uint64_t ls[2] = {0, 0};
-#pragma unroll 1
-                for (int h = 0; h < kKeys / 32; ++h) {
-                    uint32_t sr[32], pk[16];
-                    ld32(t_s + 32u * h, sr);
-                    ld_wait();
-                    if (L::kApart && h == kKeys / 32 - 1) {   // the next S may come
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(bar + kBarSFree + 8u * g);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        const ulonglong2 s4 = lds_2x2(sc + 4u * (32 * h + k)), v4 = lds_2x2(sc + 4u * (kKeys + 32 * h + k));
-#pragma unroll
-                        for (int f = 0; f < 2; ++f) {
-                            const int kk = 32 * h + k + 2 * f;
-                            const uint64_t d = fma2(pair(sr[k + 2 * f], sr[k + 2 * f + 1]), f ? s4.y : s4.x, nm);
-                            uint32_t e0 = __float_as_uint(ex2(lo_of(d))), e1 = __float_as_uint(ex2(hi_of(d)));
-                            if (kTail) {
-                                e0 = kk < kvalid ? e0 : 0;
-                                e1 = kk + 1 < kvalid ? e1 : 0;
-                            }
-                            const uint64_t e = pair(e0, e1);
-                            ls[f] = add2(ls[f], e);
-                            const uint64_t q = mul2(e, f ? v4.y : v4.x);
-                            pk[k / 2 + f] = pack_bf16x2(lo_of(q), hi_of(q));
-                        }
-                    }
-                    st16u(t_p + 16u * h, pk);   // (over scores that have been read, where P is not apart)
+                if (L::kApart) {   // the next S may come
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar + kBarSFree + 8u * g);
                 }
-                l = l * corr + ((lo_of(ls[0]) + hi_of(ls[0])) + (lo_of(ls[1]) + hi_of(ls[1])));
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    lq[j] += lo_of(ls[j]) + hi_of(ls[j]);
                 st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(bar + kBarPFull + 8u * (L::kBufs * g + b));
-                m_used = m_new;
             };
             for (int i = g; ok && i < n; i += kG, ++m_it) {
                 if (x.keys - (x.c_lo + (i >> w.pairs)) * kKeys >= kKeys)
@@ -753,6 +825,13 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
                 ok = wait_w<false>(bar + kBarPvDone + 8u * (L::kBufs * g + ((m_it - 1) & (L::kBufs - 1))), ((m_it - 1) / L::kBufs) & 1,
                                    abort_flag, hdr, kSitePvDone);
             tc_fence_after();
+            // this thread's own row from here on
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                lq[j] += __shfl_xor_sync(0xFFFFFFFFu, lq[j], 1);
+                lq[j] += __shfl_xor_sync(0xFFFFFFFFu, lq[j], 2);
+            }
+            const float m_used = of_row(mq, lane), l = of_row(lq, lane);
             if (w.split > 1) {
                 // ---- merge of a split unit's kG s partial rows: each is pushed to
                 // the CTA that owns the row, over the memory of the ring, once
