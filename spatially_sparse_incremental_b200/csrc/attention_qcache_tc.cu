@@ -159,13 +159,13 @@ __device__ __forceinline__ uint32_t place(uint32_t atom, int j, int v)
 
 // One staging thread's share of a chunk of K or V: up to N vectors of 8 codes,
 // vector i being (key j, vector v) number t + kStage i of the chunk, v fastest.
-// Where they lie in the chunk and in shared memory is worked out once; kSets
-// register sets hold the codes on their way.
-template <int N, int kSets, int kKeys>
+// Where they lie in the chunk and in shared memory is worked out once; the next
+// chunk's codes are on their way in registers.
+template <int N, int kKeys>
 struct Stager {
     uint32_t src[N];      // byte offset from the chunk's first key
     uint32_t to[N];       // offset in the staged rows | key << 16 (kKeys: no such vector, kZero: zeros for padded channels)
-    uint2 raw[kSets][N];
+    uint2 raw[N];
     static constexpr uint32_t kZero = 0x7FFF;
     const uint8_t *at;    // the next chunk to fetch
     uint32_t step;        // bytes of a chunk's keys
@@ -193,42 +193,40 @@ struct Stager {
     __device__ __forceinline__ void start(const uint8_t *codes, int64_t e) { at = codes + (fmt == SIGE_Q_S4 ? e >> 1 : e); }
 
     // the next chunk, of which `nkeys` keys exist (zeros for the others)
-    template <int S>
     __device__ __forceinline__ void fetch(int nkeys)
     {
         const uint32_t lim = (uint32_t)min(nkeys, kKeys) << 16;
         if (fmt == SIGE_Q_S4) {
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                raw[S][i] = make_uint2(to[i] < lim ? __ldg(reinterpret_cast<const uint32_t *>(at + src[i])) : 0u, 0u);
+                raw[i] = make_uint2(to[i] < lim ? __ldg(reinterpret_cast<const uint32_t *>(at + src[i])) : 0u, 0u);
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                raw[S][i] = make_uint2(0, 0);
+                raw[i] = make_uint2(0, 0);
                 if (to[i] < lim)
-                    raw[S][i] = __ldg(reinterpret_cast<const uint2 *>(at + src[i]));
+                    raw[i] = __ldg(reinterpret_cast<const uint2 *>(at + src[i]));
             }
         }
         at += step;
     }
 
-    template <int S, int kFmt>
+    template <int kFmt>
     __device__ __forceinline__ void store_as(uint32_t base)
     {
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if (to[i] >> 16 != kKeys)
-                sts128(base + (to[i] & 0xFFFFu), codes8<kFmt>(raw[S][i]));
+                sts128(base + (to[i] & 0xFFFFu), codes8<kFmt>(raw[i]));
     }
-    template <int S>
     __device__ __forceinline__ void store(uint32_t base)
     {
         if (fmt == SIGE_Q_S8)
-            store_as<S, SIGE_Q_S8>(base);
+            store_as<SIGE_Q_S8>(base);
         else if (fmt == SIGE_Q_E4M3)
-            store_as<S, SIGE_Q_E4M3>(base);
+            store_as<SIGE_Q_E4M3>(base);
         else
-            store_as<S, SIGE_Q_S4>(base);
+            store_as<SIGE_Q_S4>(base);
     }
 };
 
@@ -334,29 +332,13 @@ __device__ __forceinline__ float of_row(const float (&v)[4], int lane)
     return lane < 16 ? (lane < 8 ? a : b) : (lane < 24 ? c : d);
 }
 
-// Bounded waits by every lane of a warp, inline (a call would keep the
-// compiler from splitting the registers between the roles): false, in all
-// lanes, when the limit expired or another role gave up.
+// Bounded waits by every lane of a warp: false, in all lanes, when the limit
+// expired or another role gave up.
 template <bool kPeer>
 __device__ __forceinline__ bool wait_w(uint32_t b, uint32_t parity, volatile int *abort_flag, WsHeader *hdr, int where)
 {
-    bool ok = kPeer ? mbar_try_cluster(b, parity) : mbar_try(b, parity);
-    if (__all_sync(0xFFFFFFFFu, ok))
-        return true;
-    const long long t0 = clock64();
-    while (!__all_sync(0xFFFFFFFFu, ok)) {
-        if (!ok)
-            ok = kPeer ? mbar_try_cluster(b, parity) : mbar_try(b, parity);
-        const bool late = clock64() - t0 > kWaitCycles;
-        if (__any_sync(0xFFFFFFFFu, *abort_flag || late)) {
-            if (!*abort_flag) {
-                *abort_flag = 1;
-                record_error(hdr, SIGE_ERR_TIMEOUT, where);
-            }
-            return false;
-        }
-    }
-    return true;
+    return __all_sync(0xFFFFFFFFu, kPeer ? mbar_wait_cluster(b, parity, abort_flag, hdr, where)
+                                         : mbar_wait(b, parity, abort_flag, hdr, where));
 }
 
 // A unit and the chunks of it that one CTA takes.
@@ -467,8 +449,7 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
             const int t = (int)threadIdx.x - (L::kSoft + 64);
             const int nk = p.dh >> 3, nkv = args.dhp >> 3;   // 8-channel vectors of a query row; padded to 16 channels
             constexpr int kPer = (kKeys * KD / 8 + kStage - 1) / kStage;   // vectors of K, and of V, a thread
-            constexpr int kSets = 2;   // chunks on their way while one is converted
-            Stager<kPer, kSets, kKeys> K, V;
+            Stager<kPer, kKeys> K, V;
             K.init(t, nkv, args.dkv, nk, p.D, p.kfmt, L::kKvAtom);
             V.init(t, p.dvh >> 3, args.dvv, p.dvh >> 3, p.Dv, p.vfmt, L::kKvAtom);
             int it = 0, st = 0, nu = 0;
@@ -486,23 +467,19 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
                 const float *vs = p.vs + row0 * p.vng + x.head * p.dvh / p.vgroup;
                 const int left = x.keys - x.c_lo * kKeys;   // keys from the first chunk on
                 constexpr int kSc = (2 * kKeys + kStage - 1) / kStage;
-                float sr[kSets][kSc];
-                auto fetch = [&](int i, auto set) {
-                    constexpr int s = decltype(set)::value;
+                float sr[kSc];
+                auto fetch = [&](int i) {
                     const int nkeys = left - i * kKeys;
-                    K.template fetch<s>(nkeys);
-                    V.template fetch<s>(nkeys);
+                    K.fetch(nkeys);
+                    V.fetch(nkeys);
 #pragma unroll
                     for (int e = 0; e < kSc; ++e) {
                         const int k = t + e * kStage, key = k & (kKeys - 1), row = i * kKeys + key;
-                        sr[s][e] = 0.0f;
+                        sr[e] = 0.0f;
                         if (k < 2 * kKeys && key < nkeys)
-                            sr[s][e] = k < kKeys ? __ldg(ks + (int64_t)row * p.kng) * args.sc : __ldg(vs + (int64_t)row * p.vng);
+                            sr[e] = k < kKeys ? __ldg(ks + (int64_t)row * p.kng) * args.sc : __ldg(vs + (int64_t)row * p.vng);
                     }
                 };
-                fetch(0, std::integral_constant<int, 0>());
-                if (kSets > 1 && n > 1)
-                    fetch(1, std::integral_constant<int, kSets - 1>());
                 // the unit's queries, a row a thread, zeros for padding slots and channels
                 if (nu > 0 && !wait_w<false>(bar + kBarQEmpty, (nu - 1) & 1, abort_flag, hdr, kSiteQEmpty))
                     break;
@@ -528,32 +505,29 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
                 fence_async_smem();
                 mbar_arrive(bar + kBarQFull);
                 ++nu;
-                auto stage = [&](int i, auto set) -> bool {
-                    constexpr int s = decltype(set)::value;
-                    if (it >= L::kStages && !wait_w<false>(bar + kBarKvEmpty + 8u * st, ph, abort_flag, hdr, kSiteKvEmpty))
-                        return false;
+#pragma unroll 1
+                for (int i = 0; i < n; ++i, ++it) {
+                    if (i == 0)
+                        fetch(0);
+                    if (it >= L::kStages && !wait_w<false>(bar + kBarKvEmpty + 8u * st, ph, abort_flag, hdr, kSiteKvEmpty)) {
+                        ok = false;
+                        break;
+                    }
                     const uint32_t kb = sb + L::kOffK + (uint32_t)st * L::kKvStage;
-                    K.template store<s>(kb);
-                    V.template store<s>(kb + L::kAtoms * L::kKvAtom);
+                    K.store(kb);
+                    V.store(kb + L::kAtoms * L::kKvAtom);
 #pragma unroll
                     for (int e = 0; e < kSc; ++e)
                         if (t + e * kStage < 2 * kKeys)
-                            sts_f1(sb + L::kOffSc + (uint32_t)st * L::kScStage + (uint32_t)(t + e * kStage) * 4u, sr[s][e]);
+                            sts_f1(sb + L::kOffSc + (uint32_t)st * L::kScStage + (uint32_t)(t + e * kStage) * 4u, sr[e]);
                     fence_async_smem();
                     mbar_arrive(bar + kBarKvFull + 8u * st);
-                    if (i + kSets < n)
-                        fetch(i + kSets, set);
-                    ++it;
+                    if (i + 1 < n)
+                        fetch(i + 1);
                     if (++st == L::kStages) {
                         st = 0;
                         ph ^= 1;
                     }
-                    return true;
-                };
-                for (int i = 0; ok && i < n; i += 2) {
-                    ok = stage(i, std::integral_constant<int, 0>());
-                    if (ok && i + 1 < n)
-                        ok = stage(i + 1, std::integral_constant<int, kSets - 1>());
                 }
             }
             __syncwarp();
@@ -745,7 +719,6 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
                 // the group's previous P V has landed: P may be written, O rescaled.
                 // (Each phase of the barrier is waited for in turn: a parity tells
                 // two neighbouring phases apart, no more.)
-                bool again = i < kG;
                 if (i >= kG) {
                     const int pb = (m_it - 1) & (L::kBufs - 1);
                     if (!wait_w<false>(bar + kBarPvDone + 8u * (L::kBufs * g + pb), ((m_it - 1) / L::kBufs) & 1, abort_flag, hdr,
@@ -754,48 +727,50 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
                         return;
                     }
                     tc_fence_after();
-                    if constexpr (L::kApart) {
-                        pass(std::false_type());
-                        again = __any_sync(0xFFFFFFFFu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kSlack);
-                    } else {
-                        again = true;   // (P would lie over scores that are needed again: the maximum first)
-                    }
                 }
-                if (again) {
-                    if (i < kG || !L::kApart) {
-                        pass(std::true_type());
+                // A first job has no base yet, and where P lies over the scores they
+                // cannot be read again: the maximum first.
+                bool move = i < kG || !L::kApart;
+                if (move) {
+                    pass(std::true_type());
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            top[j] -= i < kG ? 0.0f : mq[j];
-                    }
-                    float corr[4];
-                    bool grow = false;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        // (a first job: from -inf to its maximum; a row whose scores
-                        // are all -inf or NaN keeps a base of -inf)
-                        const bool up = i < kG || top[j] > (L::kApart ? 0.0f : 8.0f);
-                        const float base = i < kG ? top[j] : mq[j] + top[j];
-                        corr[j] = up && i >= kG ? ex2(-top[j]) : 1.0f;
-                        if (up) {
-                            mq[j] = base;
-                            lq[j] *= corr[j];
-                            grow = grow || i >= kG;
-                        }
-                    }
-                    if (__any_sync(0xFFFFFFFFu, grow)) {
-                        const float f = of_row(corr, lane);
+                    for (int j = 0; j < 4; ++j)
+                        top[j] -= i < kG ? 0.0f : mq[j];
+                }
 #pragma unroll 1
-                        for (int pc = 0; pc < args.dvp; pc += 16) {
-                            float v[16];
-                            tmem_ld16(t_o + (uint32_t)pc, v);
+                while (true) {
+                    if (move) {
+                        float corr[4];
+                        bool grow = false;
 #pragma unroll
-                            for (int q = 0; q < 16; ++q)
-                                v[q] *= f;
-                            st16(t_o + (uint32_t)pc, v);
+                        for (int j = 0; j < 4; ++j) {
+                            // (a first job: from -inf to its maximum; a row whose
+                            // scores are all -inf or NaN keeps a base of -inf)
+                            const bool up = i < kG || top[j] > (L::kApart ? 0.0f : 8.0f);
+                            corr[j] = up && i >= kG ? ex2(-top[j]) : 1.0f;
+                            if (up) {
+                                mq[j] = i < kG ? top[j] : mq[j] + top[j];
+                                lq[j] *= corr[j];
+                                grow = grow || i >= kG;
+                            }
+                        }
+                        if (__any_sync(0xFFFFFFFFu, grow)) {
+                            const float f = of_row(corr, lane);
+#pragma unroll 1
+                            for (int pc = 0; pc < args.dvp; pc += 16) {
+                                float v[16];
+                                tmem_ld16(t_o + (uint32_t)pc, v);
+#pragma unroll
+                                for (int q = 0; q < 16; ++q)
+                                    v[q] *= f;
+                                st16(t_o + (uint32_t)pc, v);
+                            }
                         }
                     }
                     pass(std::false_type());
+                    if (move || !__any_sync(0xFFFFFFFFu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kSlack))
+                        break;
+                    move = true;
                 }
                 if (L::kApart) {   // the next S may come
                     tc_fence_before();
