@@ -543,22 +543,25 @@ class QCache:
     __slots__ = ("codes", "scales", "format", "shape", "desc")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, format: str):
-        if format not in _QFMT:
+        fmt = _QFMT.get(format)
+        if fmt is None:
             raise ValueError(f"unknown format {format!r}: one of {sorted(_QFMT)}")
-        if codes.dtype != _QSTORE[format] or scales.dtype != torch.float32:
+        if codes.dtype is not _QSTORE[format] or scales.dtype is not torch.float32:
             raise ValueError(f"{format} codes are {_QSTORE[format]}, scales are torch.float32")
-        cs, ss = codes.shape, scales.shape
-        if len(cs) != 4 or len(ss) != 4 or cs[:3] != ss[:3]:
+        if codes.dim() != 4 or scales.dim() != 4:
+            raise ValueError("expected codes and scales [N, H, W, *] of one map")
+        n, h, w, c = codes.shape
+        sn, sh, sw, ng = scales.shape
+        if n != sn or h != sh or w != sw:
             raise ValueError("expected codes and scales [N, H, W, *] of one map")
         if not codes.is_contiguous() or not scales.is_contiguous():
             raise ValueError("expected contiguous codes and scales")
-        n, h, w, c = cs
-        c = 2 * c if format == "s4" else c
-        ng = ss[3]
+        if fmt == Q_S4:
+            c *= 2
         if ng < 1 or c % ng:
             raise ValueError(f"{ng} scales a pixel do not divide {c} channels")
         self.codes, self.scales, self.format, self.shape = codes, scales, format, (n, h, w, c)
-        self.desc = QCacheDesc(n, h, w, c, _QFMT[format], c // ng)
+        self.desc = QCacheDesc(n, h, w, c, fmt, c // ng)
 
     @property
     def group(self) -> int:
@@ -611,7 +614,7 @@ class _Launch:
     def __enter__(self):
         st = self.stream
         if st is None:
-            if self.dev != torch.cuda.current_device():
+            if self.dev != torch._C._cuda_getDevice():
                 self.ctx = torch.cuda.device(self.dev)
                 self.ctx.__enter__()
             return torch._C._cuda_getCurrentRawStream(self.dev)
@@ -670,9 +673,9 @@ def sige_qcache_write(x, cache: QCache, idx=None, count=None, capacity=0, block=
     b, i, c, cap = _tile_args(what, idx, count, capacity, block)
     dev = _device_index(what, x, cache.codes, cache.scales, idx, count, gn_scale, gn_shift)
     with _Launch(dev, stream) as st:
-        _check(lib().sige_qcache_write(x.data_ptr(), ctypes.byref(xd), _addr(gn_scale), _addr(gn_shift),
+        _check(lib().sige_qcache_write(x.data_ptr(), xd, _addr(gn_scale), _addr(gn_shift),
                                        1 if silu else 0, b, i, c, cap, cache.codes.data_ptr(), cache.scales.data_ptr(),
-                                       ctypes.byref(cache.desc), st), what)
+                                       cache.desc, st), what)
     return cache
 
 
@@ -688,8 +691,8 @@ def sige_qcache_read(cache: QCache, y=None, idx=None, count=None, capacity=0, bl
         if y is None:
             y = (torch.empty if idx is None else torch.zeros)(cache.shape, dtype=dtype, device=cache.codes.device)
         yd = _map_desc(what, y, cache.shape)
-        _check(lib().sige_qcache_read(cache.codes.data_ptr(), cache.scales.data_ptr(), ctypes.byref(cache.desc), b, i, c,
-                                      cap, y.data_ptr(), ctypes.byref(yd), st), what)
+        _check(lib().sige_qcache_read(cache.codes.data_ptr(), cache.scales.data_ptr(), cache.desc, b, i, c,
+                                      cap, y.data_ptr(), yd, st), what)
     return y
 
 
@@ -714,9 +717,9 @@ def sige_qlinear(a: QCache, w: QCache, bias=None, y=None, idx=None, count=None, 
         yd = _map_desc(what, y, shape)
         if workspace is None:
             workspace = zeros_workspace(WORKSPACE_HEADER, a.codes.device)
-        _check(lib().sige_qlinear(a.codes.data_ptr(), a.scales.data_ptr(), ctypes.byref(a.desc), w.codes.data_ptr(),
-                                  w.scales.data_ptr(), ctypes.byref(w.desc), _addr(bias), b, i, c, cap, _addr(residual),
-                                  y.data_ptr(), ctypes.byref(yd), workspace.data_ptr(), workspace.nbytes, st), what)
+        _check(lib().sige_qlinear(a.codes.data_ptr(), a.scales.data_ptr(), a.desc, w.codes.data_ptr(),
+                                  w.scales.data_ptr(), w.desc, _addr(bias), b, i, c, cap, _addr(residual),
+                                  y.data_ptr(), yd, workspace.data_ptr(), workspace.nbytes, st), what)
     return y
 
 
@@ -749,9 +752,9 @@ def sige_attention_qcache(q, k: QCache, v: QCache, heads: int, o=None, idx=None,
             o = (torch.empty if idx is None else torch.zeros)(shape, dtype=torch.bfloat16, device=q.device)
         if workspace is None:
             workspace = zeros_workspace(WORKSPACE_HEADER, q.device)
-        _check(lib().sige_attention_qcache(q.data_ptr(), ctypes.byref(qd), k.codes.data_ptr(), k.scales.data_ptr(),
-                                           ctypes.byref(k.desc), v.codes.data_ptr(), v.scales.data_ptr(),
-                                           ctypes.byref(v.desc), _addr(key_counts), heads, b, i, c, cap, o.data_ptr(),
+        _check(lib().sige_attention_qcache(q.data_ptr(), qd, k.codes.data_ptr(), k.scales.data_ptr(),
+                                           k.desc, v.codes.data_ptr(), v.scales.data_ptr(),
+                                           v.desc, _addr(key_counts), heads, b, i, c, cap, o.data_ptr(),
                                            workspace.data_ptr(), workspace.nbytes, st), what)
     return o
 

@@ -71,24 +71,37 @@ __device__ __forceinline__ float group_scale(uint32_t amax)
     }
 }
 
-// What the quotient is formed with: the scale's reciprocal (exact for e4m3;
-// 0 where the group stores zeros: scale 0 or NaN).
-__device__ __forceinline__ float scale_reciprocal(float s) { return s > 0.0f ? __frcp_rn(s) : 0.0f; }
+// What the quotient is formed with: the scale's reciprocal, 0 where the group
+// stores zeros (scale 0 or NaN).  Exact for e4m3 (a power of two); for the
+// integers within 2^-23 (an approximate reciprocal: the scale and its reciprocal
+// are normal numbers).
+template <int kFmt>
+__device__ __forceinline__ float scale_reciprocal(float s)
+{
+    if constexpr (kFmt == SIGE_Q_E4M3) {
+        return s > 0.0f ? __uint_as_float(0x7F000000u - __float_as_uint(s)) : 0.0f;
+    } else {
+        float r;
+        asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
+        return s > 0.0f ? r : 0.0f;
+    }
+}
 
 // round(v / s) to the nearest integer, ties to even, of the exact quotient.
-// v * (1 / s) is off by less than 2^-15 for |v / s| <= 127.5; only where that
-// could cross a tie does the exact remainder decide (its product has at most
-// 32 significant bits: exact in double).
+// v * (1 / s) is off by at most 127.5 (2^-23 + 2^-24) < 2^-15 for |v / s| <=
+// 127.5, so its nearest integer k is the right one or, next to a tie, its
+// neighbour.  The remainder e = v - k s tells: it is exact in float32 (a
+// multiple of half the scale's last bit, below 2^24 of them; above the smallest
+// subnormal), and k stands unless 2 |e| > s, or 2 |e| = s with k odd.
+constexpr float kRoundBase = 12582912.0f;   // 1.5 * 2^23: a sum's low bits are the rounded integer's
+__device__ __forceinline__ float quotient_rest(float v, float s, float k) { return fmaf(-k, s, v); }
 __device__ __forceinline__ int quotient_code(float v, float s, float r)
 {
-    const float q = v * r;
-    float k = rintf(q);
-    if (fabsf(q - k) > 0.5f - 1.0f / 32768.0f) {
-        const float f = floorf(q);
-        const double d = (double)v - ((double)f + 0.5) * (double)s;
-        k = d > 0.0 ? f + 1.0f : d < 0.0 ? f : 2.0f * rintf(0.5f * f + 0.25f);
-    }
-    return (int)k;
+    const float k = rintf(v * r), e = quotient_rest(v, s, k), e2 = 2.0f * fabsf(e);
+    int c = (int)k;
+    if (e2 > s || (e2 == s && (c & 1)))
+        c += e > 0.0f ? 1 : -1;
+    return c;
 }
 
 // Four codes of an integer format from a 32-bit word (s8) or half a word (s4).

@@ -64,16 +64,28 @@ int launch_check();           // SIGE_OK or SIGE_ERR_CUDA after a launch
 // Every kernel of the library asks for the largest shared-memory carveout, the
 // configuration the tensor-core conv needs: consecutive launches then run
 // without reconfiguring the SM's L1 / shared-memory split in between.
-template <typename K>
-inline void prefer_max_shared(K kernel)
+inline void prefer_max_shared_at(const void *kernel, std::atomic<int> *done)
 {
-    static std::atomic<int> done[64];   // per device; concurrent first calls both set the same attribute
+    // a flag per device; concurrent first calls both set the same attribute
     int d = 0;
     if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= 64 || done[d].load(std::memory_order_acquire))
         return;
     cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);
     cudaGetLastError();   // a refused preference is not an error of the call
     done[d].store(1, std::memory_order_release);
+}
+template <typename K>
+inline void prefer_max_shared(K kernel)
+{
+    static std::atomic<int> done[64];
+    prefer_max_shared_at(reinterpret_cast<const void *>(kernel), done);
+}
+// Kernels of one signature (instances of a template) each need their own flags.
+template <auto kKernel>
+inline void prefer_max_shared_of()
+{
+    static std::atomic<int> done[64];
+    prefer_max_shared_at(reinterpret_cast<const void *>(kKernel), done);
 }
 void count_launch();
 int device_sm_count();

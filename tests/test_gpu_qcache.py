@@ -265,3 +265,53 @@ def test_streams_and_graphs():
                                   **where)
     torch.cuda.synchronize()
     assert torch.equal(out, eager)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("group", [8, 16, 24, 32, 56, 72, 80, 168, 320, 640, 1000, 1280, 2040, 2048])
+def test_write_group_widths(group, dtype, fmt):
+    """Every split of a group over lanes and vectors, two groups a pixel; half of
+    a group's largest magnitude, the commonest near tie of bf16 maps, in each."""
+    rng = np.random.default_rng(group)
+    x = random_map(rng, 1, 5, 7, 2 * group, dtype)
+    g = x.view(-1, group)
+    g[:, group // 2] = g.abs().amax(1) / 2
+    check_write(x, group, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["s8", "s4"])
+@pytest.mark.parametrize("shift", [-119, -118, -117, -60, 60, 124])
+def test_write_near_ties_of_extreme_scales(fmt, shift):
+    """The near ties of test_write_near_ties with scales from 2^-126 up to the
+    largest: shifts by a power of two, exact but for subnormal elements."""
+    rng = np.random.default_rng(12)
+    qm = oq.QMAX[fmt]
+    m = rng.uniform(1.0, 2.0, size=(2000, 1)).astype(np.float32)
+    s = m / np.float32(qm)
+    k = rng.integers(-int(qm), int(qm), size=(2000, 15))
+    v = ((k + 0.5) * s.astype(np.float64)).astype(np.float32)
+    v = np.where(rng.random(v.shape) < 0.4, np.nextafter(v, np.float32(0)), v)
+    x = np.ldexp(np.concatenate([m, np.clip(v, -m, m)], 1), shift).astype(np.float32)
+    check_write(torch.from_numpy(x).view(1, 20, 100, 16), 16, fmt)
+
+
+def test_more_groups_than_32_bits_count():
+    """More than 2^31 groups and vectors in the map, few of them listed: the
+    last tile's, with a transform whose channels follow from the group."""
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB of device memory")
+    h, w, c = 1024, 1024, 18432
+    rng = np.random.default_rng(5)
+    small = random_map(rng, 1, 2, 2, c, torch.bfloat16).clamp(-50, 50).to(DEV)
+    x = torch.empty((1, h, w, c), dtype=torch.bfloat16, device=DEV)
+    x[:, -2:, -2:] = small
+    gn = dict(gn_scale=torch.from_numpy(rng.normal(size=(1, c)).astype(np.float32)).to(DEV),
+              gn_shift=torch.from_numpy(rng.normal(size=(1, c)).astype(np.float32)).to(DEV))
+    where = dict(idx=torch.tensor([[h - 2, w - 2]], dtype=torch.int32, device=DEV),
+                 count=torch.ones(1, dtype=torch.int32, device=DEV), capacity=1, block=2)
+    cache = sige.sige_qcache_write(x, sige.qcache_empty(1, h, w, c, "s8", 8), **where, **gn)
+    ref = sige.sige_qcache_write(small, sige.qcache_empty(1, 2, 2, c, "s8", 8), **gn)
+    assert torch.equal(cache.codes[:, -2:, -2:], ref.codes) and torch.equal(cache.scales[:, -2:, -2:], ref.scales)
+    sige.sige_qcache_read(cache, x, **where)
+    assert torch.equal(x[:, -2:, -2:], sige.sige_qcache_read(ref))
