@@ -2,15 +2,10 @@
 // sums by tcgen05.mma kind::i8 (exact, int32 in tensor memory), the two scales,
 // bias and residual in the epilogue, one rounding into the cached output.
 //
-// A work unit is 128 rows x `bn` columns of the product, K in chunks of 128
-// bytes (four MMAs of 32):
-//   * many tokens: the tokens are the rows and bn (256 .. 32) output channels
-//     the columns;
-//   * at most kSwapTokens tokens: the output channels are the rows and the
-//     tokens (padded to 16) the columns, so that the 128 rows of an MMA are
-//     filled by the weights, whose reading bounds such a call.
-// The choice, bn and the K split depend on the number of tokens, which only
-// the device knows for a tile list, so every CTA derives them at its start.
+// A work unit is 128 tokens x `bn` (256 .. 32) output channels, K in chunks of
+// 128 bytes (four MMAs of 32).  bn and the K split depend on the number of
+// tokens, which only the device knows for a tile list, so every CTA derives
+// them at its start.
 //   * warp 0 loads the operands by TMA into a ring of stages, 128-byte rows
 //     with the 128-byte swizzle (the K-major operands of the MMA): weights and
 //     whole maps by boxes of rows, the tokens of a tile list straight from the
@@ -39,7 +34,6 @@ constexpr int kRows = 128;
 constexpr int kChunk = 128;              // bytes of K a stage
 constexpr int kMaxBn = 256;
 constexpr int kSplitBn = 64;             // widest unit whose K is split
-constexpr int kSwapTokens = 64;
 constexpr int kCluster = 4;
 constexpr int kMaxStages = 9;
 
@@ -48,8 +42,7 @@ constexpr uint32_t kOffRecv = kRing;     // sums pushed by the other CTAs of a s
                                          // output tiles of the warps)
 constexpr uint32_t kRecvBytes = (kCluster - 1) * kRows * (kSplitBn / kCluster) * 4;
 constexpr uint32_t kOffCol = kOffRecv + kRecvBytes;          // per accumulator: column scales and biases
-constexpr uint32_t kOffTok = kOffCol + 2 * 2 * kMaxBn * 4;   // swapped units: the columns' pixels
-constexpr uint32_t kOffBar = kOffTok + kSwapTokens * 4;
+constexpr uint32_t kOffBar = kOffCol + 2 * 2 * kMaxBn * 4;
 constexpr uint32_t kBarFull = 0;                             // + 8 stage
 constexpr uint32_t kBarEmpty = 8 * kMaxStages;
 constexpr uint32_t kBarAccFull = 16 * kMaxStages;            // + 8 accumulator
@@ -67,7 +60,7 @@ static_assert(kSmem <= 227 * 1024, "shared memory");
 constexpr int kSiteEmpty = 301, kSiteFull = 302, kSiteAccEmpty = 303, kSiteAccFull = 304, kSiteRecv = 305;
 
 struct Plan {
-    int swap, bn, stages, split, nch;
+    int bn, stages, split, nch;
     uint32_t slots, rblocks, cblocks, units;
 };
 
@@ -83,12 +76,22 @@ __host__ __device__ inline void cut_at(int i, int *bn, int *split)
     *split = i < 8 ? 1 : i == 9 ? 4 : 2;
 }
 
-// Estimated cycles of a cut: rounds of units, each the longer of its chunks
-// (the operands' way into shared memory at about 60 bytes a cycle measured
-// longer than the products, 2 bn cycles; 250 for the issue of a small one) and
+// What a call's kind adds: cycles of a token row of a chunk (copied by boxes, or
+// gathered four a copy, about 60 a copy) and of a split's exchange (a whole map
+// gives up k_qlinear_whole for it: 16 tokens x 1280 -> 1280 4.2 us, split 5.9).
+struct Costs {
+    uint32_t token, split;
+};
+constexpr Costs kMapCosts = {2, 4300};
+__host__ __device__ inline Costs list_costs(int tile_rows) { return {tile_rows ? 2u : 15u, 1300}; }
+
+// Estimated cycles of a cut: rounds of units, each the longer of its chunks and
 // its outputs (about 12 cycles a column); a fill and a drain; the exchange of a
-// split.  0xFFFFFFFF: not possible.
-__host__ __device__ inline uint32_t cut_cost(int i, uint32_t rblocks, int Co, int nch, int grid, int cluster)
+// split, by quarters of 32 rows.  A chunk: the operands' way into shared memory
+// at about 60 bytes a cycle (measured longer than the products, 2 bn cycles);
+// 250 for the issue of a small one.  rows: tokens of a unit.  0xFFFFFFFF: not
+// possible.
+__host__ __device__ inline uint32_t cut_cost(int i, uint32_t rblocks, int rows, Costs k, int Co, int nch, int grid, int cluster)
 {
     int bn, split;
     cut_at(i, &bn, &split);
@@ -96,48 +99,37 @@ __host__ __device__ inline uint32_t cut_cost(int i, uint32_t rblocks, int Co, in
     if (split > cluster || (split > 1 && (units * (uint32_t)split > (uint32_t)grid || nch < 2 * split)))
         return 0xFFFFFFFFu;
     const uint32_t rounds = (units * (uint32_t)split + grid - 1) / grid;
-    uint32_t chunk = (uint32_t)(kRows + bn) * 2u + (uint32_t)(kRows + bn) / 8u;
+    uint32_t chunk = (uint32_t)bn * 17u / 8u + (uint32_t)rows * k.token;
     chunk = chunk < 250u ? 250u : chunk;
     const uint32_t mul = (uint32_t)((nch + split - 1) / split) * chunk, out = 12u * (uint32_t)bn;
-    const float c = (float)rounds * (float)(mul > out ? mul : out) + (float)(1000u + out / split + (split > 1 ? 2500u : 0u));
+    const uint32_t exchange = split > 1 ? k.split + 300u * (uint32_t)((rows + 31) / 32) : 0u;
+    const float c = (float)rounds * (float)(mul > out ? mul : out) + (float)(1000u + out / split + exchange);
     return c < 2e9f ? (uint32_t)c : 2000000000u;
 }
 
-// The launch's work for `slots` tokens on `grid` CTAs in clusters of `cluster`.
-// On the device the whole warp calls it: a lane prices each cut.
-__host__ __device__ inline Plan make_plan(uint32_t slots, int Co, int C, int grid, int cluster)
+// The launch's work for `slots` tokens on `grid` CTAs in clusters of `cluster`.  On the device the whole warp calls it: a lane
+// prices each cut.
+__host__ __device__ inline Plan make_plan(uint32_t slots, Costs k, int Co, int C, int grid, int cluster)
 {
     Plan q;
     q.slots = slots;
     q.nch = (C + kChunk - 1) / kChunk;
-    q.swap = slots <= kSwapTokens;
-    if (q.swap) {
-        // wide enough that every CTA of a split unit finishes 16 columns
-        const int wide = cluster < 4 || q.nch < 4 ? 16 : q.nch < 8 ? 32 : 64;
-        q.bn = slots > 48 ? 64 : slots > 32 ? 48 : slots > 16 ? 32 : 16;
-        q.bn = q.bn > wide ? q.bn : wide;
-        q.rblocks = ((uint32_t)Co + kRows - 1) / kRows;
-        q.cblocks = slots > 0;
-        q.units = q.rblocks * q.cblocks;
-        q.split = cluster;
-        while (q.split > 1 && (q.units * (uint32_t)q.split > (uint32_t)grid || q.nch < 2 * q.split || q.bn % (16 * q.split)))
-            q.split >>= 1;
-    } else {
-        q.rblocks = (slots + kRows - 1) / kRows;
+    q.rblocks = (slots + kRows - 1) / kRows;
+    const int rows = slots < (uint32_t)kRows ? (int)slots : kRows;
 #ifdef __CUDA_ARCH__
-        const int lane = (int)(threadIdx.x & 31);
-        const uint32_t mine = cut_cost(least(lane, kCuts - 1), q.rblocks, Co, q.nch, grid, cluster);
-        const int best = __ffs(__ballot_sync(0xFFFFFFFFu, mine == __reduce_min_sync(0xFFFFFFFFu, mine))) - 1;
+    const int lane = (int)(threadIdx.x & 31);
+    const uint32_t mine = cut_cost(least(lane, kCuts - 1), q.rblocks, rows, k, Co, q.nch, grid, cluster);
+    const int best = __ffs(__ballot_sync(0xFFFFFFFFu, mine == __reduce_min_sync(0xFFFFFFFFu, mine))) - 1;
 #else
-        int best = 0;
-        for (int i = 1; i < kCuts; ++i)
-            if (cut_cost(i, q.rblocks, Co, q.nch, grid, cluster) < cut_cost(best, q.rblocks, Co, q.nch, grid, cluster))
-                best = i;
+    int best = 0;
+    for (int i = 1; i < kCuts; ++i)
+        if (cut_cost(i, q.rblocks, rows, k, Co, q.nch, grid, cluster) <
+            cut_cost(best, q.rblocks, rows, k, Co, q.nch, grid, cluster))
+            best = i;
 #endif
-        cut_at(best, &q.bn, &q.split);
-        q.cblocks = ((uint32_t)Co + q.bn - 1) / q.bn;
-        q.units = q.rblocks * q.cblocks;
-    }
+    cut_at(best, &q.bn, &q.split);
+    q.cblocks = ((uint32_t)Co + q.bn - 1) / q.bn;
+    q.units = q.rblocks * q.cblocks;
     q.stages = q.bn > 128 ? 4 : q.bn > 64 ? 6 : q.bn > 32 ? 8 : 9;
     return q;
 }
@@ -260,7 +252,7 @@ __device__ __noinline__ void drain_products(uint32_t bar)
 struct Args {
     QLinearParams q;
     int vec;       // y and the residual take 32-byte accesses of 16 columns
-    int tile_rows; // tokens of a tile that one box copies, 0: four tokens a copy
+    int tile_rows; // tokens that one box copies (a tile's; a whole map's of a unit), 0: four tokens a copy
     Plan plan;     // of a whole map (a list's is made on the device)
 };
 
@@ -448,7 +440,8 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     pdl_wait();
-    const Plan plan = p.px.idx ? make_plan((uint32_t)pixel_slots(p.px), p.Co, p.C, (int)gridDim.x, (int)csize) : args.plan;
+    const Plan plan = p.px.idx ? make_plan((uint32_t)pixel_slots(p.px), list_costs(args.tile_rows), p.Co, p.C, (int)gridDim.x, (int)csize)
+                               : args.plan;
     const int split_n = plan.split;
     const int per = (int)csize / split_n;                  // units a cluster takes at a time
     const int rank = csize > 1 ? (int)cluster_rank() : 0;
@@ -457,8 +450,9 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
     const uint32_t u_step = (gridDim.x / csize) * (uint32_t)per;
     const int c_lo = split * plan.nch / split_n, c_hi = (split + 1) * plan.nch / split_n;   // never empty
     if (threadIdx.x == 0) {
-        // pushed by the warps of the unit's other CTAs
-        mbar_init(bar + kBarRecv, (uint32_t)max(1, (split_n - 1) * kEpiWarps));
+        // pushed by the warps of the unit's other CTAs whose rows hold a token
+        const uint32_t left = u_first < plan.units ? plan.slots - u_first / plan.cblocks * kRows : 0;
+        mbar_init(bar + kBarRecv, max(1u, (uint32_t)(split_n - 1) * (kEpiWarps / 4) * min(4u, (left + 31) / 32)));
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     tc_fence_before();
@@ -477,12 +471,10 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
         const bool tiles = lists && args.tile_rows;   // whole tiles by boxes
         // weight rows: one box for a whole map; for a list (whose bn the host
         // does not know) boxes of 128, 64 and 32, one a lane
-        const int wrows = plan.swap ? kRows : plan.bn;
-        const int n128 = wrows >> 7, n64 = (wrows >> 6) & 1, nw = n128 + n64 + ((wrows >> 5) & 1);
+        const int n128 = plan.bn >> 7, n64 = (plan.bn >> 6) & 1, nw = n128 + n64 + ((plan.bn >> 5) & 1);
         const CUtensorMap *wmap = lane < n128 ? &tw : lane < n128 + n64 ? &tw64 : &tw32;
         const int wofs = lane < n128 ? 128 * lane : lane < n128 + n64 ? 128 * n128 : 128 * n128 + 64 * n64;
-        const uint32_t wdst = plan.swap ? 0u : (uint32_t)(kRows * kChunk);
-        const uint32_t tdst = plan.swap ? (uint32_t)(kRows * kChunk) : 0u;
+        constexpr uint32_t wdst = kRows * kChunk;          // weights behind the tokens
         const int per_copy = tiles ? args.tile_rows : 4;   // tokens a copy of a list, one copy a lane
         int it = 0, st = 0;
         uint32_t ph = 1;
@@ -490,12 +482,13 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
         for (uint32_t u = u_first; ok && u < plan.units; u += u_step) {
             const uint32_t rb = u / plan.cblocks;
             const int cb = (int)(u - rb * plan.cblocks);
-            const int wrow = plan.swap ? (int)rb * kRows : cb * plan.bn;
-            const uint32_t s_first = plan.swap ? 0 : rb * kRows;
+            const int wrow = cb * plan.bn;
+            const uint32_t s_first = rb * kRows;
             // the copies that hold a token of the list: what lies in the other
             // rows of a stage enters only products that are not written
             const int nt = lists ? (int)((min(plan.slots - s_first, (uint32_t)kRows) + per_copy - 1) / per_copy) : 0;
-            const uint32_t bytes = lists ? (uint32_t)(wrows + nt * per_copy) * kChunk : stage_bytes;
+            const uint32_t bytes = lists ? (uint32_t)(plan.bn + nt * per_copy) * kChunk
+                                         : (uint32_t)(plan.bn + args.tile_rows) * kChunk;
             // this lane's four tokens of the unit, or its tile (a clipped slot
             // reads the first token's row or tile)
             int t0 = 0, t1 = 0, t2 = 0, t3 = 0;
@@ -524,7 +517,7 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                 const uint32_t full = bar + kBarFull + 8u * st;
                 const uint32_t dst = sb + (uint32_t)st * stage_bytes;
                 if (!lists) {
-                    tma_stage_w(dst + wdst, &tw, wrow, dst + tdst, &tbox, (int)s_first, full, bytes, c * kChunk);
+                    tma_stage_w(dst + wdst, &tw, wrow, dst, &tbox, (int)s_first, full, bytes, c * kChunk);
                 } else {
                     if (lane == 0)
                         mbar_expect_tx(full, bytes);
@@ -532,7 +525,7 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                     if (lane < nw)
                         tma_load_2d(dst + wdst + (uint32_t)wofs * kChunk, wmap, full, c * kChunk, wrow + wofs);
                     if (lane < nt) {
-                        const uint32_t d = dst + tdst + (uint32_t)(lane * per_copy) * kChunk;
+                        const uint32_t d = dst + (uint32_t)(lane * per_copy) * kChunk;
                         if (tiles)
                             tma_load_4d(d, &tbox, full, c * kChunk, t0, t1, t2);
                         else
@@ -603,33 +596,15 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
             const int cb = (int)(u - rb * plan.cblocks);
             const uint32_t col = sb + kOffCol + (uint32_t)ab * 2 * kMaxBn * 4;
             float *colp = reinterpret_cast<float *>(smem + kOffCol + (uint32_t)ab * 2 * kMaxBn * 4);
-            int *tokp = reinterpret_cast<int *>(smem + kOffTok);
-            float rs = 0.0f, rbias = 0.0f;
-            int64_t pix = -1;
-            int chan = -1;
-            if (plan.swap) {
-                // columns: tokens (their scale and pixel); row: a channel
-                if (et < plan.bn) {
-                    const int64_t q = (uint32_t)et < plan.slots ? pixel_of(p.px, (uint32_t)et) : -1;
-                    tokp[et] = (int)q;
-                    colp[et] = q >= 0 ? __ldg(p.sa + q) : 0.0f;
-                }
-                chan = (int)rb * kRows + r < p.Co ? (int)rb * kRows + r : -1;
-                if (chan >= 0) {
-                    rs = __ldg(p.sw + chan);
-                    rbias = p.bias ? __ldg(p.bias + chan) : 0.0f;
-                }
-            } else {
-                if (et < plan.bn) {
-                    const int c = cb * plan.bn + et;
-                    colp[et] = c < p.Co ? __ldg(p.sw + c) : 0.0f;
-                    colp[kMaxBn + et] = c < p.Co && p.bias ? __ldg(p.bias + c) : 0.0f;
-                }
-                const uint32_t s = rb * kRows + (uint32_t)r;
-                pix = s < plan.slots ? pixel_of(p.px, s) : -1;
-                if (pix >= 0)
-                    rs = __ldg(p.sa + pix);
+            if (et < plan.bn) {
+                const int c = cb * plan.bn + et;
+                colp[et] = c < p.Co ? __ldg(p.sw + c) : 0.0f;
+                colp[kMaxBn + et] = c < p.Co && p.bias ? __ldg(p.bias + c) : 0.0f;
             }
+            const uint32_t s = rb * kRows + (uint32_t)r;
+            const int64_t pix = s < plan.slots ? pixel_of(p.px, s) : -1;
+            const float rs = pix >= 0 ? __ldg(p.sa + pix) : 0.0f;
+            const bool live = rb * kRows + (uint32_t)((warp & 3) * 32) < plan.slots;   // the warp's rows hold a token
             epi_sync();
             if (!mbar_wait_w(bar + kBarAccFull + 8u * ab, (nu >> 1) & 1, abort_flag, hdr, kSiteAccFull)) {
                 ok = false;
@@ -646,11 +621,8 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                 }
                 // push the other slices to their owners: 16 columns at a time,
                 // [sender][4 columns][row] of 16 bytes
-                // (a slice without tokens of a swapped unit is nobody's)
-                for (int o = 1; o < split_n; ++o) {
+                for (int o = 1; live && o < split_n; ++o) {
                     const int to = (split + o) & (split_n - 1);
-                    if (plan.swap && to * cw >= (int)plan.slots)
-                        continue;
                     const int from = ((split - to) & (split_n - 1)) - 1;   // this CTA among the owner's senders
                     for (int g = 16 * half; g < cw; g += 32) {
                         int acc[16];
@@ -667,13 +639,12 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                     if (lane == 0)
                         mbar_arrive_peer(map_peer(bar + kBarRecv, (uint32_t)(sub * split_n + to)));
                 }
-                if ((!plan.swap || col0 < (int)plan.slots) &&
-                    !__all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar + kBarRecv, 0, abort_flag, hdr, kSiteRecv))) {
+                if (live && !__all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar + kBarRecv, 0, abort_flag, hdr, kSiteRecv))) {
                     ok = false;
                     continue;
                 }
             }
-            if (split_n == 1 && !plan.swap) {
+            if (split_n == 1) {
                 // 32 columns at a time, the next ones on their way
                 int acc[2][32];
                 auto load = [&](int g, int (&r)[32]) {
@@ -714,7 +685,7 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                     mbar_arrive(bar + kBarAccEmpty + 8u * ab);
                 continue;
             }
-            for (int g = 16 * half; g < cw && (!plan.swap || col0 + g < (int)plan.slots); g += 32) {
+            for (int g = 16 * half; live && g < cw; g += 32) {
                 int acc[16];
                 ld_cols(t_acc + (uint32_t)(col0 + g), acc);
                 ld_done();
@@ -729,19 +700,7 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                         acc[4 * q + 3] += v.w;
                     }
                 }
-                if (plan.swap) {
-                    const int nt = min(16, (int)plan.slots - col0 - g);
-                    if (chan >= 0) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            if (k < nt) {
-                                const int t = tokp[col0 + g + k];
-                                if (t >= 0)
-                                    put1(p, (int64_t)t * p.Co + chan, qlinear_value(acc[k], colp[col0 + g + k], rs) + rbias);
-                            }
-                        }
-                    }
-                } else if (pix >= 0) {
+                if (pix >= 0) {
                     float v[16];
                     scale16(acc, col + 4u * (uint32_t)(col0 + g), rs, v);
                     put_cols(args, v, pix, cb * plan.bn + col0 + g);
@@ -768,7 +727,7 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
     }
 }
 
-// The same for a whole map whose units are neither swapped nor split and whose
+// The same for a whole map whose units are not split and whose
 // outputs TMA can store: the loops that bound the large products, with nothing
 // else in them (the general kernel's outputs, with every case in one loop, ran
 // at about half their rate).  kE: bytes of an output element.
@@ -833,7 +792,7 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                 }
                 const uint32_t dst = sb + (uint32_t)st * stage_bytes;
                 tma_stage_w(dst + kRows * kChunk, &tw, cb * plan.bn, dst, &tbox, (int)rb * kRows, bar + kBarFull + 8u * st,
-                            stage_bytes, c * kChunk);
+                            (uint32_t)(plan.bn + args.tile_rows) * kChunk, c * kChunk);
                 if (++st == plan.stages) {
                     st = 0;
                     ph ^= 1;
@@ -1071,10 +1030,10 @@ int launch_qlinear_tc(const QLinearParams &p, cudaStream_t stream)
     const int most = qt::kCluster * ncl;
     bool solo = false, whole = false;
     if (!p.px.idx) {
-        a.plan = qt::make_plan((uint32_t)p.slots, p.Co, p.C, most, qt::kCluster);
+        a.plan = qt::make_plan((uint32_t)p.slots, qt::kMapCosts, p.Co, p.C, most, qt::kCluster);
         solo = a.plan.split == 1;
         if (solo)
-            a.plan = qt::make_plan((uint32_t)p.slots, p.Co, p.C, sms, 1);
+            a.plan = qt::make_plan((uint32_t)p.slots, qt::kMapCosts, p.Co, p.C, sms, 1);
         cfg.gridDim = dim3(solo ? (unsigned)std::min<int64_t>(sms, a.plan.units)
                                 : (a.plan.units * a.plan.split + qt::kCluster - 1) / qt::kCluster * qt::kCluster);
     } else {
@@ -1090,10 +1049,13 @@ int launch_qlinear_tc(const QLinearParams &p, cudaStream_t stream)
     const CUtensorMapL2promotion l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
     bool good;
     if (!p.px.idx) {
-        good = encode_rows(&tw, p.w, p.Co, p.C, a.plan.swap ? qt::kRows : a.plan.bn, l2, encode) &&
-               encode_rows(&tbox, p.a, p.rows, p.C, a.plan.swap ? a.plan.bn : qt::kRows, l2, encode);
+        // (rows of a box past the map's end are zeros, but not for nothing: one
+        // token x 5120 -> 1280 with boxes of 128 rows 8.4 us, 32 tokens 6.8)
+        a.tile_rows = (int)std::min<int64_t>((p.slots + 7) / 8 * 8, qt::kRows);
+        good = encode_rows(&tw, p.w, p.Co, p.C, a.plan.bn, l2, encode) &&
+               encode_rows(&tbox, p.a, p.rows, p.C, a.tile_rows, l2, encode);
         tw64 = tw32 = tw;
-        whole = solo && !a.plan.swap && a.vec && encode_out(&ty, p, esz, encode);
+        whole = solo && a.vec && encode_out(&ty, p, esz, encode);
     } else {
         good = encode_rows(&tw, p.w, p.Co, p.C, 128, l2, encode) && encode_rows(&tw64, p.w, p.Co, p.C, 64, l2, encode) &&
                encode_rows(&tw32, p.w, p.Co, p.C, 32, l2, encode);
