@@ -7,24 +7,37 @@
 // scale); the only rounding of an operand is that of weight * scale to bf16.
 //
 // Work unit: one or two blocks of 128 query slots of one (batch item, head), the
-// keys in chunks of 64.  Roles of a CTA's warps:
-//   * seven warps stage the operands: the unit's queries once, and for each
-//     chunk the codes (global loads of 8 codes a lane, two chunks ahead), turned
-//     into bf16 rows of 128 bytes with the 128-byte swizzle (K-major for the
-//     first product, MN-major for the second), and the chunk's scales;
-//   * one warp issues S = Q K^T (M 128, N 64) and O += P V (M 128, K 64);
-//   * four groups of four warps (heads up to 64; two groups for wider ones) do
-//     the softmax, taking (block, chunk) jobs in turn:
-//     running maximum and sum (float32), P = 2^(s - max) * value scale as bf16
-//     over the chunk's own S columns, the O row in tensor memory rescaled only
-//     when the maximum has grown by more than 8 (base 2).  A thread reads its
-//     scores twice, 32 at a time (once for the maximum, once for the weights):
-//     few registers, so that four warps a scheduler cover each other's waits.
-// With more units than CTAs a unit is two blocks, so that a chunk is staged once
-// for 256 queries.  Rows (O, max, sum) of groups that share a block are merged
-// through shared memory at the end of a unit.  Where units are fewer than half
-// the CTAs, the CTAs of a cluster also split the keys and push their rows to
-// the row's owner through distributed shared memory.
+// keys in chunks of 128 (heads up to 64 channels) or 64 (wider).  A job is one
+// chunk against one block.  Roles of a CTA's 16 warps:
+//   * warp 0 issues S = Q K^T (M 128, N a chunk), warp 1 O += P V (M 128, K a
+//     chunk), each from one elected lane.  One warp for both took about 1300
+//     cycles a job, more than a softmax group.  Warps 0 and 1 because the
+//     schedulers serve the lowest numbers first: 84 -> 83 us on one map;
+//   * six warps stage the operands: the unit's queries once, and for each chunk
+//     the codes (global loads of 8 codes a thread, a chunk ahead in registers),
+//     turned into bf16 rows of 128 bytes with the 128-byte swizzle (K-major for
+//     the first product, MN-major for the second), and the chunk's scales;
+//   * two groups of four warps do the softmax of a job each, in one pass over the
+//     scores: read in the fragment layout, scaled, weighted against a standing
+//     exponent base, P = 2^(s - base) * value scale stored as bf16.  The base
+//     moves only when a score lies kSlack above it, so an ordinary job reads its
+//     scores once and leaves O alone.  Four groups at 80 registers were slower.
+// With more units than CTAs a unit is two blocks, one for each group, so that a
+// chunk is staged once for 256 queries (64x64, 8 heads of 40, one map: 80 us, 112
+// in units of one block); otherwise the groups take the chunks of one block in
+// turn and their rows (O, base, sum) are merged through shared memory at the end
+// of the unit.  Where units are few, the CTAs of a cluster also split the keys and
+// push their rows to the row's owner through distributed shared memory (25 tiles
+// of 4x4 against 4096 keys, 32 units on 148 SMs: 26 us, 57 without the split; 32x32,
+// 8 heads of 80: 23 and 30 us).  The CUDA-core kernel takes 2575 us for the 25
+// tiles and 5680 us for the map.
+//
+// Bound: the softmax groups.  One map (4096 queries and keys, 8 heads of 40) is
+// 134M exponentials, 30 us at 16 a cycle and SM, and 21.5 GFLOP (26 with heads of
+// 40 run as 48), 16 us at the bf16 rate.  A job of 128 queries x 128 keys takes
+// about 2500 cycles of a group: the scores' way out of tensor memory, scaling,
+// exponentials and packing of its 128 values a lane, with the two groups' four
+// schedulers shared with staging (codes to bf16) and issue.
 #include <algorithm>
 #include <atomic>
 #include <math.h>
@@ -42,14 +55,13 @@ constexpr int kRows = 128;
 constexpr int kGroup = 128;         // threads of a softmax group
 constexpr int kStage = 192;         // staging threads
 constexpr int kCluster = 4;
-constexpr int kMaxStages = 3;
 constexpr float kSlack = 40.0f;     // how far (base 2) a score may lie above the exponent base
 
 // Shared and tensor memory for heads of up to KD (64 or 128) channels.
 template <int KD>
 struct Lay {
     static constexpr int kKeys = KD == 64 ? 128 : 64;                 // keys of a chunk
-    static constexpr int kSoft = 2 * kGroup, kMmaWarp = kSoft / 32, kThreads = kSoft + 64 + kStage;
+    static constexpr int kSoft = 2 * kGroup, kThreads = kSoft + 64 + kStage;
     static constexpr int kAtoms = KD / 64;                            // 64-channel blocks of 128-byte rows
     static constexpr int kStages = 3;                                 // chunk ring
     static constexpr uint32_t kQAtom = kRows * 128, kKvAtom = kKeys * 128;
@@ -249,7 +261,7 @@ __device__ __forceinline__ void mma_s_w(uint32_t d, uint64_t a, uint64_t b, uint
         : "memory");
 }
 
-// O (+)= P V over a chunk's 64 keys for one 64-channel block of V: four steps
+// O (+)= P V over 64 keys for one 64-channel block of V: four steps
 // of 16 keys (8 columns of P in tensor memory, 2 KB of V), from one elected lane.
 __device__ __forceinline__ void mma_pv_w(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
 {
@@ -385,7 +397,7 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kOffBar + kAbort);
     WsHeader *hdr = p.hdr;
 
-    if (warp == L::kMmaWarp) {
+    if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(bar + kTmemSlot),
                      "r"(kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -414,7 +426,7 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
         w.u_step = (int)(gridDim.x / kCluster) * w.per;
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kMaxStages; ++i) {
+        for (int i = 0; i < L::kStages; ++i) {
             mbar_init(bar + kBarKvFull + 8u * i, kStage);
             mbar_init(bar + kBarKvEmpty + 8u * i, 1);
         }
@@ -428,7 +440,7 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
         mbar_init(bar + kBarQFull, kStage);
         mbar_init(bar + kBarQEmpty, 1);
         // one arrival a warp: of every softmax warp of the unit's CTAs; of the
-        // warps whose rows this CTA owns (kGroups s parts of 128 / s rows)
+        // warps whose rows this CTA owns (two groups of s CTAs, 128 / s rows of each)
         mbar_init(bar + kBarReady, (uint32_t)(L::kSoft / 32 * w.split));
         mbar_init(bar + kBarPush, (uint32_t)L::kSoft / 32);
         mbar_init(bar + kBarDrain, 1);
@@ -443,10 +455,12 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
     cluster_arrive();   // the peers' barriers are initialised before the first remote arrival
     bool joined = false;
 
-    if (warp >= L::kMmaWarp) {
-        if (warp > L::kMmaWarp + 1) {
+    // roles: warps 0 and 1 the products (the lowest numbers: the schedulers serve
+    // them first), 4 .. 11 the softmax groups, the others staging
+    if (warp < 4 || warp >= 12) {
+        if (warp >= 2) {
             // ---- staging
-            const int t = (int)threadIdx.x - (L::kSoft + 64);
+            const int t = (int)threadIdx.x - (warp < 4 ? 64 : 64 + L::kSoft);
             const int nk = p.dh >> 3, nkv = args.dhp >> 3;   // 8-channel vectors of a query row; padded to 16 channels
             constexpr int kPer = (kKeys * KD / 8 + kStage - 1) / kStage;   // vectors of K, and of V, a thread
             Stager<kPer, kKeys> K, V;
@@ -532,9 +546,8 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
             }
             __syncwarp();
         } else {
-            // ---- products: one warp the scores, one the weighted values (one warp
-            // for both took about 1300 cycles a job, more than a softmax group)
-            const bool scores = warp == L::kMmaWarp;
+            // ---- products: warp 0 the scores, warp 1 the weighted values
+            const bool scores = warp == 0;
             const uint32_t id_s = idesc_bf16(kKeys);
             const int dv0 = min(args.dvp, 64), dv1 = args.dvp - dv0;
             const uint32_t id_o0 = idesc_bf16(dv0) | (1u << 16), id_o1 = idesc_bf16(dv1) | (1u << 16);   // B (V) MN-major
@@ -620,7 +633,7 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
     } else {
         // ---- softmax: thread = query row r of group g
         constexpr int kG = 2, kSoft = L::kSoft;
-        const int g = warp >> 2;
+        const int g = (warp >> 2) - 1, tid = (int)threadIdx.x - 128;
         const int r = (warp & 3) * 32 + lane;
         const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t t_o = t_row + L::tmem_o(g);
@@ -846,7 +859,7 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
                     ok = false;
                     continue;
                 }
-                for (int item = (int)threadIdx.x; item < rows * ng; item += kSoft) {
+                for (int item = tid; item < rows * ng; item += kSoft) {
                     const int j = item % rows, gi = item / rows;
                     const int slot = x.slot0 + w.rank_split * rows + j;
                     const int64_t pix = slot < w.slots ? query_pixel(p, x.n, slot) : -1;
@@ -898,7 +911,7 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
             // the two groups share the block: each keeps the 8-channel groups of
             // its parity and merges them with the other's copy of them
             float o[KD / 2];
-            const int tid = (int)threadIdx.x, pt = (g ^ 1) * kGroup + r;
+            const int pt = (g ^ 1) * kGroup + r;
             soft_sync<kSoft>();   // the last unit's rows have been read
 #pragma unroll
             for (int k = 0; k < KD / 16; ++k) {
@@ -947,7 +960,7 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
         cluster_wait();
     tc_fence_before();
     __syncthreads();
-    if (warp == L::kMmaWarp) {
+    if (warp == 0) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
     }
