@@ -569,8 +569,9 @@ int sige_qlinear_path(int32_t c);
  *   workspace : as (10)
  * sige_attention_qcache_path says which kernel a call gets.  On the tensor
  * cores the weights exp(s - max), times the value's scale, are rounded to bf16
- * before the second product (as in (8)).  Errors: SIGE_ERR_INVALID_ARG (NULL,
- * sizes that differ, D or Dv not a multiple of heads, overlap, misaligned
+ * before the second product (as in (8)), against a running maximum that may lag
+ * by up to 2^40: values (code * scale) have to stay below 2^60.  Errors:
+ * SIGE_ERR_INVALID_ARG (NULL, sizes that differ, D or Dv not a multiple of heads, overlap, misaligned
  * list), SIGE_ERR_UNSUPPORTED (q not bf16 NHWC, head width > 256, group not a
  * multiple of the head width, block > 64, sizes past 32 bits),
  * SIGE_ERR_WORKSPACE, SIGE_ERR_CUDA. */
@@ -580,9 +581,10 @@ int sige_attention_qcache(const void *q, const sige_tensor_desc *qd, const void 
                           const int32_t *idx, const int32_t *count, int32_t capacity, void *o, void *workspace,
                           size_t workspace_bytes, sige_stream_t stream);
 
-/* Which kernel sige_attention_qcache runs for head widths dh and dvh (16-byte
- * aligned buffers): 1 = tcgen05 tensor cores, 0 = CUDA cores,
- * SIGE_ERR_UNSUPPORTED above 256.  Host only. */
+/* Which kernel sige_attention_qcache runs for head widths dh and dvh: 1 =
+ * tcgen05 tensor cores (up to 192; widths that are multiples of 8 and 16-byte
+ * aligned buffers are the fast form), 0 = CUDA cores, SIGE_ERR_UNSUPPORTED above
+ * 256.  Host only. */
 int sige_attention_qcache_path(int32_t dh, int32_t dvh);
 
 /* ------------------------------------------------------------ utilities */

@@ -6,8 +6,8 @@
 // pruning the query tokens of unedited regions; the cache's formats are this
 // library's.)
 //
-// This file holds the call and the CUDA-core kernel, which takes every head
-// width up to 256: a CTA owns 64 query slots of one (batch item, head) and
+// This file holds the call and the CUDA-core kernel, for head widths the
+// tensor-core kernel has no room for (193 .. 256): a CTA owns 64 query slots of one (batch item, head) and
 // walks the keys in chunks of 32 decoded into shared memory; a warp owns 8
 // queries, lane j scores key j, and a running maximum and sum per query
 // (float32) rescale the lanes' accumulators of the columns lane + 32 c.

@@ -29,8 +29,13 @@
 // of the unit.  Where units are few, the CTAs of a cluster also split the keys and
 // push their rows to the row's owner through distributed shared memory (25 tiles
 // of 4x4 against 4096 keys, 32 units on 148 SMs: 26 us, 57 without the split; 32x32,
-// 8 heads of 80: 23 and 30 us).  The CUDA-core kernel takes 2575 us for the 25
-// tiles and 5680 us for the map.
+// 8 heads of 80: 23 and 30 us).
+//
+// Head widths up to 192 in three layouts (64, 128, 192 channels staged a row), each
+// in two forms: vectors of 8 codes and 16-byte query and output vectors, or (kAny:
+// widths that are not multiples of 8, unaligned tensors) codes out of aligned words
+// and the rest element by element: 43 us for the 25 tiles, 135 for the map (the
+// CUDA-core kernel: 2575 and 5680).
 //
 // Bound: the softmax groups.  One map (4096 queries and keys, 8 heads of 40) is
 // 134M exponentials, 30 us at 16 a cycle and SM, and 21.5 GFLOP (26 with heads of
@@ -57,41 +62,44 @@ constexpr int kStage = 192;         // staging threads
 constexpr int kCluster = 4;
 constexpr float kSlack = 40.0f;     // how far (base 2) a score may lie above the exponent base
 
-// Shared and tensor memory for heads of up to KD (64 or 128) channels.
+// Shared and tensor memory for heads of up to KD (64, 128 or 192) channels.
 template <int KD>
 struct Lay {
     static constexpr int kKeys = KD == 64 ? 128 : 64;                 // keys of a chunk
     static constexpr int kSoft = 2 * kGroup, kThreads = kSoft + 64 + kStage;
     static constexpr int kAtoms = KD / 64;                            // 64-channel blocks of 128-byte rows
-    static constexpr int kStages = 3;                                 // chunk ring
+    static constexpr int kStages = KD == 192 ? 2 : 3;                 // chunk ring
     static constexpr uint32_t kQAtom = kRows * 128, kKvAtom = kKeys * 128;
     static constexpr uint32_t kOffQ = 0;                              // queries, a second block's at kOffQ2
     static constexpr uint32_t kOffQ2 = kAtoms * kQAtom;
-    // rows exchanged by the groups of a block, half a row a softmax thread (over
-    // the second block's queries: units of one block only)
+    // rows exchanged by the groups of a block, 32 floats a softmax thread at a
+    // time (over the second block's queries: units of one block only)
     static constexpr uint32_t kOffX = kOffQ2;
-    static constexpr uint32_t kOffK = kOffX + kSoft * (KD / 2) * 4;   // [stage][K atoms, V atoms]
+    static constexpr uint32_t kX = kSoft * 32 * 4 > kAtoms * kQAtom ? kSoft * 32 * 4 : kAtoms * kQAtom;
+    static constexpr uint32_t kOffK = kOffX + kX;                     // [stage][K atoms, V atoms]
     static constexpr uint32_t kKvStage = 2 * kAtoms * kKvAtom;
     static constexpr uint32_t kScStage = 2 * kKeys * 4;
     static constexpr uint32_t kOffSc = kOffK + kStages * kKvStage;    // [stage][key scales, value scales]
     static constexpr uint32_t kOffMl = kOffSc + kStages * kScStage;   // (max, sum) of a softmax thread's row
     static constexpr uint32_t kOffBar = kOffMl + kSoft * 8;
     static constexpr uint32_t kBytes = kOffBar + 256 + 1024;          // + alignment slack
-    // rows pushed by the CTAs of a split unit, over the exchange rows and the
-    // ring (both idle by then): kSoft rows of KD floats
-    static constexpr uint32_t kOffPush = kOffX;
+    // rows pushed by the CTAs of a split unit, over the queries and the ring
+    // (both idle by then): kSoft rows of KD floats
+    static constexpr uint32_t kOffPush = 0;
     static_assert(kOffPush + kSoft * KD * 4 <= kOffSc, "pushed rows");
-    static_assert(kOffQ2 + kAtoms * kQAtom <= kOffK && kOffK % 1024 == 0, "second block's queries");
+    static_assert(kOffK % 1024 == 0, "swizzled rows");
     static_assert(kBytes <= 227 * 1024, "shared memory");
     // Tensor memory, 512 columns.  Heads up to 64: a group's S (128 columns), its
     // P apart (64), so that the next S comes while the weights are still being
-    // made; O (64).  Wider heads: two buffers of 64 columns a group, P over S; O
-    // (128).
+    // made; O (64).  Up to 128: two buffers of 64 columns a group, P over S; O
+    // (128).  Up to 192: one such buffer; O (192).
     static constexpr bool kApart = KD == 64;
-    static constexpr int kBufs = kApart ? 1 : 2;
-    static __device__ __forceinline__ uint32_t tmem_s(uint32_t g, uint32_t b) { return kApart ? 128u * g : 64u * (2 * g + b); }
+    static constexpr int kBufs = KD == 128 ? 2 : 1;
+    static constexpr uint32_t kOCol = KD == 64 ? 384 : KD == 128 ? 256 : 128;
+    static __device__ __forceinline__ uint32_t tmem_s(uint32_t g, uint32_t b) { return kApart ? 128u * g : 64u * (kBufs * g + b); }
     static __device__ __forceinline__ uint32_t tmem_p(uint32_t g, uint32_t b) { return kApart ? 256u + 64u * g : tmem_s(g, b); }
-    static __device__ __forceinline__ uint32_t tmem_o(uint32_t g) { return kApart ? 384u + 64u * g : 256u + 128u * g; }
+    static __device__ __forceinline__ uint32_t tmem_o(uint32_t g) { return kOCol + (uint32_t)KD * g; }
+    static_assert(kOCol + 2 * KD == 512, "tensor memory");
 };
 
 constexpr uint32_t kBarKvFull = 0;      // + 8 stage
@@ -116,8 +124,9 @@ constexpr int kSiteKvEmpty = 401, kSiteKvFull = 402, kSiteQEmpty = 403, kSitePFu
 struct Args {
     AttnQParams a;
     int32_t dhp, dvp;         // head widths padded to 16
+    int32_t nk, nv;           // 8-channel vectors of a query or key row, of a value row
     float sc;                 // log2(e) / sqrt(dh): scores in base-2 exponent units
-    UDiv dkv, dvv;            // 8-channel vectors of a key row (padded), of a value row
+    UDiv dkv, dvv;            // dhp / 8, nv
 };
 
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b)
@@ -163,6 +172,43 @@ __device__ __forceinline__ uint4 codes8(uint2 w)
     }
 }
 
+// The first n (1 .. 8) of 8 codes from element e on, at any address, zeros for
+// the others: the aligned words that hold them, shifted into place.
+__device__ __forceinline__ uint2 codes_any(const uint8_t *codes, int64_t e, uint32_t n, bool s4)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(codes) + (uintptr_t)(s4 ? e >> 1 : e);
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(a & ~(uintptr_t)3);
+    const uint32_t sh = 8u * (uint32_t)(a & 3) + (s4 ? 4u * (uint32_t)(e & 1) : 0u), bits = s4 ? 4u * n : 8u * n;
+    const uint32_t w0 = __ldg(w), w1 = sh + bits > 32u ? __ldg(w + 1) : 0u, w2 = sh + bits > 64u ? __ldg(w + 2) : 0u;
+    uint2 r = make_uint2(__funnelshift_r(w0, w1, sh), __funnelshift_r(w1, w2, sh));
+    r.x &= bits < 32u ? (1u << bits) - 1u : 0xFFFFFFFFu;
+    r.y &= bits < 32u ? 0u : bits < 64u ? (1u << (bits - 32u)) - 1u : 0xFFFFFFFFu;
+    return r;
+}
+// The first n of 8 elements of a query row.
+__device__ __forceinline__ uint4 bf16_any(const __nv_bfloat16 *q, int n)
+{
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (k < n)
+            w[k >> 1] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short *>(q) + k) << (16 * (k & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// 8 channels of an output row, kAny: the first n of them, at any address.
+template <bool kAny>
+__device__ __forceinline__ void put8(__nv_bfloat16 *dst, const float *v, float inv, int n)
+{
+    if constexpr (kAny) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < n)
+                dst[k] = __float2bfloat16_rn(v[k] * inv);
+    } else {
+        store8(dst, v, inv);
+    }
+}
+
 // Swizzled place of 8-channel vector v of row j: block v / 8, 16 bytes at v ^ j.
 __device__ __forceinline__ uint32_t place(uint32_t atom, int j, int v)
 {
@@ -172,21 +218,26 @@ __device__ __forceinline__ uint32_t place(uint32_t atom, int j, int v)
 // One staging thread's share of a chunk of K or V: up to N vectors of 8 codes,
 // vector i being (key j, vector v) number t + kStage i of the chunk, v fastest.
 // Where they lie in the chunk and in shared memory is worked out once; the next
-// chunk's codes are on their way in registers.
-template <int N, int kKeys>
+// chunk's codes are on their way in registers.  kAny: code by code, a row's last
+// vector as far as the head goes.
+template <int N, int kKeys, bool kAny>
 struct Stager {
-    uint32_t src[N];      // byte offset from the chunk's first key
-    uint32_t to[N];       // offset in the staged rows | key << 16 (kKeys: no such vector, kZero: zeros for padded channels)
+    uint32_t src[N];      // offset from the chunk's first key: bytes (kAny: codes)
+    uint32_t to[N];       // offset in the staged rows (kAny: + codes of the vector) | key << 16 (kKeys: no such vector,
+                          // kZero: zeros for padded channels)
     uint2 raw[N];
     static constexpr uint32_t kZero = 0x7FFF;
-    const uint8_t *at;    // the next chunk to fetch
-    uint32_t step;        // bytes of a chunk's keys
+    const uint8_t *at;    // the next chunk to fetch (kAny: the codes)
+    int64_t e0;           // kAny: the next chunk's first code
+    uint32_t step;        // bytes (kAny: codes) of a chunk's keys
     int fmt;
 
-    __device__ __forceinline__ void init(int t, int nv, UDiv dnv, int real, int ch, int format, uint32_t atom)
+    // nv vectors staged a row, the first `real` of them with codes of a head of
+    // `head` channels; ch channels a key
+    __device__ __forceinline__ void init(int t, int nv, UDiv dnv, int real, int head, int ch, int format, uint32_t atom)
     {
         fmt = format;
-        const int sh = format == SIGE_Q_S4 ? 1 : 0;
+        const int sh = !kAny && format == SIGE_Q_S4 ? 1 : 0;
         step = ((uint32_t)kKeys * (uint32_t)ch) >> sh;
         const int dj = (int)udiv(kStage, dnv), dv = kStage - dj * nv;
         int j = (int)udiv((uint32_t)t, dnv), v = t - j * nv;
@@ -194,6 +245,8 @@ struct Stager {
         for (int i = 0; i < N; ++i) {
             src[i] = ((uint32_t)j * (uint32_t)ch + 8u * (uint32_t)v) >> sh;
             to[i] = j >= kKeys ? (uint32_t)kKeys << 16 : place(atom, j, v) | ((v < real ? (uint32_t)j : kZero) << 16);
+            if (kAny && j < kKeys)
+                to[i] |= (uint32_t)max(0, min(8, head - 8 * v));
             j += dj;
             v += dv;
             if (v >= nv) {
@@ -202,12 +255,30 @@ struct Stager {
             }
         }
     }
-    __device__ __forceinline__ void start(const uint8_t *codes, int64_t e) { at = codes + (fmt == SIGE_Q_S4 ? e >> 1 : e); }
+    __device__ __forceinline__ void start(const uint8_t *codes, int64_t e)
+    {
+        if constexpr (kAny) {
+            at = codes;
+            e0 = e;
+        } else {
+            at = codes + (fmt == SIGE_Q_S4 ? e >> 1 : e);
+        }
+    }
 
     // the next chunk, of which `nkeys` keys exist (zeros for the others)
     __device__ __forceinline__ void fetch(int nkeys)
     {
         const uint32_t lim = (uint32_t)min(nkeys, kKeys) << 16;
+        if constexpr (kAny) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                raw[i] = make_uint2(0, 0);
+                if (to[i] < lim)
+                    raw[i] = codes_any(at, e0 + src[i], to[i] & 15u, fmt == SIGE_Q_S4);
+            }
+            e0 += step;
+            return;
+        }
         if (fmt == SIGE_Q_S4) {
 #pragma unroll
             for (int i = 0; i < N; ++i)
@@ -229,7 +300,7 @@ struct Stager {
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if (to[i] >> 16 != kKeys)
-                sts128(base + (to[i] & 0xFFFFu), codes8<kFmt>(raw[i]));
+                sts128(base + (to[i] & 0xFFF0u), codes8<kFmt>(raw[i]));
     }
     __device__ __forceinline__ void store(uint32_t base)
     {
@@ -382,7 +453,7 @@ __device__ __forceinline__ Unit unit_at(const AttnQParams &p, const Work &w, int
 
 using namespace at;
 
-template <int KD>
+template <int KD, bool kAny>
 __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(const __grid_constant__ at::Args args)
 {
     using L = Lay<KD>;
@@ -461,11 +532,11 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
         if (warp >= 2) {
             // ---- staging
             const int t = (int)threadIdx.x - (warp < 4 ? 64 : 64 + L::kSoft);
-            const int nk = p.dh >> 3, nkv = args.dhp >> 3;   // 8-channel vectors of a query row; padded to 16 channels
+            const int nk = args.nk, nkv = args.dhp >> 3;   // (padded to 16 channels)
             constexpr int kPer = (kKeys * KD / 8 + kStage - 1) / kStage;   // vectors of K, and of V, a thread
-            Stager<kPer, kKeys> K, V;
-            K.init(t, nkv, args.dkv, nk, p.D, p.kfmt, L::kKvAtom);
-            V.init(t, p.dvh >> 3, args.dvv, p.dvh >> 3, p.Dv, p.vfmt, L::kKvAtom);
+            Stager<kPer, kKeys, kAny> K, V;
+            K.init(t, nkv, args.dkv, nk, p.dh, p.D, p.kfmt, L::kKvAtom);
+            V.init(t, args.nv, args.dvv, args.nv, p.dvh, p.Dv, p.vfmt, L::kKvAtom);
             int it = 0, st = 0, nu = 0;
             uint32_t ph = 1;
             bool ok = true;
@@ -507,8 +578,13 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
 #pragma unroll
                         for (int g = 0; g < 4; ++g) {
                             q[g] = make_uint4(0, 0, 0, 0);
-                            if (pix >= 0 && g0 + g < nk)
-                                q[g] = ld_nc16(p.q + pix * p.D + x.head * p.dh + 8 * (g0 + g));
+                            if (pix >= 0 && g0 + g < nk) {
+                                const __nv_bfloat16 *src = p.q + pix * p.D + x.head * p.dh + 8 * (g0 + g);
+                                if constexpr (kAny)
+                                    q[g] = bf16_any(src, p.dh - 8 * (g0 + g));
+                                else
+                                    q[g] = ld_nc16(src);
+                            }
                         }
 #pragma unroll
                         for (int g = 0; g < 4; ++g)
@@ -549,9 +625,11 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
             // ---- products: warp 0 the scores, warp 1 the weighted values
             const bool scores = warp == 0;
             const uint32_t id_s = idesc_bf16(kKeys);
-            const int dv0 = min(args.dvp, 64), dv1 = args.dvp - dv0;
-            const uint32_t id_o0 = idesc_bf16(dv0) | (1u << 16), id_o1 = idesc_bf16(dv1) | (1u << 16);   // B (V) MN-major
-            const int ks0 = min(args.dhp, 64) / 16, ks1 = args.dhp / 16 - ks0;   // 16-channel steps of each block
+            // 64-channel blocks: of the last of them, the 16-channel steps of K and
+            // the product's shape with V (B, MN-major)
+            const int kb = (args.dhp + 63) / 64, vb = (args.dvp + 63) / 64;
+            const int ks_last = args.dhp / 16 - 4 * (kb - 1);
+            const uint32_t id_o = idesc_bf16(64) | (1u << 16), id_o_last = idesc_bf16(args.dvp - 64 * (vb - 1)) | (1u << 16);
             const uint64_t qd = desc_sw128(sb + L::kOffQ), q2d = desc_sw128(sb + (w.pairs ? L::kOffQ2 : L::kOffQ));
             const uint64_t kd = desc_sw128(sb + L::kOffK), vd = desc_sw128(sb + L::kOffK + L::kAtoms * L::kKvAtom);
             int st = 0, nu = 0;   // stage of the next job's chunk; units so far
@@ -590,9 +668,11 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
                         tc_fence_after();
                         const uint64_t ad = g ? q2d : qd, bd = kd + (uint64_t)((uint32_t)st * (L::kKvStage >> 4));
                         const uint32_t d = tmem + L::tmem_s(g, b);
-                        mma_s_w(d, ad, bd, id_s, 0, ks0);
-                        if (KD > 64 && ks1 > 0)
-                            mma_s_w(d, ad + (L::kQAtom >> 4), bd + (L::kKvAtom >> 4), id_s, 1, ks1);
+#pragma unroll
+                        for (int c = 0; c < L::kAtoms; ++c)
+                            if (c < kb)
+                                mma_s_w(d, ad + c * (L::kQAtom >> 4), bd + c * (L::kKvAtom >> 4), id_s, c > 0,
+                                        c + 1 < kb ? 4 : ks_last);
                         tc_commit_w(bar + kBarSFull + 8u * buf);
                         if (j + 1 == jobs)
                             tc_commit_w(bar + kBarQEmpty);
@@ -605,11 +685,12 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
                         const uint32_t d = tmem + L::tmem_o(g), pa = tmem + L::tmem_p(g, b);
                         const uint64_t bd = vd + (uint64_t)((uint32_t)st * (L::kKvStage >> 4));
 #pragma unroll
-                        for (int k = 0; k < kKeys / 64; ++k) {
-                            mma_pv_w(d, pa + 32u * k, bd + 512u * k, id_o0, j >= 2 || k > 0);
-                            if (KD > 64 && dv1 > 0)
-                                mma_pv_w(d + 64u, pa + 32u * k, bd + (L::kKvAtom >> 4) + 512u * k, id_o1, j >= 2 || k > 0);
-                        }
+                        for (int k = 0; k < kKeys / 64; ++k)
+#pragma unroll
+                            for (int c = 0; c < L::kAtoms; ++c)
+                                if (c < vb)
+                                    mma_pv_w(d + 64u * c, pa + 32u * k, bd + c * (L::kKvAtom >> 4) + 512u * k,
+                                             c + 1 < vb ? id_o : id_o_last, j >= 2 || k > 0);
                         tc_commit_w(bar + kBarPvDone + 8u * buf);
                         if (!w.pairs || g)
                             tc_commit_w(bar + kBarKvEmpty + 8u * st);
@@ -637,7 +718,7 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
         const int r = (warp & 3) * 32 + lane;
         const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t t_o = t_row + L::tmem_o(g);
-        const int ng = p.dvh >> 3;             // 8-channel groups of an output row
+        const int ng = args.nv;                // 8-channel groups of an output row
         int chunk = 0, m_it = 0;               // chunks of the CTA so far; jobs of this group
         bool ok = true;
         for (int u = w.u_first; u < w.units; u += w.u_step) {
@@ -882,7 +963,7 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
                         acc[4] = fmaf(wt, y1.x, acc[4]); acc[5] = fmaf(wt, y1.y, acc[5]);
                         acc[6] = fmaf(wt, y1.z, acc[6]); acc[7] = fmaf(wt, y1.w, acc[7]);
                     }
-                    store8(p.o + pix * p.Dv + x.head * p.dvh + 8 * gi, acc, x.keys > 0 ? 1.0f / sum : 0.0f);
+                    put8<kAny>(p.o + pix * p.Dv + x.head * p.dvh + 8 * gi, acc, x.keys > 0 ? 1.0f / sum : 0.0f, p.dvh - 8 * gi);
                 }
                 continue;
             }
@@ -901,59 +982,68 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
                     for (int q = 0; q < 16; ++q)
                         v[q] = mine ? v[q] : 0.0f;
                     if (pix >= 0)
-                        store8(dst + pc, v, inv);
+                        put8<kAny>(dst + pc, v, inv, p.dvh - pc);
                     if (pix >= 0 && pc / 8 + 1 < ng)
-                        store8(dst + pc + 8, v + 8, inv);
+                        put8<kAny>(dst + pc + 8, v + 8, inv, p.dvh - pc - 8);
                 }
                 tc_fence_before();
                 continue;
             }
             // the two groups share the block: each keeps the 8-channel groups of
-            // its parity and merges them with the other's copy of them
-            float o[KD / 2];
+            // its parity and merges them with the other's copy of them, 64
+            // channels at a time
             const int pt = (g ^ 1) * kGroup + r;
-            soft_sync<kSoft>();   // the last unit's rows have been read
+            float wa = 0.0f, wb = 0.0f, inv = 0.0f;
+#pragma unroll 1
+            for (int p0 = 0; p0 < args.dvp; p0 += 64) {
+                float o[32];
+                soft_sync<kSoft>();   // the last rows have been read
 #pragma unroll
-            for (int k = 0; k < KD / 16; ++k) {
-                float v[16];
-                const bool in = ok && mine && 16 * k < args.dvp;
-                if (in)
-                    tmem_ld16(t_o + 16u * k, v);
-                const uint32_t at = sb + L::kOffX + (uint32_t)(2 * k * kSoft + tid) * 16u;
-                float m[8];
+                for (int k = 0; k < 4; ++k) {
+                    float v[16];
+                    const bool in = ok && mine && p0 + 16 * k < args.dvp;
+                    if (in)
+                        tmem_ld16(t_o + (uint32_t)(p0 + 16 * k), v);
+                    const uint32_t at = sb + L::kOffX + (uint32_t)(2 * k * kSoft + tid) * 16u;
+                    float m[8];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const float a = in ? v[q] : 0.0f, c = in ? v[8 + q] : 0.0f;
-                    m[q] = g ? a : c;
-                    o[8 * k + q] = g ? c : a;
+                    for (int q = 0; q < 8; ++q) {
+                        const float a = in ? v[q] : 0.0f, c = in ? v[8 + q] : 0.0f;
+                        m[q] = g ? a : c;
+                        o[8 * k + q] = g ? c : a;
+                    }
+                    sts_f4(at, m);
+                    sts_f4(at + kSoft * 16u, m + 4);
                 }
-                sts_f4(at, m);
-                sts_f4(at + kSoft * 16u, m + 4);
+                if (p0 == 0)   // (a sum of -1: no key)
+                    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sb + L::kOffMl + (uint32_t)tid * 8u), "f"(m_used),
+                                 "f"(mine ? l : -1.0f) : "memory");
+                soft_sync<kSoft>();
+                if (p0 == 0) {
+                    const float2 ml = lds_f2(sb + L::kOffMl + (uint32_t)pt * 8u);
+                    const bool other = ml.y != -1.0f;
+                    const float mm = fmaxf(mine ? m_used : -INFINITY, other ? ml.x : -INFINITY);
+                    wa = mine ? ex2(m_used - mm) : 0.0f;
+                    wb = other ? ex2(ml.x - mm) : 0.0f;
+                    const float sum = (mine ? l * wa : 0.0f) + (other ? ml.y * wb : 0.0f);
+                    inv = mine || other ? 1.0f / sum : 0.0f;   // (no key at all: zeros)
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int gi = p0 / 8 + 2 * k + g;
+                    if (ok && pix >= 0 && gi < ng) {
+                        const uint32_t src = sb + L::kOffX + (uint32_t)(2 * k * kSoft + pt) * 16u;
+                        const float4 y0 = lds_f4(src), y1 = lds_f4(src + kSoft * 16u);
+                        float *oo = o + 8 * k;
+                        oo[0] = fmaf(y0.x, wb, oo[0] * wa); oo[1] = fmaf(y0.y, wb, oo[1] * wa);
+                        oo[2] = fmaf(y0.z, wb, oo[2] * wa); oo[3] = fmaf(y0.w, wb, oo[3] * wa);
+                        oo[4] = fmaf(y1.x, wb, oo[4] * wa); oo[5] = fmaf(y1.y, wb, oo[5] * wa);
+                        oo[6] = fmaf(y1.z, wb, oo[6] * wa); oo[7] = fmaf(y1.w, wb, oo[7] * wa);
+                        put8<kAny>(dst + 8 * gi, oo, inv, p.dvh - 8 * gi);
+                    }
+                }
             }
             tc_fence_before();
-            // (a sum of -1: no key)
-            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sb + L::kOffMl + (uint32_t)tid * 8u), "f"(m_used),
-                         "f"(mine ? l : -1.0f) : "memory");
-            soft_sync<kSoft>();
-            const float2 ml = lds_f2(sb + L::kOffMl + (uint32_t)pt * 8u);
-            const bool other = ml.y != -1.0f;
-            const float mm = fmaxf(mine ? m_used : -INFINITY, other ? ml.x : -INFINITY);
-            const float wa = mine ? ex2(m_used - mm) : 0.0f, wb = other ? ex2(ml.x - mm) : 0.0f;
-            const float sum = (mine ? l * wa : 0.0f) + (other ? ml.y * wb : 0.0f);
-            const float inv = mine || other ? 1.0f / sum : 0.0f;   // (no key at all: zeros)
-#pragma unroll
-            for (int k = 0; k < KD / 16; ++k) {
-                if (ok && pix >= 0 && 2 * k + g < ng) {
-                    const uint32_t src = sb + L::kOffX + (uint32_t)(2 * k * kSoft + pt) * 16u;
-                    const float4 y0 = lds_f4(src), y1 = lds_f4(src + kSoft * 16u);
-                    float *oo = o + 8 * k;
-                    oo[0] = fmaf(y0.x, wb, oo[0] * wa); oo[1] = fmaf(y0.y, wb, oo[1] * wa);
-                    oo[2] = fmaf(y0.z, wb, oo[2] * wa); oo[3] = fmaf(y0.w, wb, oo[3] * wa);
-                    oo[4] = fmaf(y1.x, wb, oo[4] * wa); oo[5] = fmaf(y1.y, wb, oo[5] * wa);
-                    oo[6] = fmaf(y1.z, wb, oo[6] * wa); oo[7] = fmaf(y1.w, wb, oo[7] * wa);
-                    store8(dst + 8 * (2 * k + g), oo, inv);
-                }
-            }
         }
     }
     if (!joined)
@@ -971,14 +1061,12 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
 
 // ------------------------------------------------------------------ host
 
-bool attention_qcache_tc_scope(int dh, int dvh)
-{
-    return dh > 0 && dvh > 0 && dh % 8 == 0 && dvh % 8 == 0 && dh <= 128 && dvh <= 128;
-}
+bool attention_qcache_tc_scope(int dh, int dvh) { return dh > 0 && dvh > 0 && dh <= 192 && dvh <= 192; }
 
-template <int KD>
+template <int KD, bool kAny>
 static int launch_kd(const at::Args &a, int64_t units_max, cudaStream_t stream)
 {
+    constexpr auto kernel = k_attn_qcache_tc<KD, kAny>;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
         return SIGE_ERR_CUDA;
@@ -997,24 +1085,24 @@ static int launch_kd(const at::Args &a, int64_t units_max, cudaStream_t stream)
     static std::atomic<int> clusters_of[64];   // co-resident clusters, per device
     int ncl = clusters_of[dev].load(std::memory_order_acquire);
     if (ncl == 0) {
-        if (cudaFuncSetAttribute(k_attn_qcache_tc<KD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)at::Lay<KD>::kBytes) != cudaSuccess) {
             cudaGetLastError();
             return SIGE_ERR_CUDA;
         }
         cfg.gridDim = dim3(at::kCluster * (device_sm_count() / at::kCluster));
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&ncl, k_attn_qcache_tc<KD>, &cfg) != cudaSuccess || ncl < 1) {
+        if (cudaOccupancyMaxActiveClusters(&ncl, kernel, &cfg) != cudaSuccess || ncl < 1) {
             cudaGetLastError();
             return SIGE_ERR_CUDA;
         }
         clusters_of[dev].store(ncl, std::memory_order_release);
     }
-    prefer_max_shared(k_attn_qcache_tc<KD>);
+    prefer_max_shared_of<kernel>();
     cfg.numAttrs = 2;
     // every unit a launch can have needs at most one cluster
     cfg.gridDim = dim3((unsigned)(at::kCluster * std::max<int64_t>(1, std::min<int64_t>(ncl, units_max))));
-    if (cudaLaunchKernelEx(&cfg, k_attn_qcache_tc<KD>, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
         cudaGetLastError();
         return SIGE_ERR_CUDA;
     }
@@ -1026,10 +1114,6 @@ int launch_attention_qcache_tc(const AttnQParams &p, cudaStream_t stream)
 {
     if (!attention_qcache_tc_scope(p.dh, p.dvh))
         return 1;
-    // 16-byte query and output vectors, 8 codes at once
-    if (!aligned_to(p.q, 16) || !aligned_to(p.o, 16) || !aligned_to(p.kc, p.kfmt == SIGE_Q_S4 ? 4 : 8) ||
-        !aligned_to(p.vc, p.vfmt == SIGE_Q_S4 ? 4 : 8))
-        return 1;
     const int64_t units_max = (p.slots + at::kRows - 1) / at::kRows * p.N * p.heads;
     // (units and the bytes of a chunk's rows are counted in 32 bits)
     if (units_max > INT32_MAX / 16 || p.D > (1 << 24) || p.Dv > (1 << 24))
@@ -1038,10 +1122,22 @@ int launch_attention_qcache_tc(const AttnQParams &p, cudaStream_t stream)
     a.a = p;
     a.dhp = (p.dh + 15) / 16 * 16;
     a.dvp = (p.dvh + 15) / 16 * 16;
+    a.nk = (p.dh + 7) / 8;
+    a.nv = (p.dvh + 7) / 8;
     a.sc = (float)(1.4426950408889634 / std::sqrt((double)p.dh));
     a.dkv = udiv_make((uint32_t)(a.dhp / 8));
-    a.dvv = udiv_make((uint32_t)(p.dvh / 8));
-    return a.dhp <= 64 && a.dvp <= 64 ? launch_kd<64>(a, units_max, stream) : launch_kd<128>(a, units_max, stream);
+    a.dvv = udiv_make((uint32_t)a.nv);
+    // 16-byte query and output vectors, 8 codes at once, or element by element
+    const bool any = p.dh % 8 || p.dvh % 8 || !aligned_to(p.q, 16) || !aligned_to(p.o, 16) ||
+                     !aligned_to(p.kc, p.kfmt == SIGE_Q_S4 ? 4 : 8) || !aligned_to(p.vc, p.vfmt == SIGE_Q_S4 ? 4 : 8);
+    const int kd = std::max(a.dhp, a.dvp);
+    if (any)
+        return kd <= 64    ? launch_kd<64, true>(a, units_max, stream)
+               : kd <= 128 ? launch_kd<128, true>(a, units_max, stream)
+                           : launch_kd<192, true>(a, units_max, stream);
+    return kd <= 64    ? launch_kd<64, false>(a, units_max, stream)
+           : kd <= 128 ? launch_kd<128, false>(a, units_max, stream)
+                       : launch_kd<192, false>(a, units_max, stream);
 }
 
 } // namespace sige

@@ -282,3 +282,25 @@ def test_layer_runs_its_steps(cross, kf, heads, C):
     yref = (os_ * osc.astype(np.float64)) @ W(wo).T + oq.f64(bo) + oq.f64(x).reshape(n, h * w, C)[:, tok]
     mag = np.abs((os_ * osc.astype(np.float64)) @ W(wo).T) + np.abs(oq.f64(bo)) + np.abs(oq.f64(x).reshape(n, h * w, C)[:, tok])
     assert (np.abs(oq.f64(y).reshape(n, h * w, C)[:, tok] - yref) <= np.abs(yref) * 2.0 ** -8 * 1.0001 + mag * 2.0 ** -21).all()
+
+
+@pytest.mark.parametrize("kf,vf", [("s8", "e4m3"), ("e4m3", "s8"), ("s4", "s4")])
+@pytest.mark.parametrize("dh,dvh", [(192, 192), (184, 136), (136, 40), (24, 192), (100, 100), (12, 20), (190, 2), (66, 130), (254, 200)])
+def test_head_widths(dh, dvh, kf, vf):
+    """Every width class, aligned or not, with one block of queries for a unit and
+    with the keys split."""
+    case(dh, 2, 9, 10, 2, dh, dvh, 143, kf, vf, 4)
+    case(dvh, 1, 6, 6, 1, dh, dvh, 1111, kf, vf, 2)
+
+
+@pytest.mark.parametrize("dh,dvh", [(1, 1), (3, 5), (37, 37), (129, 63), (191, 33)])
+def test_odd_head_widths(dh, dvh):
+    case(dh, 2, 9, 10, 3, dh, dvh, 143, "s8", "e4m3", 4)
+    case(dvh, 1, 6, 6, 1, dh, dvh, 1111, "e4m3", "s8", 2)
+    # 4-bit codes of odd heads begin at odd halves of a byte
+    case(dh + 1, 1, 7, 9, 4, dh, dvh, 150, "s4", "s4", 4, token_scale=True)
+
+
+@pytest.mark.parametrize("dh", [100, 136, 192])
+def test_two_blocks_a_unit_of_wide_heads(dh):
+    case(dh, 2, 48, 47, 8, dh, dh, 200, "s8", "s8", counts=[200, 65])
