@@ -60,6 +60,12 @@ constexpr int kRows = 128;
 constexpr int kGroup = 128;         // threads of a softmax group
 constexpr int kStage = 192;         // staging threads
 constexpr int kCluster = 4;
+// Items of at most kShort keys have their weights in two bf16 terms: the rounding
+// of a weight does not average out over few keys, and with one or two it is all
+// that a row's values share (their error was 1.7 times the output rounding's).
+// The second terms lie where the weights of the next kShort keys would, and meet
+// the same values.
+constexpr int kShort = 32;
 constexpr float kSlack = 40.0f;     // how far (base 2) a score may lie above the exponent base
 
 // Shared and tensor memory for heads of up to KD (64, 128 or 192) channels.
@@ -332,20 +338,21 @@ __device__ __forceinline__ void mma_s_w(uint32_t d, uint64_t a, uint64_t b, uint
         : "memory");
 }
 
-// O (+)= P V over 64 keys for one 64-channel block of V: four steps
-// of 16 keys (8 columns of P in tensor memory, 2 KB of V), from one elected lane.
-__device__ __forceinline__ void mma_pv_w(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+// O (+)= P V over 64 keys for one 64-channel block of V: four steps of 16 keys (8
+// columns of P in tensor memory, 2 KB of V; the last two from b2 on), from one
+// elected lane.
+__device__ __forceinline__ void mma_pv_w(uint32_t d, uint32_t a, uint64_t b, uint64_t b2, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile(
-        "{\n .reg .pred p, e, t;\n .reg .b32 l, a1, a2, a3;\n .reg .b64 b1, b2, b3;\n"
-        " elect.sync l|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
+        "{\n .reg .pred p, e, t;\n .reg .b32 l, a1, a2, a3;\n .reg .b64 b1, b3;\n"
+        " elect.sync l|e, 0xffffffff;\n setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, 0, 0;\n"
         " add.u32 a1, %1, 8;\n add.u32 a2, %1, 16;\n add.u32 a3, %1, 24;\n"
-        " add.s64 b1, %2, 128;\n add.s64 b2, %2, 256;\n add.s64 b3, %2, 384;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        " add.s64 b1, %2, 128;\n add.s64 b3, %3, 128;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, t;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], %3, %4, t;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %4, t;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "l"(b2), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -690,6 +697,7 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
                             for (int c = 0; c < L::kAtoms; ++c)
                                 if (c < vb)
                                     mma_pv_w(d + 64u * c, pa + 32u * k, bd + c * (L::kKvAtom >> 4) + 512u * k,
+                                             bd + c * (L::kKvAtom >> 4) + 512u * k + (k == 0 && x.keys <= kShort ? 0u : 256u),
                                              c + 1 < vb ? id_o : id_o_last, j >= 2 || k > 0);
                         tc_commit_w(bar + kBarPvDone + 8u * buf);
                         if (!w.pairs || g)
@@ -810,6 +818,43 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
                         top[j] = fmaxf(top[j], __shfl_xor_sync(0xFFFFFFFFu, top[j], 2));
                     }
                 };
+                // the weights of an item of at most kShort keys, in two terms
+                auto brief = [&]() {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {   // (16 rows at a time: few registers)
+                        uint32_t sr[16], hi[8], lo[8];
+                        ld16x32(t_s + ((16u * half) << 16), sr);
+                        ld_wait();
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint64_t s2 = lds_2(sq + 32u * q), v2 = lds_2(sq + 4u * (kKeys + 8 * q));
+#pragma unroll
+                            for (int i2 = 0; i2 < 2; ++i2) {
+                                const int j = 2 * half + i2;
+                                const uint32_t nm = __float_as_uint(-mq[j]);
+                                const uint64_t d = fma2(pair(sr[4 * q + 2 * i2], sr[4 * q + 2 * i2 + 1]), s2, pair(nm, nm));
+                                const float x0 = 8 * q + k0 < kvalid ? lo_of(d) : -INFINITY;
+                                const float x1 = 8 * q + k0 + 1 < kvalid ? hi_of(d) : -INFINITY;
+                                const uint64_t w2 = pair(__float_as_uint(ex2(x0)), __float_as_uint(ex2(x1)));
+                                ls[j] = q == 0 ? w2 : add2(ls[j], w2);
+                                const uint64_t y = mul2(w2, v2);
+                                const uint32_t t = pack_bf16x2(lo_of(y), hi_of(y));
+                                hi[2 * q + i2] = t;
+                                lo[2 * q + i2] = pack_bf16x2(lo_of(y) - bf16_lo(t), hi_of(y) - bf16_hi(t));
+                            }
+                        }
+                        const uint32_t to = t_p + ((16u * half) << 16);
+                        st16x16(to, hi);
+                        st16x16(to + 16u, lo);
+                        if (kKeys > 64) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                hi[k] = 0;
+                            st16x16(to + 32u, hi);
+                            st16x16(to + 48u, hi);
+                        }
+                    }
+                };
                 // the group's previous P V has landed: P may be written, O rescaled.
                 // (Each phase of the barrier is waited for in turn: a parity tells
                 // two neighbouring phases apart, no more.)
@@ -860,6 +905,10 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
                                 st16(t_o + (uint32_t)pc, v);
                             }
                         }
+                    }
+                    if (kTail && x.keys <= kShort) {   // (one job, and the maximum is known)
+                        brief();
+                        break;
                     }
                     pass(std::false_type());
                     if (move || !__any_sync(0xFFFFFFFFu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kSlack))

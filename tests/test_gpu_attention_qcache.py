@@ -304,3 +304,61 @@ def test_odd_head_widths(dh, dvh):
 @pytest.mark.parametrize("dh", [100, 136, 192])
 def test_two_blocks_a_unit_of_wide_heads(dh):
     case(dh, 2, 48, 47, 8, dh, dh, 200, "s8", "s8", counts=[200, 65])
+
+
+@pytest.mark.parametrize("kf,vf", [("s8", "s8"), ("e4m3", "s4")])
+@pytest.mark.parametrize("dh", [16, 40, 100, 128, 160])
+@pytest.mark.parametrize("keys,counts", [(1, None), (2, [2, 1]), (32, [32, 17]), (150, [31, 32]), (4096, [3, 32])])
+def test_short_items_keep_their_weights(dh, keys, counts, kf, vf):
+    """Up to 32 keys: weights in two bf16 terms, 2^-17 (twice half a step, once for
+    the first term's remainder) in the place of one term's 2^-8; the rest as bound()."""
+    rng = np.random.default_rng(dh + keys)
+    n, h, w, heads = 2, 9, 8, 2
+    q = torch.from_numpy(rng.normal(size=(n, h, w, heads * dh))).to(torch.bfloat16)
+    K, kq, ks = random_cache(rng, n, keys, 1, heads * dh, dh, kf)
+    V, vq, vs = random_cache(rng, n, keys, 1, heads * dh, dh, vf)
+    kc = None if counts is None else torch.tensor(counts, dtype=torch.int32, device=DEV)
+    o = sige.sige_attention_qcache(q.to(DEV), K, V, heads, key_counts=kc)
+    o = o.double().cpu().numpy().reshape(n, h * w, -1)
+    k = (kq.reshape(*ks.shape, -1).astype(np.float64) * ks[..., None]).reshape(n, keys, -1)
+    v = (vq.reshape(*vs.shape, -1).astype(np.float64) * vs[..., None]).reshape(n, keys, -1)
+    qd = q.double().numpy().reshape(n, h * w, -1)
+    for i in range(n):
+        L = keys if counts is None else counts[i]
+        ref, ref_abs = oq.attention(qd[i], k[i], v[i], heads, L)
+        allow = bound(qd[i], k[i][:L], ref, ref_abs, heads, L) - ref_abs * (2.0 ** -8 - 2.0 ** -17)
+        assert (np.abs(o[i] - ref) <= allow).all()
+
+
+def test_two_graphs_share_a_workspace():
+    """The layer captured twice with one workspace and replayed on two streams at
+    once: each replay gives the eager call's bits."""
+    rng = np.random.default_rng(44)
+    n, h, w, C, heads, b = 1, 32, 32, 320, 8, 4
+    weights = [sige.sige_qcache_write(torch.from_numpy(rng.normal(0, C ** -0.5, size=(C, 1, 1, C)).astype(np.float32)).to(DEV),
+                                      sige.qcache_empty(C, 1, 1, C)) for _ in range(4)]
+    wq, wk, wv, wo = weights
+    ws = sige.zeros_workspace(256, DEV)
+    runs = []
+    for frac in (0.1, 0.5):
+        _, where = tile_list(rng, h, w, b, frac)
+        x = torch.from_numpy(rng.normal(size=(n, h, w, C))).to(torch.bfloat16).to(DEV)
+        kv = [random_cache(rng, n, h, w, C, C // heads, "s8")[0] for _ in range(2)]
+        y = torch.zeros_like(x)
+        call = lambda x=x, where=where, kv=kv, y=y: sige.sige_attention_sparse_q(
+            x, where["idx"], where["count"], where["capacity"], b, wq, wo, None, heads, *kv, y, wk=wk, wv=wv, workspace=ws)
+        call()
+        torch.cuda.synchronize()
+        want = y.clone()
+        graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph):
+            call()
+        runs.append((graph, stream, y, want, call))   # (the call keeps the graph's inputs alive)
+    for _ in range(20):
+        for graph, stream, y, _, _ in runs:
+            with torch.cuda.stream(stream):
+                y.zero_()
+                graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for _, _, y, want, _ in runs)
+    assert not ws.any()
