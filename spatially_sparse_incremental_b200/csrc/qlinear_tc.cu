@@ -252,26 +252,10 @@ __device__ __noinline__ void drain_products(uint32_t bar)
 struct Args {
     QLinearParams q;
     int vec;       // y and the residual take 32-byte accesses of 16 columns
+    int width;     // elements of y an access takes otherwise (put_rows)
     int tile_rows; // tokens that one box copies (a tile's; a whole map's of a unit), 0: four tokens a copy
     Plan plan;     // of a whole map (a list's is made on the device)
 };
-
-__device__ __forceinline__ float residual1(const QLinearParams &p, int64_t e)
-{
-    return p.dtype == SIGE_BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.residual)[e])
-                                : reinterpret_cast<const float *>(p.residual)[e];
-}
-
-// One output element.
-__device__ __forceinline__ void put1(const QLinearParams &p, int64_t e, float v)
-{
-    if (p.residual)
-        v += residual1(p, e);
-    if (p.dtype == SIGE_BF16)
-        reinterpret_cast<__nv_bfloat16 *>(p.y)[e] = __float2bfloat16_rn(v);
-    else
-        reinterpret_cast<float *>(p.y)[e] = v;
-}
 
 // 16 sums of one token, scaled and biased: scales and biases from shared
 // memory (col: kMaxBn scales, then kMaxBn biases).
@@ -383,17 +367,128 @@ __device__ __forceinline__ void put16(const QLinearParams &p, int64_t e, float *
     }
 }
 
-// 16 columns from c on of one token (pix): put16 where whole sectors allow it.
-__device__ __forceinline__ void put_cols(const Args &a, float *v, int64_t pix, int c)
+// 16 columns from c on of a warp's 32 rows, where a row's columns are no whole
+// sectors (or not all there): lane r leaves row r's values in shared memory (2 KB
+// of the warp, 16-byte pieces at piece ^ ((row / 2) mod 4)), then neighbouring
+// lanes take neighbouring columns, kW elements each.  A lane for each row's
+// columns stored 2 bytes of 32 different lines an instruction: 16384 x 640 ->
+// 5112 812 us.
+template <int kE, int kW>
+__device__ __noinline__ void put_rows_as(const QLinearParams &p, uint32_t tile, int pix, int col)
+{
+    constexpr int kLanes = 16 / kW;   // of a row
+    constexpr int kRowsAt = 32 / kLanes, kPass = 32 / kRowsAt, kGo = kPass < 8 ? kPass : 8;   // passes under way at once
+    const int lane = (int)(threadIdx.x & 31), c = col + (lane % kLanes) * kW;
+    const uint32_t k0 = (uint32_t)(c - col);
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += kGo * kRowsAt) {
+        float v[kGo][kW];
+        int64_t e[kGo];   // byte offset, -1: nothing to store
+#pragma unroll
+        for (int i = 0; i < kGo; ++i) {
+            const int row = r0 + i * kRowsAt + lane / kLanes, at = __shfl_sync(0xFFFFFFFFu, pix, row);
+            e[i] = at < 0 || c >= p.Co ? -1 : ((int64_t)at * p.Co + c) * kE;
+            const uint32_t src = tile + 64u * (uint32_t)row, sw = (uint32_t)(row >> 1) & 3u;
+            if constexpr (kW >= 4) {
+#pragma unroll
+                for (int k = 0; k < kW / 4; ++k) {
+                    const float4 x = lds_f32x4(src + (((k0 / 4 + k) ^ sw) << 4));
+                    v[i][4 * k] = x.x; v[i][4 * k + 1] = x.y; v[i][4 * k + 2] = x.z; v[i][4 * k + 3] = x.w;
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < kW; ++k)
+                    asm volatile("ld.shared.f32 %0, [%1];"
+                                 : "=f"(v[i][k]) : "r"(src + (((k0 / 4) ^ sw) << 4) + 4u * (k0 % 4 + k)) : "memory");
+            }
+        }
+        if (p.residual) {
+            uint4 w[kGo];
+#pragma unroll
+            for (int i = 0; i < kGo; ++i) {
+                w[i] = make_uint4(0, 0, 0, 0);
+                if (e[i] >= 0) {
+                    if constexpr (kE * kW == 16)
+                        w[i] = *reinterpret_cast<const uint4 *>(p.residual + e[i]);
+                    else if constexpr (kE * kW == 4)
+                        w[i].x = *reinterpret_cast<const uint32_t *>(p.residual + e[i]);
+                    else
+                        w[i].x = *reinterpret_cast<const uint16_t *>(p.residual + e[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kGo; ++i) {
+                const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                for (int k = 0; k < kW; ++k)
+                    v[i][k] += kE == 4 ? __uint_as_float(x[k & 3]) : k & 1 ? bf16_hi(x[k >> 1]) : bf16_lo(x[k >> 1]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kGo; ++i) {
+            if (e[i] < 0)
+                continue;
+            uint8_t *dst = p.y + e[i];
+            const float *u = v[i];
+            if constexpr (kE == 2 && kW == 8)
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]),
+                                                             pack_bf16x2(u[4], u[5]), pack_bf16x2(u[6], u[7]));
+            else if constexpr (kE == 4 && kW == 4)
+                *reinterpret_cast<float4 *>(dst) = make_float4(u[0], u[1], u[2], u[3]);
+            else if constexpr (kE == 2 && kW == 2)
+                *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(u[0], u[1]);
+            else if constexpr (kE == 2)
+                *reinterpret_cast<__nv_bfloat16 *>(dst) = __float2bfloat16_rn(u[0]);
+            else
+                *reinterpret_cast<float *>(dst) = u[0];
+        }
+    }
+    __syncwarp();
+}
+__device__ __noinline__ void put_rows(const Args &a, uint32_t tile, int pix, int col)
 {
     const QLinearParams &p = a.q;
-    if (a.vec && c + 16 <= p.Co) {
-        put16(p, pix * p.Co + c, v);
+    if (p.dtype == SIGE_BF16) {
+        if (a.width == 8)
+            put_rows_as<2, 8>(p, tile, pix, col);
+        else if (a.width == 2)
+            put_rows_as<2, 2>(p, tile, pix, col);
+        else
+            put_rows_as<2, 1>(p, tile, pix, col);
     } else {
+        if (a.width == 4)
+            put_rows_as<4, 4>(p, tile, pix, col);
+        else
+            put_rows_as<4, 1>(p, tile, pix, col);
+    }
+}
+// The widest access of put_rows: aligned at every row, and a divisor of the columns.
+inline int row_width(const QLinearParams &p)
+{
+    const int esz = p.dtype == SIGE_BF16 ? 2 : 4;
+    for (int w = 16 / esz; w > 1; w = w == 8 ? 2 : 1)
+        if (p.Co % w == 0 && aligned_to(p.y, (uintptr_t)(w * esz)) && aligned_to(p.residual, (uintptr_t)(w * esz)))
+            return w;
+    return 1;
+}
+
+// 16 columns from c on of the warp's tokens (pix: this lane's, -1: none): whole
+// sectors of a lane's own row, or put_rows.
+__device__ __forceinline__ void put_cols(const Args &a, float *v, int64_t pix, int c, uint32_t tile)
+{
+    if (a.vec && c + 16 <= a.q.Co) {
+        if (pix >= 0)
+            put16(a.q, pix * a.q.Co + c, v);
+    } else if (c < a.q.Co) {
+        const int lane = (int)(threadIdx.x & 31);
+        const uint32_t own = tile + 64u * (uint32_t)lane, sw = (uint32_t)(lane >> 1) & 3u;
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-            if (c + k < p.Co)
-                put1(p, pix * p.Co + c + k, v[k]);
+        for (int k = 0; k < 4; ++k)
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(own + (((uint32_t)k ^ sw) << 4)), "f"(v[4 * k]),
+                         "f"(v[4 * k + 1]), "f"(v[4 * k + 2]), "f"(v[4 * k + 3])
+                         : "memory");
+        __syncwarp();
+        put_rows(a, tile, (int)pix, c);
     }
 }
 
@@ -584,6 +679,9 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
         const int r = (warp & 3) * 32 + lane;              // row of the unit = tensor-memory lane
         const int half = (warp - 2) >> 2;
         const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        // put_rows' memory: that of the pushed sums or, where there are any, the
+        // ring's, idle once a split unit's products (its CTA's only ones) are done
+        const uint32_t tile = sb + (split_n > 1 ? 0u : kOffRecv) + 2048u * (uint32_t)(warp - 2);
         int nu = 0;
         bool ok = true;
         for (uint32_t u = u_first; u < plan.units; u += u_step, ++nu) {
@@ -656,8 +754,7 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                     for (int h = 0; h < 2; ++h) {
                         float v[16];
                         scale16(q + 16 * h, col + 4u * (uint32_t)(g + 16 * h), rs, v);
-                        if (pix >= 0)
-                            put_cols(args, v, pix, cb * plan.bn + g + 16 * h);
+                        put_cols(args, v, pix, cb * plan.bn + g + 16 * h, tile);
                     }
                 };
                 int g = 32 * half;
@@ -700,11 +797,9 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
                         acc[4 * q + 3] += v.w;
                     }
                 }
-                if (pix >= 0) {
-                    float v[16];
-                    scale16(acc, col + 4u * (uint32_t)(col0 + g), rs, v);
-                    put_cols(args, v, pix, cb * plan.bn + col0 + g);
-                }
+                float v[16];
+                scale16(acc, col + 4u * (uint32_t)(col0 + g), rs, v);
+                put_cols(args, v, pix, cb * plan.bn + col0 + g, tile);
             }
             tc_fence_before();
             __syncwarp();
@@ -1024,6 +1119,7 @@ int launch_qlinear_tc(const QLinearParams &p, cudaStream_t stream)
     a.q = p;
     const int esz = p.dtype == SIGE_BF16 ? 2 : 4;
     a.vec = (int64_t)p.Co * esz % 32 == 0 && aligned_to(p.y, 32) && aligned_to(p.residual, 32);
+    a.width = qt::row_width(p);
     // a whole map of enough units needs no cluster (every SM takes part); a
     // list's length is known on the device only
     const int sms = device_sm_count();

@@ -210,3 +210,24 @@ def test_binding_refusals_on_the_gpu():
     grouped = sige.QCache(A.codes, torch.ones((1, 4, 4, 2), device=DEV), "s8")
     with pytest.raises(sige.SigeError, match="unsupported"):
         sige.sige_qlinear(grouped, W)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("co", [1, 8, 15, 22, 40, 100, 333, 1000])
+@pytest.mark.parametrize("n,h,w,c", [(1, 9, 15, 64), (2, 31, 33, 336), (1, 1, 3, 5120)])
+def test_output_widths(n, h, w, c, co, dtype):
+    """Channels that are no whole sectors, at every access width, whole maps and
+    lists, with K split and without."""
+    run_case(c + co, n, h, w, c, co, dtype, residual=True)
+    rng = np.random.default_rng(c + co)
+    a, sa, wt, sw = operands(rng, n, h, w, c, co)
+    A, W = cache(a, sa), cache(wt, sw)
+    full = sige.sige_qlinear(A, W, dtype=dtype)
+    _, where = tile_list(rng, h, w, 4, 0.5)
+    y = torch.full_like(full, 3.0)
+    sige.sige_qlinear(A, W, None, y, **where)
+    idx = where["idx"][:int(where["count"])].tolist()
+    hit = torch.zeros((h, w), dtype=torch.bool, device=DEV)
+    for i, j in idx:
+        hit[i:i + 4, j:j + 4] = True
+    assert torch.equal(y[:, hit], full[:, hit]) and (y[:, ~hit] == 3).all()
