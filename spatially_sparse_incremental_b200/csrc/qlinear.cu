@@ -4,121 +4,8 @@
 // is the 1x1 layer F_l of the sparse engine (SIGE project page, "Overview") on
 // a quantised cache.
 //
-// This file holds the call and the kernel for shapes the tensor-core kernel
-// does not take (channels that are not a multiple of 16, unaligned buffers):
-// 64 tokens x 64 channels a CTA, operands staged 64 bytes of K at a time, four
-// products an instruction (dp4a), 4 x 4 outputs a thread.
-#include <algorithm>
-
+// This file holds the call and its checks; the kernels are in qlinear_tc.cu.
 #include "qlinear.cuh"
-
-namespace sige {
-namespace ql {
-
-constexpr int kThreads = 256;
-constexpr int kTile = 64;       // tokens, and channels, of a CTA's tile
-constexpr int kWords = 16;      // 32-bit words of K staged at a time
-
-// Four codes of a row from element k on, zero past the end.
-__device__ __forceinline__ int load4(const uint8_t *row, int k, int C, bool words)
-{
-    if (words && k + 4 <= C)
-        return *reinterpret_cast<const int *>(row + k);
-    uint32_t w = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (k + j < C)
-            w |= (uint32_t)row[k + j] << (8 * j);
-    return (int)w;
-}
-
-__global__ void __launch_bounds__(kThreads) k_qlinear_any(const __grid_constant__ QLinearParams p, int words)
-{
-    __shared__ int As[kWords][kTile + 1], Ws[kWords][kTile + 1];
-    __shared__ int64_t tok[kTile];
-    pdl_wait();
-    const int64_t slots = pixel_slots(p.px);
-    const int nb = (p.Co + kTile - 1) / kTile;
-    const int64_t units = (slots + kTile - 1) / kTile * nb;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-#pragma unroll 1
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t s0 = u / nb * kTile;
-        const int o0 = (int)(u % nb) * kTile;
-        __syncthreads();   // the previous unit has finished with tok
-        if (threadIdx.x < kTile)
-            tok[threadIdx.x] = s0 + threadIdx.x < slots ? pixel_of(p.px, (uint32_t)(s0 + threadIdx.x)) : -1;
-        int acc[4][4] = {};
-#pragma unroll 1
-        for (int k0 = 0; k0 < p.C; k0 += 4 * kWords) {
-            __syncthreads();
-#pragma unroll
-            for (int e = threadIdx.x; e < kTile * kWords; e += kThreads) {
-                const int r = e / kWords, j = e % kWords, k = k0 + 4 * j;
-                As[j][r] = tok[r] >= 0 && k < p.C ? load4(p.a + tok[r] * p.C, k, p.C, words) : 0;
-                Ws[j][r] = o0 + r < p.Co && k < p.C ? load4(p.w + (int64_t)(o0 + r) * p.C, k, p.C, words) : 0;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < kWords; ++j) {
-                int a[4], w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    a[i] = As[j][ty + 16 * i];
-                    w[i] = Ws[j][tx + 16 * i];
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int o = 0; o < 4; ++o)
-                        acc[i][o] = __dp4a(a[i], w[o], acc[i][o]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t t = tok[ty + 16 * i];
-            if (t < 0)
-                continue;
-            const float sa = __ldg(p.sa + t);
-#pragma unroll
-            for (int o = 0; o < 4; ++o) {
-                const int c = o0 + tx + 16 * o;
-                if (c >= p.Co)
-                    continue;
-                const int64_t e = t * p.Co + c;
-                float v = qlinear_value(acc[i][o], sa, __ldg(p.sw + c));
-                if (p.bias)
-                    v += __ldg(p.bias + c);
-                if (p.dtype == SIGE_BF16) {
-                    if (p.residual)
-                        v += __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.residual)[e]);
-                    reinterpret_cast<__nv_bfloat16 *>(p.y)[e] = __float2bfloat16_rn(v);
-                } else {
-                    if (p.residual)
-                        v += reinterpret_cast<const float *>(p.residual)[e];
-                    reinterpret_cast<float *>(p.y)[e] = v;
-                }
-            }
-        }
-    }
-}
-
-static int launch_any(const QLinearParams &p, cudaStream_t stream)
-{
-    prefer_max_shared(k_qlinear_any);
-    const int64_t units = (p.slots + kTile - 1) / kTile * ((p.Co + kTile - 1) / kTile);
-    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(units, (int64_t)device_sm_count() * 8));
-    const int words = p.C % 4 == 0 && aligned_to(p.a, 4) && aligned_to(p.w, 4);
-    if (launch_pdl(k_qlinear_any, dim3(grid), dim3(kThreads), 0, stream, p, words) != cudaSuccess) {
-        cudaGetLastError();
-        return SIGE_ERR_CUDA;
-    }
-    count_launch();
-    return launch_check();
-}
-
-} // namespace ql
-} // namespace sige
 
 using namespace sige;
 
@@ -175,8 +62,7 @@ extern "C" int sige_qlinear(const void *a_codes, const float *a_scales, const si
     p.dtype = yd->dtype;
     p.rows = rows;
     p.hdr = static_cast<WsHeader *>(workspace);
-    const int tc = launch_qlinear_tc(p, (cudaStream_t)stream);
-    return tc != 1 ? tc : ql::launch_any(p, (cudaStream_t)stream);
+    return launch_qlinear(p, (cudaStream_t)stream);
 }
 
-extern "C" int sige_qlinear_path(int32_t c) { return c > 0 && qlinear_tc_scope(c) ? 1 : 0; }
+extern "C" int sige_qlinear_path(int32_t c) { return c > 0 && qlinear_tma_scope(c) ? 1 : 0; }

@@ -26,9 +26,9 @@ struct QLinearParams {
 // float32's range where the value does not.
 __device__ __forceinline__ float qlinear_value(int acc, float sa, float sw) { return __int2float_rn(acc) * sa * sw; }
 
-// The tensor-core kernel: a sige_status, or 1 when the call is outside its
-// scope.
-int launch_qlinear_tc(const QLinearParams &p, cudaStream_t stream);
-bool qlinear_tc_scope(int c);
+// The kernels (qlinear_tc.cu): a sige_status.
+int launch_qlinear(const QLinearParams &p, cudaStream_t stream);
+// Channels whose operands TMA copies (from 16-byte aligned codes).
+bool qlinear_tma_scope(int c);
 
 } // namespace sige

@@ -1029,6 +1029,224 @@ __global__ void __launch_bounds__(qt::kThreads, 1)
     }
 }
 
+namespace qt {
+
+// k_qlinear_staged: 8 warps stage and finish, one issues.
+constexpr int kStagedThreads = kEpiThreads + 32;
+constexpr int kStagedStages = 4, kStagedBn = 128;
+constexpr uint32_t kStagedStage = (kRows + kStagedBn) * kChunk;
+constexpr uint32_t kOffStagedTile = kStagedStages * kStagedStage;            // put_rows' memory
+constexpr uint32_t kOffStagedCol = kOffStagedTile + kEpiWarps * 2048;        // per unit parity: scales and biases
+constexpr uint32_t kOffStagedBar = kOffStagedCol + 2 * 2 * kMaxBn * 4;
+constexpr uint32_t kStagedSmem = kOffStagedBar + 256 + 1024;
+constexpr int kSiteStagedEmpty = 311, kSiteStagedFull = 312, kSiteStagedAccEmpty = 313, kSiteStagedAccFull = 314;
+
+// The aligned words that hold bytes [0, n) (n at most 16) from an address on, and
+// the bytes shifted into place with zeros behind them.
+__device__ __forceinline__ void words_of(const uint8_t *at, int n, uint32_t (&w)[5])
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(at);
+    const uint32_t *p = reinterpret_cast<const uint32_t *>(a & ~(uintptr_t)3);
+    const int end = (int)(a & 3) + n;
+#pragma unroll
+    for (int k = 0; k < 5; ++k)
+        w[k] = n > 0 && 4 * k < end ? __ldg(p + k) : 0u;
+}
+__device__ __forceinline__ uint4 bytes_of(const uint32_t (&w)[5], uint32_t sh, int n)
+{
+    uint32_t r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int left = n - 4 * k;
+        r[k] = __funnelshift_r(w[k], w[k + 1], sh) & (left >= 4 ? 0xFFFFFFFFu : left > 0 ? (1u << (8 * left)) - 1u : 0u);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+} // namespace qt
+
+// The product for codes that TMA cannot copy (channels that are not a multiple of
+// 16, addresses that are not): the same units of 128 tokens x bn (128 .. 32)
+// channels, the stages filled by the CTA's threads from aligned words.  16 bytes
+// of K a thread and row, the next chunk's words on their way; bound by that
+// staging (about 110 instructions a thread and chunk of 128 x 128).  16384 x 300
+// -> 5120 810 us with four products an instruction on CUDA cores, FIGURE here.
+__global__ void __launch_bounds__(qt::kStagedThreads, 1) k_qlinear_staged(const __grid_constant__ qt::Args args)
+{
+    extern __shared__ __align__(1024) uint8_t qt_raw[];
+    const QLinearParams &p = args.q;
+    const uint32_t raw = smem_u32(qt_raw);
+    const uint32_t sb = (raw + 1023u) & ~1023u;
+    uint8_t *smem = qt_raw + (sb - raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t bar = sb + kOffStagedBar;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffStagedBar + kAbort);
+    WsHeader *hdr = p.hdr;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStagedStages; ++i) {
+            mbar_init(bar + kBarFull + 8u * i, kEpiWarps);
+            mbar_init(bar + kBarEmpty + 8u * i, 1);
+        }
+        mbar_init(bar + kBarAccFull, 1);
+        mbar_init(bar + kBarAccEmpty, kEpiWarps);
+        mbar_init(bar + kBarDrain, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kEpiWarps) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(bar + kTmemSlot),
+                     "r"(kStagedBn));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    pdl_wait();
+    const int64_t slots = pixel_slots(p.px);
+    const int64_t rblocks = (slots + kRows - 1) / kRows;
+    // the widest units that leave no CTA without one
+    int bn = kStagedBn;
+    while (bn > 32 && rblocks * ((p.Co + bn - 1) / bn) < (int64_t)gridDim.x)
+        bn >>= 1;
+    const int cblocks = (p.Co + bn - 1) / bn, nch = (p.C + kChunk - 1) / kChunk;
+    const int64_t units = rblocks * cblocks;
+    const int last_steps = (p.C - (nch - 1) * kChunk + 31) / 32;   // of the last chunk's 32-channel steps
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + kOffStagedBar + kTmemSlot);
+
+    if (warp == kEpiWarps) {
+        // ---- products
+        const uint32_t id = idesc_s8(bn);
+        const uint64_t ring = desc_sw128(sb);
+        int st = 0, nu = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x, ++nu) {
+            if (nu > 0 && !mbar_wait_w(bar + kBarAccEmpty, (nu - 1) & 1, abort_flag, hdr, kSiteStagedAccEmpty)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            for (int c = 0; c < nch; ++c) {
+                if (!mbar_wait_w(bar + kBarFull + 8u * st, ph, abort_flag, hdr, kSiteStagedFull)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t ad = ring + (uint64_t)((uint32_t)st * (kStagedStage >> 4));
+                mma_s8_commit_w(tmem, ad, ad + ((kRows * kChunk) >> 4), id, c > 0, c + 1 < nch ? 4 : last_steps,
+                                bar + kBarEmpty + 8u * st);
+                if (++st == kStagedStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+            if (ok)
+                tc_commit_w(bar + kBarAccFull);
+        }
+        if (!ok)
+            drain_products(bar);
+        __syncwarp();
+    } else {
+        // ---- staging, then outputs
+        const int et = (int)threadIdx.x, piece = et & 7, r0 = et >> 3;   // rows r0 + 32 i of tokens and of channels
+        const int r = (warp & 3) * 32 + lane, half = warp >> 2;
+        const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t tile = sb + kOffStagedTile + 2048u * (uint32_t)warp;
+        const uint32_t to = (uint32_t)r0 * kChunk + (((uint32_t)piece ^ ((uint32_t)r0 & 7u)) << 4);
+        constexpr int kPer = kRows / 32;
+        int it = 0, st = 0, nu = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++nu) {
+            const int64_t rb = u / cblocks;
+            const int c0 = (int)(u - rb * cblocks) * bn;
+            if (ok) {
+                const uint8_t *row[2 * kPer];   // tokens, channels; NULL: none
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const int64_t s = rb * kRows + r0 + 32 * i;
+                    const int64_t pix = s < slots ? pixel_of(p.px, (uint32_t)s) : -1;
+                    const int ch = c0 + r0 + 32 * i;
+                    row[i] = pix >= 0 ? p.a + pix * p.C + 16 * piece : nullptr;
+                    row[kPer + i] = 32 * i < bn && ch < p.Co ? p.w + (int64_t)ch * p.C + 16 * piece : nullptr;
+                }
+                uint32_t w[2 * kPer][5];
+                auto fetch = [&](int c) {
+                    const int n = max(0, min(16, p.C - c * kChunk - 16 * piece));
+#pragma unroll
+                    for (int i = 0; i < 2 * kPer; ++i)
+                        if (row[i])
+                            words_of(row[i] + (int64_t)c * kChunk, n, w[i]);
+                };
+                fetch(0);
+                for (int c = 0; c < nch; ++c, ++it) {
+                    if (it >= kStagedStages && !mbar_wait_w(bar + kBarEmpty + 8u * st, ph, abort_flag, hdr, kSiteStagedEmpty)) {
+                        ok = false;
+                        break;
+                    }
+                    const int n = max(0, min(16, p.C - c * kChunk - 16 * piece));
+                    const uint32_t dst = sb + (uint32_t)st * kStagedStage + to;
+                    // (rows without a token or a channel keep what they hold: it
+                    // enters only sums that are not written)
+#pragma unroll
+                    for (int i = 0; i < 2 * kPer; ++i) {
+                        if (row[i]) {
+                            const uint4 x = bytes_of(w[i], 8u * (uint32_t)(reinterpret_cast<uintptr_t>(row[i] + (int64_t)c * kChunk) & 3), n);
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 32u * (uint32_t)i * kChunk), "r"(x.x),
+                                         "r"(x.y), "r"(x.z), "r"(x.w)
+                                         : "memory");
+                        }
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar + kBarFull + 8u * st);
+                    if (c + 1 < nch)
+                        fetch(c + 1);
+                    if (++st == kStagedStages) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            const uint32_t col = sb + kOffStagedCol + (uint32_t)(nu & 1) * 2 * kMaxBn * 4;
+            float *colp = reinterpret_cast<float *>(smem + kOffStagedCol + (uint32_t)(nu & 1) * 2 * kMaxBn * 4);
+            if (et < bn) {
+                const int c = c0 + et;
+                colp[et] = c < p.Co ? __ldg(p.sw + c) : 0.0f;
+                colp[kMaxBn + et] = c < p.Co && p.bias ? __ldg(p.bias + c) : 0.0f;
+            }
+            const int64_t s = rb * kRows + r;
+            const int64_t pix = s < slots ? pixel_of(p.px, (uint32_t)s) : -1;
+            const float rs = pix >= 0 ? __ldg(p.sa + pix) : 0.0f;
+            epi_sync();   // (met by every warp, after an expired wait too)
+            if (ok)
+                ok = mbar_wait_w(bar + kBarAccFull, nu & 1, abort_flag, hdr, kSiteStagedAccFull);
+            if (!ok)
+                continue;
+            tc_fence_after();
+            for (int g = 16 * half; g < bn && c0 + g < p.Co; g += 32) {
+                int acc[16];
+                ld_cols(t_row + (uint32_t)g, acc);
+                ld_done();
+                float v[16];
+                scale16(acc, col + 4u * (uint32_t)g, rs, v);
+                put_cols(args, v, pix, c0 + g, tile);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar + kBarAccEmpty);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kEpiWarps) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kStagedBn));
+    }
+}
+
 // ------------------------------------------------------------------ host
 
 // 128-byte columns of a matrix of `rows` rows of C codes, box_rows rows a copy.
@@ -1069,14 +1287,43 @@ static bool encode_out(CUtensorMap *map, const QLinearParams &p, int esz, PFN_cu
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool qlinear_tc_scope(int c) { return c % 16 == 0; }
+bool qlinear_tma_scope(int c) { return c % 16 == 0; }
 
-int launch_qlinear_tc(const QLinearParams &p, cudaStream_t stream)
+static int launch_staged(const QLinearParams &p, cudaStream_t stream)
 {
-    // (units are counted in 32 bits)
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return SIGE_ERR_CUDA;
+    static std::atomic<int> smem_set[64];
+    if (!smem_set[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(k_qlinear_staged, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)qt::kStagedSmem) != cudaSuccess) {
+            cudaGetLastError();
+            return SIGE_ERR_CUDA;
+        }
+        smem_set[dev].store(1, std::memory_order_release);
+    }
+    prefer_max_shared_of<k_qlinear_staged>();
+    qt::Args a{};
+    a.q = p;
+    const int esz = p.dtype == SIGE_BF16 ? 2 : 4;
+    a.vec = (int64_t)p.Co * esz % 32 == 0 && aligned_to(p.y, 32) && aligned_to(p.residual, 32);
+    a.width = qt::row_width(p);
+    const int64_t most = (p.slots + qt::kRows - 1) / qt::kRows * ((p.Co + 31) / 32);
+    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, device_sm_count()));
+    if (launch_pdl(k_qlinear_staged, dim3(grid), dim3(qt::kStagedThreads), qt::kStagedSmem, stream, a) != cudaSuccess) {
+        cudaGetLastError();
+        return SIGE_ERR_CUDA;
+    }
+    count_launch();
+    return launch_check();
+}
+
+int launch_qlinear(const QLinearParams &p, cudaStream_t stream)
+{
+    // (the TMA kernels count units in 32 bits)
     const int64_t narrowest = ((p.slots + qt::kRows - 1) / qt::kRows) * (((int64_t)p.Co + 31) / 32);
-    if (!qlinear_tc_scope(p.C) || !aligned_to(p.a, 16) || !aligned_to(p.w, 16) || narrowest > INT32_MAX / 8)
-        return 1;
+    if (!qlinear_tma_scope(p.C) || !aligned_to(p.a, 16) || !aligned_to(p.w, 16) || narrowest > INT32_MAX / 8)
+        return launch_staged(p, stream);
     const PFN_cuTensorMapEncodeTiled_v12000 encode = get_encode();
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
