@@ -536,9 +536,9 @@ int sige_qcache_read(const void *codes, const float *scales, const sige_qcache_d
  *              any operand (the residual included)
  *   workspace: device, >= SIGE_WORKSPACE_HEADER_BYTES (the device error word),
  *              16-byte aligned, zero-filled before its first use
- * sige_qlinear_path says which kernel a call gets: tensor cores (c a multiple
- * of 16, codes 16-byte aligned) or CUDA cores.  A device-side wait
- * that expires records SIGE_ERR_TIMEOUT and leaves outputs unwritten.  Errors:
+ * The sums run on the tensor cores; sige_qlinear_path says how the codes reach
+ * them.  A device-side wait that expires records SIGE_ERR_TIMEOUT and leaves
+ * outputs unwritten.  Errors:
  * SIGE_ERR_INVALID_ARG, SIGE_ERR_UNSUPPORTED (format, group, dtype, layout,
  * c > 131071, block > 64, more than 2^31 - 1 pixels or listed slots),
  * SIGE_ERR_WORKSPACE, SIGE_ERR_CUDA. */
@@ -547,8 +547,9 @@ int sige_qlinear(const void *a_codes, const float *a_scales, const sige_qcache_d
                  const int32_t *idx, const int32_t *count, int32_t capacity, const void *residual, void *y,
                  const sige_tensor_desc *yd, void *workspace, size_t workspace_bytes, sige_stream_t stream);
 
-/* Which kernel sige_qlinear runs for c input channels (16-byte aligned codes):
- * 1 = tcgen05 tensor cores, 0 = CUDA cores.  Host only. */
+/* How sige_qlinear's codes reach the tensor cores for c input channels: 1 = by
+ * TMA (c a multiple of 16, 16-byte aligned codes), 0 = staged by threads, which
+ * is slower (any c, and unaligned codes).  Host only. */
 int sige_qlinear_path(int32_t c);
 
 /* (11) The attention step of (8) over quantised key and value caches: for
@@ -571,10 +572,11 @@ int sige_qlinear_path(int32_t c);
  * cores the weights exp(s - max), times the value's scale, are rounded to bf16
  * before the second product (as in (8)), against a running maximum that may lag
  * by up to 2^40: values (code * scale) have to stay below 2^60.  Errors:
- * SIGE_ERR_INVALID_ARG (NULL, sizes that differ, D or Dv not a multiple of heads, overlap, misaligned
- * list), SIGE_ERR_UNSUPPORTED (q not bf16 NHWC, head width > 256, group not a
- * multiple of the head width, block > 64, sizes past 32 bits),
- * SIGE_ERR_WORKSPACE, SIGE_ERR_CUDA. */
+ * SIGE_ERR_INVALID_ARG (NULL, sizes that differ, D or Dv not a multiple of
+ * heads, overlap, misaligned list), SIGE_ERR_UNSUPPORTED (q not bf16 NHWC, head
+ * width > 256, group not a multiple of the head width, block > 64, sizes past
+ * 32 bits), SIGE_ERR_WORKSPACE, SIGE_ERR_CUDA.  Items of at most 32 keys keep
+ * their weights in two bf16 terms. */
 int sige_attention_qcache(const void *q, const sige_tensor_desc *qd, const void *k_codes, const float *k_scales,
                           const sige_qcache_desc *kd, const void *v_codes, const float *v_scales,
                           const sige_qcache_desc *vd, const int32_t *key_counts, int32_t heads, int32_t block,

@@ -1037,40 +1037,23 @@ constexpr int kStagedStages = 4, kStagedBn = 128;
 constexpr uint32_t kStagedStage = (kRows + kStagedBn) * kChunk;
 constexpr uint32_t kOffStagedTile = kStagedStages * kStagedStage;            // put_rows' memory
 constexpr uint32_t kOffStagedCol = kOffStagedTile + kEpiWarps * 2048;        // per unit parity: scales and biases
-constexpr uint32_t kOffStagedBar = kOffStagedCol + 2 * 2 * kMaxBn * 4;
+constexpr uint32_t kOffStagedRow = kOffStagedCol + 2 * 2 * kMaxBn * 4;       // the unit's rows of tokens and channels
+constexpr uint32_t kOffStagedBar = kOffStagedRow + (kRows + kStagedBn) * 8;
 constexpr uint32_t kStagedSmem = kOffStagedBar + 256 + 1024;
 constexpr int kSiteStagedEmpty = 311, kSiteStagedFull = 312, kSiteStagedAccEmpty = 313, kSiteStagedAccFull = 314;
-
-// The aligned words that hold bytes [0, n) (n at most 16) from an address on, and
-// the bytes shifted into place with zeros behind them.
-__device__ __forceinline__ void words_of(const uint8_t *at, int n, uint32_t (&w)[5])
-{
-    const uintptr_t a = reinterpret_cast<uintptr_t>(at);
-    const uint32_t *p = reinterpret_cast<const uint32_t *>(a & ~(uintptr_t)3);
-    const int end = (int)(a & 3) + n;
-#pragma unroll
-    for (int k = 0; k < 5; ++k)
-        w[k] = n > 0 && 4 * k < end ? __ldg(p + k) : 0u;
-}
-__device__ __forceinline__ uint4 bytes_of(const uint32_t (&w)[5], uint32_t sh, int n)
-{
-    uint32_t r[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int left = n - 4 * k;
-        r[k] = __funnelshift_r(w[k], w[k + 1], sh) & (left >= 4 ? 0xFFFFFFFFu : left > 0 ? (1u << (8 * left)) - 1u : 0u);
-    }
-    return make_uint4(r[0], r[1], r[2], r[3]);
-}
 
 } // namespace qt
 
 // The product for codes that TMA cannot copy (channels that are not a multiple of
 // 16, addresses that are not): the same units of 128 tokens x bn (128 .. 32)
-// channels, the stages filled by the CTA's threads from aligned words.  16 bytes
-// of K a thread and row, the next chunk's words on their way; bound by that
-// staging (about 110 instructions a thread and chunk of 128 x 128).  16384 x 300
-// -> 5120 810 us with four products an instruction on CUDA cores, FIGURE here.
+// channels, the stages filled by the CTA's warps: lane l takes aligned word l of
+// a row's 128 bytes of K (32 rows a warp and chunk, the next chunk's on their
+// way), shifts its neighbour's bytes in and leaves 4 bytes; a row's last word's
+// neighbour comes from the lane that is the row's number.  Bound by that staging,
+// about 3200 cycles a chunk of 128 x 128.  16384 x 300 -> 5120 810 us with four
+// products an instruction on CUDA cores, 332 us with 16 bytes of a row a lane
+// (every word fetched from L2 again and again), 230 us here; 16384 x 1280 -> 320
+// 51 us, 9.2 by TMA.
 __global__ void __launch_bounds__(qt::kStagedThreads, 1) k_qlinear_staged(const __grid_constant__ qt::Args args)
 {
     extern __shared__ __align__(1024) uint8_t qt_raw[];
@@ -1148,61 +1131,84 @@ __global__ void __launch_bounds__(qt::kStagedThreads, 1) k_qlinear_staged(const 
         __syncwarp();
     } else {
         // ---- staging, then outputs
-        const int et = (int)threadIdx.x, piece = et & 7, r0 = et >> 3;   // rows r0 + 32 i of tokens and of channels
+        const int et = (int)threadIdx.x;
         const int r = (warp & 3) * 32 + lane, half = warp >> 2;
         const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t tile = sb + kOffStagedTile + 2048u * (uint32_t)warp;
-        const uint32_t to = (uint32_t)r0 * kChunk + (((uint32_t)piece ^ ((uint32_t)r0 & 7u)) << 4);
-        constexpr int kPer = kRows / 32;
+        // a warp's rows: every 8th token, then every 8th channel
+        const int mine = 16 + bn / kEpiWarps;
+        unsigned long long *rowp = reinterpret_cast<unsigned long long *>(smem + kOffStagedRow);
         int it = 0, st = 0, nu = 0;
         uint32_t ph = 1;
         bool ok = true;
         for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++nu) {
             const int64_t rb = u / cblocks;
             const int c0 = (int)(u - rb * cblocks) * bn;
+            // (every warp has staged the last unit: it has met the others since)
+            if (et < kRows) {
+                const int64_t s = rb * kRows + et;
+                const int64_t pix = s < slots ? pixel_of(p.px, (uint32_t)s) : -1;
+                rowp[et] = pix >= 0 ? reinterpret_cast<unsigned long long>(p.a + pix * p.C) : 0ull;
+            } else {
+                const int ch = c0 + et - kRows;
+                rowp[et] = et - kRows < bn && ch < p.Co ? reinterpret_cast<unsigned long long>(p.w + (int64_t)ch * p.C) : 0ull;
+            }
+            epi_sync();
             if (ok) {
-                const uint8_t *row[2 * kPer];   // tokens, channels; NULL: none
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const int64_t s = rb * kRows + r0 + 32 * i;
-                    const int64_t pix = s < slots ? pixel_of(p.px, (uint32_t)s) : -1;
-                    const int ch = c0 + r0 + 32 * i;
-                    row[i] = pix >= 0 ? p.a + pix * p.C + 16 * piece : nullptr;
-                    row[kPer + i] = 32 * i < bn && ch < p.Co ? p.w + (int64_t)ch * p.C + 16 * piece : nullptr;
-                }
-                uint32_t w[2 * kPer][5];
+                // row i of the warp: its place in the table and in a stage
+                auto place_of = [&](int i) { return warp + 8 * i; };
+                const unsigned long long own = lane < mine ? rowp[place_of(lane)] : 0ull;
+                // bits of every row's offset in a word (the same for every chunk)
+                const uint32_t low = __ballot_sync(0xFFFFFFFFu, own & 1), high = __ballot_sync(0xFFFFFFFFu, own & 2);
+                uint32_t w[32], w33 = 0;
                 auto fetch = [&](int c) {
-                    const int n = max(0, min(16, p.C - c * kChunk - 16 * piece));
+                    const int n = min(kChunk, p.C - c * kChunk);   // bytes of a row
+                    if (own) {
+                        const unsigned long long a = own + (unsigned)(c * kChunk);
+                        w33 = (int)(a & 3) + n > kChunk ? __ldg(reinterpret_cast<const uint32_t *>(a & ~3ull) + 32) : 0u;
+                    }
 #pragma unroll
-                    for (int i = 0; i < 2 * kPer; ++i)
-                        if (row[i])
-                            words_of(row[i] + (int64_t)c * kChunk, n, w[i]);
+                    for (int i = 0; i < 32; ++i) {
+                        if (i < mine) {
+                            const unsigned long long row = rowp[place_of(i)], a = row + (unsigned)(c * kChunk);
+                            w[i] = 0;
+                            if (row && 4 * lane < (int)(a & 3) + n)
+                                w[i] = __ldg(reinterpret_cast<const uint32_t *>(a & ~3ull) + lane);
+                        }
+                    }
                 };
                 fetch(0);
                 for (int c = 0; c < nch; ++c, ++it) {
+                    // (rows without a token or a channel are zeros: leaving them out by a
+                    // branch takes the rows out of step, 300 -> 420 us when it was tried)
+                    const int left = p.C - c * kChunk - 4 * lane;   // bytes of this lane's word
+                    const uint32_t mask = left >= 4 ? 0xFFFFFFFFu : left > 0 ? (1u << (8 * left)) - 1u : 0u;
+                    uint32_t x[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        if (i < mine) {
+                            const uint32_t sh = ((low >> i) & 1u) * 8u + ((high >> i) & 1u) * 16u;
+                            const uint32_t up = __shfl_down_sync(0xFFFFFFFFu, w[i], 1), end = __shfl_sync(0xFFFFFFFFu, w33, i);
+                            x[i] = __funnelshift_r(w[i], lane == 31 ? end : up, sh) & mask;
+                        }
+                    }
+                    if (c + 1 < nch)
+                        fetch(c + 1);
                     if (it >= kStagedStages && !mbar_wait_w(bar + kBarEmpty + 8u * st, ph, abort_flag, hdr, kSiteStagedEmpty)) {
                         ok = false;
                         break;
                     }
-                    const int n = max(0, min(16, p.C - c * kChunk - 16 * piece));
-                    const uint32_t dst = sb + (uint32_t)st * kStagedStage + to;
-                    // (rows without a token or a channel keep what they hold: it
-                    // enters only sums that are not written)
+                    // (row & 7 is the warp's number)
+                    const uint32_t dst = sb + (uint32_t)st * kStagedStage + 4u * (uint32_t)(lane & 3) +
+                                         (((uint32_t)(lane >> 2) ^ (uint32_t)warp) << 4);
 #pragma unroll
-                    for (int i = 0; i < 2 * kPer; ++i) {
-                        if (row[i]) {
-                            const uint4 x = bytes_of(w[i], 8u * (uint32_t)(reinterpret_cast<uintptr_t>(row[i] + (int64_t)c * kChunk) & 3), n);
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 32u * (uint32_t)i * kChunk), "r"(x.x),
-                                         "r"(x.y), "r"(x.z), "r"(x.w)
-                                         : "memory");
-                        }
-                    }
+                    for (int i = 0; i < 32; ++i)
+                        if (i < mine)
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + (uint32_t)place_of(i) * kChunk), "r"(x[i]) : "memory");
                     fence_async_smem();
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(bar + kBarFull + 8u * st);
-                    if (c + 1 < nch)
-                        fetch(c + 1);
                     if (++st == kStagedStages) {
                         st = 0;
                         ph ^= 1;
