@@ -504,8 +504,8 @@ size_t sige_qcache_scales(const sige_qcache_desc *cd);
  *   x      : device NHWC f32 or bf16 (xd), the cache's n, h, w, c
  *   codes, scales : device, not overlapping x or each other
  * A weight matrix [c_out][c_in] is written as a map of n = c_out, h = w = 1.
- * Any c, group and alignment; 16-byte aligned maps with groups that are
- * multiples of 8 (up to 2048) take the vector form.  Errors:
+ * Any c, group and alignment; 8, 4 or 2 elements move at once as the group
+ * and the addresses allow (groups up to 256 times that).  Errors:
  * SIGE_ERR_INVALID_ARG (NULL, sizes that differ, group not dividing c, bad
  * format, overlap, misaligned list, x not aligned to its element or scales to
  * 4 bytes), SIGE_ERR_UNSUPPORTED (dtype, layout, odd S4 group, block > 64, more than

@@ -315,3 +315,18 @@ def test_more_groups_than_32_bits_count():
     assert torch.equal(cache.codes[:, -2:, -2:], ref.codes) and torch.equal(cache.scales[:, -2:, -2:], ref.scales)
     sige.sige_qcache_read(cache, x, **where)
     assert torch.equal(x[:, -2:, -2:], sige.sige_qcache_read(ref))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("group", [2, 4, 6, 10, 12, 20, 44, 90, 100, 250, 510, 516, 1020, 1028])
+def test_narrow_accesses(group, dtype, fmt):
+    """Groups that four, two or no elements at once divide: written and read,
+    whole and at tiles."""
+    rng = np.random.default_rng(group)
+    x = random_map(rng, 2, 7, 6, 3 * group, dtype)
+    cache = check_write(x, group, fmt)
+    idx, where = tile_list(rng, 7, 6, 2)
+    check_write(x, group, fmt, idx, where, 2)
+    values = torch.from_numpy(oq.values(*oq.quantise(x.float().numpy(), group, fmt)).astype(np.float32)).to(dtype)
+    assert torch.equal(sige.sige_qcache_read(cache, dtype=dtype).cpu(), values.view(x.shape))
