@@ -540,7 +540,8 @@ int sige_qcache_read(const void *codes, const float *scales, const sige_qcache_d
  * them.  A device-side wait that expires records SIGE_ERR_TIMEOUT and leaves
  * outputs unwritten.  Errors:
  * SIGE_ERR_INVALID_ARG, SIGE_ERR_UNSUPPORTED (format, group, dtype, layout,
- * c > 131071, block > 64, more than 2^31 - 1 pixels or listed slots),
+ * c > 131071, c_out > 2^31 - 1025, block > 64, more than 2^31 - 1 pixels or
+ * listed slots),
  * SIGE_ERR_WORKSPACE, SIGE_ERR_CUDA. */
 int sige_qlinear(const void *a_codes, const float *a_scales, const sige_qcache_desc *ad, const void *w_codes,
                  const float *w_scales, const sige_qcache_desc *wd, const float *bias, int32_t block,

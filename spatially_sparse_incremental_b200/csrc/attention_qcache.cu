@@ -197,7 +197,9 @@ static int check(const sige_tensor_desc *qd, const sige_qcache_desc *kd, const s
     if (qd->dtype != SIGE_BF16 || qd->layout != SIGE_NHWC || dh > kMaxHead || dvh > kMaxHead || kd->group % dh ||
         vd->group % dvh)
         return SIGE_ERR_UNSUPPORTED;
-    if ((int64_t)qd->n * qd->h > INT32_MAX || (int64_t)qd->n * qd->h * qd->w > INT32_MAX)
+    // (keys are counted in 32 bits, up to a chunk past the last)
+    if ((int64_t)qd->n * qd->h > INT32_MAX || (int64_t)qd->n * qd->h * qd->w > INT32_MAX ||
+        (int64_t)kd->h * kd->w > INT32_MAX - 1024)
         return SIGE_ERR_UNSUPPORTED;
     return SIGE_OK;
 }
@@ -238,8 +240,8 @@ extern "C" int sige_attention_qcache(const void *q, const sige_tensor_desc *qd, 
     if (p.slots == 0)
         return SIGE_OK;
     p.slots /= qd->n;
-    // the device indexes a unit's slots, keys, items and heads in 32 bits
-    if (p.slots > INT32_MAX - 1024 || (int64_t)kd->h * kd->w > INT32_MAX - 1024 || (int64_t)qd->n * heads > INT32_MAX)
+    // the device indexes a unit's slots, items and heads in 32 bits
+    if (p.slots > INT32_MAX - 1024 || (int64_t)qd->n * heads > INT32_MAX)
         return SIGE_ERR_UNSUPPORTED;
     p.q = static_cast<const __nv_bfloat16 *>(q);
     p.o = static_cast<__nv_bfloat16 *>(o);

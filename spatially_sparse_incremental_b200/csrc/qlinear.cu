@@ -30,7 +30,8 @@ extern "C" int sige_qlinear(const void *a_codes, const float *a_scales, const si
     if ((yd->dtype != SIGE_BF16 && yd->dtype != SIGE_F32) || yd->layout != SIGE_NHWC)
         return SIGE_ERR_UNSUPPORTED;
     // a sum of 131071 products of magnitude 2^14 (codes of -128 included) stays in 32 bits
-    if (ad->c > 131071)
+    // (and channels are counted in 32 bits, up to a tile past the last)
+    if (ad->c > 131071 || wd->n > INT32_MAX - 1024)
         return SIGE_ERR_UNSUPPORTED;
     const int esz = yd->dtype == SIGE_BF16 ? 2 : 4;
     if (!aligned_to(a_scales, 4) || !aligned_to(w_scales, 4) || !aligned_to(bias, 4) || !aligned_to(y, esz) ||

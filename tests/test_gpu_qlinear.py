@@ -231,3 +231,29 @@ def test_output_widths(n, h, w, c, co, dtype):
     for i, j in idx:
         hit[i:i + 4, j:j + 4] = True
     assert torch.equal(y[:, hit], full[:, hit]) and (y[:, ~hit] == 3).all()
+
+
+@pytest.mark.parametrize("n,h,w,c,co", [(1, 3, 5, 5121, 40), (1, 20, 20, 1025, 130), (2, 33, 31, 127, 300), (1, 12, 11, 129, 64),
+                                        (1, 64, 64, 100, 1000), (1, 2, 2, 8190, 9)])
+def test_channels_staged_by_threads(n, h, w, c, co):
+    """Channels that are not a multiple of 16: last chunks of one byte, of all but
+    one, more chunks than stages, more units than CTAs."""
+    run_case(c, n, h, w, c, co, torch.bfloat16, residual=True)
+
+
+@pytest.mark.parametrize("c", [64, 257, 1282])
+@pytest.mark.parametrize("ao,wo", [(1, 2), (3, 0), (4, 7), (0, 13)])
+def test_codes_at_any_byte(c, ao, wo):
+    rng = np.random.default_rng(c + ao)
+    n, h, w, co = 1, 5, 7, 70
+    a, sa, wt, sw = operands(rng, n, h, w, c, co)
+    def at(x, off):
+        buf = torch.full((x.size + off + 16,), 77, dtype=torch.int8, device=DEV)
+        v = buf[off:off + x.size].view(x.shape)
+        v.copy_(torch.from_numpy(x))
+        return v
+    A = sige.QCache(at(a, ao), torch.from_numpy(sa).to(DEV), "s8")
+    W = sige.QCache(at(wt, wo), torch.from_numpy(sw).to(DEV), "s8")
+    y = sige.sige_qlinear(A, W, dtype=torch.float32)
+    torch.cuda.synchronize()
+    check(y, a, sa, wt, sw, None, None, torch.float32)

@@ -148,3 +148,16 @@ def test_binding_refusals():
         sige.sige_qlinear(c, c, bias=torch.zeros(3))
     with pytest.raises(ValueError):
         sige.sige_attention_qcache(x, c, c, 2, key_counts=torch.zeros(2, dtype=torch.int32))
+
+
+def test_counts_near_the_end_of_32_bits(L):
+    """Channels or keys so many that a tile past the last would leave 32 bits are
+    refused, whatever the addresses."""
+    most = 2 ** 31 - 1
+    r = ctypes.byref
+    a, w, y = _qd(n=1, h=1, w=1, c=16, group=16), _qd(n=most, h=1, w=1, c=16, group=16), _td(n=1, h=1, w=1, c=most)
+    assert L.sige_qlinear(CODES, SCALES, r(a), W, SW, r(w), None, 1, None, None, 0, None, OUT, r(y), WS, 256,
+                          None) == sige.ERR_UNSUPPORTED
+    q, k = _td(n=1, h=1, w=1, c=16), _qd(n=1, h=most, w=1, c=16, group=16)
+    assert L.sige_attention_qcache(X, r(q), CODES, SCALES, r(k), W, SW, r(k), None, 1, 1, None, None, 0, OUT, WS, 256,
+                                   None) == sige.ERR_UNSUPPORTED
