@@ -571,8 +571,9 @@ int sige_qlinear_path(int32_t c);
  *   workspace : as (10)
  * sige_attention_qcache_path says which kernel a call gets.  On the tensor
  * cores the weights exp(s - max), times the value's scale, are rounded to bf16
- * before the second product (as in (8)), against a running maximum that may lag
- * by up to 2^40: values (code * scale) have to stay below 2^60.  Errors:
+ * before the second product (as in (8)).  Values of any finite magnitude give
+ * finite results; the sums q . key codes (before the key's scale) have to stay
+ * below 2^128.  Errors:
  * SIGE_ERR_INVALID_ARG (NULL, sizes that differ, D or Dv not a multiple of
  * heads, overlap, misaligned list), SIGE_ERR_UNSUPPORTED (q not bf16 NHWC, head
  * width > 256, group not a multiple of the head width, block > 64, sizes past

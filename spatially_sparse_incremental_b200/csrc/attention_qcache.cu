@@ -97,13 +97,16 @@ __global__ void __launch_bounds__(kThreads) k_attention_qcache(const __grid_cons
                 Ks[j * dhp + d] = j < nk ? code_at(p.kc, row * p.D + head * dh + d, p.kfmt) * __ldg(p.ks + row * p.kng + kg)
                                          : 0.0f;
             }
+            int big = 0;   // (kBigScale)
 #pragma unroll 1
             for (int e = threadIdx.x; e < kKeys * dvh; e += kThreads) {
                 const int j = e / dvh, d = e - j * dvh;
                 const int64_t row = kbase + k0 + j;
-                Vs[e] = j < nk ? code_at(p.vc, row * p.Dv + head * dvh + d, p.vfmt) * __ldg(p.vs + row * p.vng + vg) : 0.0f;
+                const float s = j < nk ? __ldg(p.vs + row * p.vng + vg) : 0.0f;
+                Vs[e] = j < nk ? code_at(p.vc, row * p.Dv + head * dvh + d, p.vfmt) * s : 0.0f;
+                big |= fabsf(s) >= kBigScale;
             }
-            __syncthreads();
+            const float room = __syncthreads_or(big) ? kRoom * 0.6931472f : 0.0f;
 #pragma unroll
             for (int s = 0; s < kPerWarp; ++s) {
                 const int qi = warp + kWarps * s;
@@ -115,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) k_attention_qcache(const __grid_cons
                 for (int d = 0; d < dh; ++d)
                     sc = fmaf(qr[d], kr[d], sc);
                 sc = lane < nk ? sc * p.scale : -INFINITY;
-                const float mn = fmaxf(m[s], wmax(sc));
+                const float mn = fmaxf(m[s], wmax(sc) + room);
                 const float pj = lane < nk ? expf(sc - mn) : 0.0f;
                 const float corr = expf(m[s] - mn);   // 0 on the first chunk (m = -inf)
                 l[s] = l[s] * corr + wsum(pj);

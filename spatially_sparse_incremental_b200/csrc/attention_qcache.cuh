@@ -6,6 +6,17 @@
 
 namespace sige {
 
+// Sums of weighted values are kept before they are divided by the sum of the
+// weights, so they are larger than the result: by the weights' sum (up to the
+// number of keys) and by how far a weight's exponent base lies below the row's
+// maximum.  Value scales below kBigScale leave room for both: 2^49 (448 times the
+// scale) x 2^40 (the tensor-core kernel's base) x 2^31 keys < 2^128.  A chunk of
+// keys with a larger one has its base 2^kRoom above the maximum, so that weights
+// are at most 2^-kRoom and any finite value summed over any number of keys stays
+// finite.
+constexpr float kBigScale = 1099511627776.0f;   // 2^40
+constexpr float kRoom = 32.0f;
+
 struct AttnQParams {
     const __nv_bfloat16 *q;      // [N][H][W][D]
     __nv_bfloat16 *o;            // [N][H][W][Dv]

@@ -66,7 +66,7 @@ constexpr int kCluster = 4;
 // The second terms lie where the weights of the next kShort keys would, and meet
 // the same values.
 constexpr int kShort = 32;
-constexpr float kSlack = 40.0f;     // how far (base 2) a score may lie above the exponent base
+constexpr float kSlack = 40.0f;     // how far (base 2) a score may lie above the exponent base (kBigScale)
 
 // Shared and tensor memory for heads of up to KD (64, 128 or 192) channels.
 template <int KD>
@@ -92,6 +92,7 @@ struct Lay {
     // rows pushed by the CTAs of a split unit, over the queries and the ring
     // (both idle by then): kSoft rows of KD floats
     static constexpr uint32_t kOffPush = 0;
+    static_assert(232 + 8 * kStages <= 256, "flags behind the barriers (kBig)");
     static_assert(kOffPush + kSoft * KD * 4 <= kOffSc, "pushed rows");
     static_assert(kOffK % 1024 == 0, "swizzled rows");
     static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -121,6 +122,7 @@ constexpr uint32_t kBarPush = 200;      // the rows this CTA owns have been push
 constexpr uint32_t kBarDrain = 208;     // + 8 for the P V warp
 constexpr uint32_t kTmemSlot = 224;
 constexpr uint32_t kAbort = 228;
+constexpr uint32_t kBig = 232;          // + 8 stage, a byte of each staging warp: value scales of kBigScale in the chunk
 constexpr uint32_t kTmemCols = 512;
 
 // wait sites (the detail of a recorded SIGE_ERR_TIMEOUT)
@@ -524,6 +526,8 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
         mbar_init(bar + kBarDrain, 1);
         mbar_init(bar + kBarDrain + 8u, 1);
         *abort_flag = 0;
+        for (int i = 0; i < L::kStages; ++i)
+            *reinterpret_cast<volatile uint64_t *>(smem + L::kOffBar + kBig + 8u * i) = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     tc_fence_before();
@@ -613,10 +617,17 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
                     const uint32_t kb = sb + L::kOffK + (uint32_t)st * L::kKvStage;
                     K.store(kb);
                     V.store(kb + L::kAtoms * L::kKvAtom);
+                    bool big = false;
 #pragma unroll
-                    for (int e = 0; e < kSc; ++e)
+                    for (int e = 0; e < kSc; ++e) {
                         if (t + e * kStage < 2 * kKeys)
                             sts_f1(sb + L::kOffSc + (uint32_t)st * L::kScStage + (uint32_t)(t + e * kStage) * 4u, sr[e]);
+                        big = big || (t + e * kStage >= kKeys && fabsf(sr[e]) >= kBigScale);
+                    }
+                    big = __any_sync(0xFFFFFFFFu, big);
+                    if (lane == 0)
+                        asm volatile("st.shared.u8 [%0], %1;" ::"r"(bar + kBig + 8u * st + (uint32_t)(t >> 5)), "r"((uint32_t)big)
+                                     : "memory");
                     fence_async_smem();
                     mbar_arrive(bar + kBarKvFull + 8u * st);
                     if (i + 1 < n)
@@ -754,6 +765,8 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
                 }
                 tc_fence_after();
                 const uint32_t sc = sb + L::kOffSc + (uint32_t)(ci % L::kStages) * L::kScStage;
+                // (kBigScale; read where it is needed: a register is dear)
+                auto big = [&]() { return lds_2(bar + kBig + 8u * (uint32_t)(ci % L::kStages)) != 0; };
                 const uint32_t t_s = t_row + L::tmem_s(g, b), t_p = t_row + L::tmem_p(g, b);
                 // The scores are read in the fragment layout: a thread has a quarter
                 // of the keys for four rows, so it reads a quarter of the scales,
@@ -868,8 +881,9 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
                     tc_fence_after();
                 }
                 // A first job has no base yet, and where P lies over the scores they
-                // cannot be read again: the maximum first.
-                bool move = i < kG || !L::kApart;
+                // cannot be read again: the maximum first.  With large values the base
+                // has to lie kRoom above it.
+                bool move = i < kG || !L::kApart || big();
                 if (move) {
                     pass(std::true_type());
 #pragma unroll
@@ -881,11 +895,14 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
                     if (move) {
                         float corr[4];
                         bool grow = false;
+                        const bool wide = big();
+                        const float room = wide ? kRoom : 0.0f;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             // (a first job: from -inf to its maximum; a row whose
                             // scores are all -inf or NaN keeps a base of -inf)
-                            const bool up = i < kG || top[j] > (L::kApart ? 0.0f : 8.0f);
+                            const bool up = i < kG || top[j] > (wide ? -kRoom : L::kApart ? 0.0f : 8.0f);
+                            top[j] += room;
                             corr[j] = up && i >= kG ? ex2(-top[j]) : 1.0f;
                             if (up) {
                                 mq[j] = i < kG ? top[j] : mq[j] + top[j];

@@ -362,3 +362,32 @@ def test_two_graphs_share_a_workspace():
     torch.cuda.synchronize()
     assert all(torch.equal(y, want) for _, _, y, want, _ in runs)
     assert not ws.any()
+
+
+@pytest.mark.parametrize("fmt", ["s8", "e4m3"])
+@pytest.mark.parametrize("dh", [40, 80, 160, 30, 200])
+def test_large_values(dh, fmt):
+    """Finite values give finite results, however large: at even weights (a sum of
+    as many weights as there are keys), where the scores rise along the keys (an
+    exponent base of the first ones lies 2^35 below the maximum), where only some
+    keys' values are large, and for the few keys of a short item."""
+    rng = np.random.default_rng(dh)
+    u = rng.normal(size=dh)
+    u /= np.linalg.norm(u)
+    # (ends of the scores, in base 2: 0 and `rise`, whatever the width)
+    for keys, rise, top, mixed in ((1200, 0, 2.0 ** 123, False), (1200, 35, 2.0 ** 100, False), (1200, 35, 2.0 ** 90, True),
+                                   (1200, -35, 2.0 ** 100, True), (20, 3, 2.0 ** 125, False)):
+        q = torch.from_numpy(u + 0.01 * rng.normal(size=(1, 4, 5, dh))).to(torch.bfloat16)
+        kv = (np.linspace(0, rise * np.log(2) * np.sqrt(dh), keys)[:, None] * u + 0.01 * rng.normal(size=(keys, dh)))
+        kq, ks = oq.quantise(kv.astype(np.float32)[None, :, None], dh, fmt)
+        vv = top * (1 + rng.random(size=(keys, dh)))
+        if mixed:
+            vv[rng.random(keys) < 0.7] *= 2.0 ** -90
+        vq, vs = oq.quantise(vv.astype(np.float32)[None, :, None], dh, fmt)
+        store = {"s8": torch.int8, "e4m3": torch.float8_e4m3fn}[fmt]
+        K = sige.QCache(torch.from_numpy(oq.stored(kq, fmt)).view(store).to(DEV), torch.from_numpy(ks).to(DEV), fmt)
+        V = sige.QCache(torch.from_numpy(oq.stored(vq, fmt)).view(store).to(DEV), torch.from_numpy(vs).to(DEV), fmt)
+        o = sige.sige_attention_qcache(q.to(DEV), K, V, 1)
+        assert torch.isfinite(o).all(), (keys, rise, top, mixed)
+        compare(o.cpu().view(1, 20, dh), oq.f64(q).reshape(1, 20, dh), oq.values(kq, ks)[:, :, 0], oq.values(vq, vs)[:, :, 0], 1,
+                np.arange(20))
