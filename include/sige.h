@@ -537,8 +537,8 @@ int sige_qcache_read(const void *codes, const float *scales, const sige_qcache_d
  *   workspace: device, >= SIGE_WORKSPACE_HEADER_BYTES (the device error word),
  *              16-byte aligned, zero-filled before its first use
  * The sums run on the tensor cores; sige_qlinear_path says how the codes reach
- * them.  A device-side wait that expires records SIGE_ERR_TIMEOUT and leaves
- * outputs unwritten.  Errors:
+ * them.  A device-side wait that expires records SIGE_ERR_TIMEOUT: outputs that
+ * its CTA had not finished are left unwritten, others hold their values.  Errors:
  * SIGE_ERR_INVALID_ARG, SIGE_ERR_UNSUPPORTED (format, group, dtype, layout,
  * c > 131071, c_out > 2^31 - 1025, block > 64, more than 2^31 - 1 pixels or
  * listed slots),

@@ -1060,6 +1060,7 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
             // channels at a time
             const int pt = (g ^ 1) * kGroup + r;
             float wa = 0.0f, wb = 0.0f, inv = 0.0f;
+            bool both = false;   // neither group's wait has expired
 #pragma unroll 1
             for (int p0 = 0; p0 < args.dvp; p0 += 64) {
                 float o[32];
@@ -1081,13 +1082,14 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
                     sts_f4(at, m);
                     sts_f4(at + kSoft * 16u, m + 4);
                 }
-                if (p0 == 0)   // (a sum of -1: no key)
+                if (p0 == 0)   // (a sum of -1: no key; -2: a wait expired, the row is not written)
                     asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sb + L::kOffMl + (uint32_t)tid * 8u), "f"(m_used),
-                                 "f"(mine ? l : -1.0f) : "memory");
+                                 "f"(!ok ? -2.0f : mine ? l : -1.0f) : "memory");
                 soft_sync<kSoft>();
                 if (p0 == 0) {
                     const float2 ml = lds_f2(sb + L::kOffMl + (uint32_t)pt * 8u);
                     const bool other = ml.y != -1.0f;
+                    both = ok && ml.y != -2.0f;
                     const float mm = fmaxf(mine ? m_used : -INFINITY, other ? ml.x : -INFINITY);
                     wa = mine ? ex2(m_used - mm) : 0.0f;
                     wb = other ? ex2(ml.x - mm) : 0.0f;
@@ -1097,7 +1099,7 @@ __global__ void __launch_bounds__(at::Lay<KD>::kThreads, 1) k_attn_qcache_tc(con
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int gi = p0 / 8 + 2 * k + g;
-                    if (ok && pix >= 0 && gi < ng) {
+                    if (both && pix >= 0 && gi < ng) {
                         const uint32_t src = sb + L::kOffX + (uint32_t)(2 * k * kSoft + pt) * 16u;
                         const float4 y0 = lds_f4(src), y1 = lds_f4(src + kSoft * 16u);
                         float *oo = o + 8 * k;
