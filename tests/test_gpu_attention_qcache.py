@@ -391,3 +391,15 @@ def test_large_values(dh, fmt):
         assert torch.isfinite(o).all(), (keys, rise, top, mixed)
         compare(o.cpu().view(1, 20, dh), oq.f64(q).reshape(1, 20, dh), oq.values(kq, ks)[:, :, 0], oq.values(vq, vs)[:, :, 0], 1,
                 np.arange(20))
+
+
+@pytest.mark.parametrize("n,h,w,heads,dh,keys,counts", [
+    (32, 8, 8, 8, 40, 260, None), (25, 8, 16, 8, 40, 129, None), (20, 8, 8, 8, 80, 200, None), (19, 5, 5, 8, 30, 150, None),
+    (12, 24, 16, 8, 40, 300, None), (9, 24, 16, 8, 40, 300, None), (10, 19, 17, 8, 100, 70, None), (150, 3, 3, 1, 160, 90, None),
+    (40, 4, 4, 4, 40, 200, "ragged"), (23, 24, 13, 4, 80, 140, "ragged"),
+])
+def test_more_units_than_ctas(n, h, w, heads, dh, keys, counts):
+    """One, two or three blocks of queries an item and more of them than the launch
+    has CTAs: alone or two to a unit."""
+    counts = None if counts is None else [(37 * i) % (keys + 1) for i in range(n)]
+    case(n + dh, n, h, w, heads, dh, dh, keys, "s8", "e4m3", counts=counts)
