@@ -52,8 +52,9 @@ __device__ __forceinline__ int64_t query_pixel(const AttnQParams &p, int n, int 
     const int2 org = __ldg(reinterpret_cast<const int2 *>(p.idx) + t);
     if (org.x < 0 || org.y < 0 || org.x >= p.H || org.y >= p.W)
         return -1;
-    const int y = org.x + (int)dy, x = org.y + (int)dx;
-    return y < p.H && x < p.W ? ((int64_t)n * p.H + y) * p.W + x : -1;
+    if ((int)dy >= p.H - org.x || (int)dx >= p.W - org.y)   // (a sum may leave 32 bits)
+        return -1;
+    return ((int64_t)n * p.H + org.x + (int)dy) * p.W + org.y + (int)dx;
 }
 
 __device__ __forceinline__ int key_count(const AttnQParams &p, int n)

@@ -38,10 +38,9 @@ __device__ __forceinline__ int64_t pixel_of(const PixelList &p, uint32_t i)
     const int2 org = __ldg(reinterpret_cast<const int2 *>(p.idx) + t);
     if (org.x < 0 || org.y < 0 || org.x >= p.H || org.y >= p.W)
         return -1;
-    const int y = org.x + (int)dy, x = org.y + (int)dx;
-    if (y >= p.H || x >= p.W)
+    if ((int)dy >= p.H - org.x || (int)dx >= p.W - org.y)   // (a sum may leave 32 bits)
         return -1;
-    return ((int64_t)n * p.H + y) * p.W + x;
+    return ((int64_t)n * p.H + org.x + (int)dy) * p.W + org.y + (int)dx;
 }
 
 // Fills `p`; a sige_status.  *slots = the most pixels the call can cover.
