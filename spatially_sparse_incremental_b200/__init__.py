@@ -763,6 +763,50 @@ def sige_attention_qcache_path(dh: int, dvh: int) -> int:
     return int(lib().sige_attention_qcache_path(int(dh), int(dvh)))
 
 
+def _overlap(a, b) -> bool:
+    return a.data_ptr() < b.data_ptr() + b.nbytes and b.data_ptr() < a.data_ptr() + a.nbytes
+
+
+def _check_sparse_q(x, where, wq, wo, bo, heads, k_map, v_map, y, wk, wv, residual, key_counts, workspace) -> int:
+    """Everything that a step of sige_attention_sparse_q would refuse, before the
+    first step: once the caches are updated there is no way back.  The device's
+    index."""
+    what = "sige_attention_sparse_q"
+    xs = x.shape
+    _map_desc(what + ": x", x, xs)
+    _tile_args(what, **where)
+    N, H, W, C = xs
+    D, Dv = k_map.shape[3], v_map.shape[3]
+    for name, w, rows, cols in (("wq", wq, D, C), ("wk", wk, D, C), ("wv", wv, Dv, C), ("wo", wo, wo.shape[0], Dv)):
+        if w is not None and (w.format != "s8" or w.shape != (rows, 1, 1, cols) or w.group != cols):
+            raise ValueError(f'{what}: {name} is an "s8" cache [{rows}, 1, 1, {cols}] with one scale a row')
+    for name, w, cache in (("k_map", wk, k_map), ("v_map", wv, v_map)):
+        if cache.shape[0] != N or (w is not None and cache.shape[:3] != (N, H, W)):
+            raise ValueError(f"{what}: {name} of shape {cache.shape} does not fit a map {tuple(xs)}")
+        if w is not None and (_overlap(cache.codes, cache.scales) or _overlap(k_map.codes, v_map.codes) or
+                              _overlap(k_map.scales, v_map.scales)):
+            raise ValueError(f"{what}: the key and value caches share memory")
+    if k_map.shape[1] * k_map.shape[2] != v_map.shape[1] * v_map.shape[2]:
+        raise ValueError(f"{what}: keys {k_map.shape} and values {v_map.shape} differ in number")
+    if heads < 1 or D % heads or Dv % heads:
+        raise ValueError(f"{what}: {heads} heads do not divide {D} and {Dv} channels")
+    if k_map.group % (D // heads) or v_map.group % (Dv // heads) or sige_attention_qcache_path(D // heads, Dv // heads) < 0:
+        raise ValueError(f"{what}: heads of {D // heads} and {Dv // heads} channels, scales of {k_map.group} and {v_map.group}: "
+                         "a scale covers whole heads of up to 256 channels")
+    if key_counts is not None and (key_counts.dtype != torch.int32 or key_counts.numel() != N or not key_counts.is_contiguous()):
+        raise ValueError(f"{what}: key_counts is a contiguous int32 tensor of one count per item")
+    _map_desc(what + ": y", y, (N, H, W, wo.shape[0]))
+    _f32(what + ": bo", bo, (wo.shape[0],))
+    if residual is not None and (residual.shape != y.shape or residual.dtype != y.dtype or not residual.is_contiguous()):
+        raise ValueError(f"{what}: the residual is a contiguous tensor of y's shape and dtype")
+    if any(t is not None and _overlap(y, t) for t in (residual, bo, wo.codes, wo.scales, where["idx"], where["count"], workspace)):
+        raise ValueError(f"{what}: y shares memory with an operand")
+    if workspace is not None and (workspace.nbytes < WORKSPACE_HEADER or workspace.data_ptr() % 16):
+        raise ValueError(f"{what}: a workspace of {WORKSPACE_HEADER} bytes, 16-byte aligned, is expected")
+    caches = [t for c in (wq, wk, wv, wo, k_map, v_map) if c is not None for t in (c.codes, c.scales)]
+    return _device_index(what, x, y, where["idx"], where["count"], bo, residual, key_counts, workspace, *caches)
+
+
 def sige_attention_sparse_q(x, idx, count, capacity: int, block: int, wq: QCache, wo: QCache, bo, heads: int,
                             k_map: QCache, v_map: QCache, y, wk: QCache | None = None, wv: QCache | None = None,
                             residual=None, key_counts=None, workspace=None, stream=None):
@@ -772,11 +816,14 @@ def sige_attention_sparse_q(x, idx, count, capacity: int, block: int, wq: QCache
     the key and value caches ``k_map`` / ``v_map`` (any format) are updated at
     those tokens when ``wk`` / ``wv`` are given (self-attention; else they are
     the context's), and y = o Wo + bo (+ residual) at those tokens of the
-    cached output ``y``."""
+    cached output ``y``.  Queries, keys, values and the step's output are rounded
+    to bf16 between the calls, as in sige_attention_sparse.  A call that is
+    refused leaves caches and output as they were."""
+    where = dict(idx=idx, count=count, capacity=capacity, block=block)
+    index = _check_sparse_q(x, where, wq, wo, bo, heads, k_map, v_map, y, wk, wv, residual, key_counts, workspace)
     N, H, W, C = x.shape
     dev = x.device
-    where = dict(idx=idx, count=count, capacity=capacity, block=block)
-    with _Launch(_device_index("sige_attention_sparse_q", x, y, k_map.codes, v_map.codes), stream):
+    with _Launch(index, stream):
         if workspace is None:
             workspace = zeros_workspace(WORKSPACE_HEADER, dev)
         xq = sige_qcache_write(x, qcache_empty(N, H, W, C, device=dev), **where)

@@ -403,3 +403,32 @@ def test_more_units_than_ctas(n, h, w, heads, dh, keys, counts):
     has CTAs: alone or two to a unit."""
     counts = None if counts is None else [(37 * i) % (keys + 1) for i in range(n)]
     case(n + dh, n, h, w, heads, dh, dh, keys, "s8", "e4m3", counts=counts)
+
+
+def test_a_refused_layer_changes_nothing():
+    """Whatever step would refuse: the caches and the output keep their bytes."""
+    rng = np.random.default_rng(3)
+    n, h, w, C, heads, b = 1, 8, 8, 64, 2, 4
+    q8 = lambda co, ci: sige.sige_qcache_write(torch.from_numpy(rng.normal(size=(co, 1, 1, ci)).astype(np.float32)).to(DEV),
+                                               sige.qcache_empty(co, 1, 1, ci))
+    _, where = tile_list(rng, h, w, b, 0.5)
+    x = torch.from_numpy(rng.normal(size=(n, h, w, C))).to(torch.bfloat16).to(DEV)
+    K, V = (random_cache(rng, n, h, w, C, C // heads, "s8")[0] for _ in range(2))
+    y = torch.from_numpy(rng.normal(size=(n, h, w, C))).to(torch.bfloat16).to(DEV)
+    good = dict(x=x, **where, wq=q8(C, C), wo=q8(C, C), bo=None, heads=heads, k_map=K, v_map=V, y=y, wk=q8(C, C), wv=q8(C, C))
+    state = lambda: [t.clone() for t in (K.codes, K.scales, V.codes, V.scales, y)]
+    before = state()
+    grouped = sige.QCache(good["wo"].codes, torch.ones((C, 1, 1, 2), device=DEV), "s8")
+    for bad in (dict(wv=q8(C, 32)), dict(wv=q8(32, C)), dict(wo=q8(C, 32)), dict(wo=grouped), dict(wo=q8(48, C)), dict(heads=3), dict(heads=0),
+                dict(heads=4096), dict(y=y[:, :4]), dict(y=y.float().double()), dict(residual=x.float()), dict(residual=y), dict(bo=torch.ones(3, device=DEV)),
+                dict(key_counts=torch.ones(2, dtype=torch.int32, device=DEV)), dict(v_map=K), dict(v_map=random_cache(rng, n, 4, w, C, 32, "s8")[0]),
+                dict(v_map=random_cache(rng, n, h, w, C, 16, "s8")[0]), dict(k_map=random_cache(rng, n, h, w, C, 8, "e4m3")[0]),
+                dict(workspace=torch.zeros(64, dtype=torch.uint8, device=DEV)), dict(wq=q8(32, C)), dict(block=65), dict(bo=torch.ones(C)),
+                dict(count=None), dict(capacity=10 ** 6), dict(capacity=-1)):
+        with pytest.raises((ValueError, sige.SigeError)):
+            sige.sige_attention_sparse_q(**{**good, **bad})
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(before, state())), bad
+    sige.sige_attention_sparse_q(**good)
+    torch.cuda.synchronize()
+    assert not any(torch.equal(a, c) for a, c in zip(before, state()))
