@@ -502,7 +502,7 @@ size_t sige_qcache_scales(const sige_qcache_desc *cd);
  * NaN scale and codes 0: it reads back as NaN.  Codes and scales of other
  * pixels are left as they are.
  *   x      : device NHWC f32 or bf16 (xd), the cache's n, h, w, c
- *   codes, scales : device, not overlapping x or each other
+ *   codes, scales : device, not overlapping any operand or each other
  * A weight matrix [c_out][c_in] is written as a map of n = c_out, h = w = 1.
  * Any c, group and alignment; 8, 4 or 2 elements move at once as the group
  * and the addresses allow (groups up to 256 times that).  Errors:
@@ -516,7 +516,8 @@ int sige_qcache_write(const void *x, const sige_tensor_desc *xd, const float *gn
 
 /* (9b) Read it back: y = round(code * scale) at the listed tiles (a restore
  * of the original's tiles from the cache, as (7)) or at every pixel; every
- * other byte of y is left as it is.  y: device NHWC f32 or bf16 (yd).
+ * other byte of y is left as it is.  y: device NHWC f32 or bf16 (yd), not
+ * overlapping any operand.
  * Arguments and errors as (9). */
 int sige_qcache_read(const void *codes, const float *scales, const sige_qcache_desc *cd, int32_t block,
                      const int32_t *idx, const int32_t *count, int32_t capacity, void *y, const sige_tensor_desc *yd,

@@ -231,7 +231,7 @@ extern "C" int sige_attention_qcache(const void *q, const sige_tensor_desc *qd, 
     if (ranges_overlap(o, obytes, q, pixels * qd->c * 2) || ranges_overlap(o, obytes, k_codes, qcache_bytes(kd)) ||
         ranges_overlap(o, obytes, v_codes, qcache_bytes(vd)) ||
         ranges_overlap(o, obytes, k_scales, 4 * qcache_scale_count(kd)) ||
-        ranges_overlap(o, obytes, v_scales, 4 * qcache_scale_count(vd)))
+        ranges_overlap(o, obytes, v_scales, 4 * qcache_scale_count(vd)) || ranges_overlap(o, obytes, key_counts, 4ll * qd->n))
         return SIGE_ERR_INVALID_ARG;
     PixelList px;
     AttnQParams p{};
@@ -240,6 +240,8 @@ extern "C" int sige_attention_qcache(const void *q, const sige_tensor_desc *qd, 
         return st;
     if (!workspace || workspace_bytes < kWsHeader || !aligned_to(workspace, 16))
         return SIGE_ERR_WORKSPACE;
+    if (list_overlaps(o, obytes, idx, count, capacity) || ranges_overlap(o, obytes, workspace, kWsHeader))
+        return SIGE_ERR_INVALID_ARG;
     if (p.slots == 0)
         return SIGE_OK;
     p.slots /= qd->n;

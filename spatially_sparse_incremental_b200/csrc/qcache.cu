@@ -563,6 +563,12 @@ extern "C" int sige_qcache_write(const void *x, const sige_tensor_desc *xd, cons
         return st;
     if ((gn_scale == nullptr) != (gn_shift == nullptr) || !aligned_to(gn_scale, 4) || !aligned_to(gn_shift, 4))
         return SIGE_ERR_INVALID_ARG;
+    // the cache is written while the other operands are read
+    const int64_t cb = qcache_bytes(cd), sb = 4 * qcache_scale_count(cd), gb = 4ll * cd->n * cd->c;
+    if (ranges_overlap(codes, cb, gn_scale, gb) || ranges_overlap(codes, cb, gn_shift, gb) ||
+        ranges_overlap(scales, sb, gn_scale, gb) || ranges_overlap(scales, sb, gn_shift, gb) ||
+        list_overlaps(codes, cb, idx, count, capacity) || list_overlaps(scales, sb, idx, count, capacity))
+        return SIGE_ERR_INVALID_ARG;
     if (slots == 0)
         return SIGE_OK;
     a.x = static_cast<const uint8_t *>(x);
@@ -589,6 +595,8 @@ extern "C" int sige_qcache_read(const void *codes, const float *scales, const si
     const int st = qc::common(&a, y, yd, codes, scales, cd, block, idx, count, capacity, &slots, &n);
     if (st != SIGE_OK)
         return st;
+    if (list_overlaps(y, (int64_t)cd->n * cd->h * cd->w * cd->c * (yd->dtype == SIGE_BF16 ? 2 : 4), idx, count, capacity))
+        return SIGE_ERR_INVALID_ARG;
     if (slots == 0)
         return SIGE_OK;
     a.y = static_cast<uint8_t *>(y);

@@ -141,6 +141,11 @@ inline bool ranges_overlap(const void *a, int64_t na, const void *b, int64_t nb)
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return a && b && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
 }
+// Whether the tile list or its count lies in memory that the call writes.
+inline bool list_overlaps(const void *a, int64_t na, const int32_t *idx, const int32_t *count, int32_t capacity)
+{
+    return idx && (ranges_overlap(a, na, idx, 8ll * capacity) || ranges_overlap(a, na, count, 4));
+}
 inline bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 } // namespace sige

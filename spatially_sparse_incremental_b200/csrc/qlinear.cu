@@ -49,6 +49,8 @@ extern "C" int sige_qlinear(const void *a_codes, const float *a_scales, const si
         return st;
     if (!workspace || workspace_bytes < kWsHeader || !aligned_to(workspace, 16))
         return SIGE_ERR_WORKSPACE;
+    if (list_overlaps(y, ybytes, idx, count, capacity) || ranges_overlap(y, ybytes, workspace, kWsHeader))
+        return SIGE_ERR_INVALID_ARG;
     if (p.slots == 0)
         return SIGE_OK;
     p.a = static_cast<const uint8_t *>(a_codes);

@@ -161,3 +161,27 @@ def test_counts_near_the_end_of_32_bits(L):
     q, k = _td(n=1, h=1, w=1, c=16), _qd(n=1, h=most, w=1, c=16, group=16)
     assert L.sige_attention_qcache(X, r(q), CODES, SCALES, r(k), W, SW, r(k), None, 1, 1, None, None, 0, OUT, WS, 256,
                                    None) == sige.ERR_UNSUPPORTED
+
+
+def test_outputs_in_an_operand_are_refused(L):
+    """An output over the list, its count, the affine, the key counts or the
+    workspace: refused like one over any other operand."""
+    r = ctypes.byref
+    at = lambda p, k: ctypes.c_void_p(p.value + k)
+    xb, cb, sb = 16 * 16 * 320 * 2, 16 * 16 * 320, 16 * 16 * 8 * 4
+    for kw in (dict(gs=at(CODES, cb - 4), gh=B), dict(gs=B, gh=at(SCALES, -4 * 320 + 4)), dict(gs=SCALES, gh=B), dict(idx=at(CODES, 8)),
+               dict(idx=at(CODES, -8 * 16 + 8)), dict(cnt=at(SCALES, sb - 4)), dict(cnt=CODES), dict(idx=SCALES)):
+        assert _rw(L, True, **kw) == sige.ERR_INVALID_ARG, kw
+    for kw in (dict(idx=at(X, xb - 8)), dict(idx=at(X, -8)), dict(cnt=X)):
+        assert _rw(L, False, **kw) == sige.ERR_INVALID_ARG, kw
+    assert _rw(L, False, idx=at(CODES, 8), cap=0) == sige.OK      # (operands may share memory)
+    lin = lambda **k: L.sige_qlinear(CODES, SCALES, r(_qd(group=320)), W, SW, r(_qd(n=64, h=1, w=1, group=320)), None, 4,
+                                     k.get("idx", IDX), k.get("cnt", CNT), 16, None, OUT, r(_td(c=64)), k.get("ws", WS), 256, None)
+    yb = 16 * 16 * 64 * 2
+    for kw in (dict(idx=OUT), dict(idx=at(OUT, yb - 8)), dict(cnt=at(OUT, 4)), dict(ws=at(OUT, yb - 16)), dict(ws=at(OUT, -240))):
+        assert lin(**kw) == sige.ERR_INVALID_ARG, kw
+    kd = _qd(h=77, w=1)
+    att = lambda **k: L.sige_attention_qcache(X, r(_td()), CODES, SCALES, r(kd), W, SW, r(kd), k.get("kc"), 8, 4, k.get("idx", IDX),
+                                              k.get("cnt", CNT), 16, OUT, k.get("ws", WS), 256, None)
+    for kw in (dict(kc=OUT), dict(kc=at(OUT, xb - 4)), dict(idx=at(OUT, -120)), dict(cnt=OUT), dict(ws=OUT)):
+        assert att(**kw) == sige.ERR_INVALID_ARG, kw
