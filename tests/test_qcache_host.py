@@ -185,3 +185,24 @@ def test_outputs_in_an_operand_are_refused(L):
                                               k.get("cnt", CNT), 16, OUT, k.get("ws", WS), 256, None)
     for kw in (dict(kc=OUT), dict(kc=at(OUT, xb - 4)), dict(idx=at(OUT, -120)), dict(cnt=OUT), dict(ws=OUT)):
         assert att(**kw) == sige.ERR_INVALID_ARG, kw
+
+
+def test_sizes_past_32_bits_are_refused():
+    """Sizes that an int32 would take modulo 2^32 (5 pixels of 2^32 + 5)."""
+    at = lambda shape, dt: torch.empty(shape, dtype=dt, device="meta")
+    for shape in ((1, 1, 2 ** 32 + 5, 1), (2 ** 32 + 1, 1, 1, 2), (1, 2 ** 31, 1, 8), (1, 1, 1, 2 ** 32 + 16)):
+        with pytest.raises(ValueError, match="32 bits"):
+            sige.QCache(at(shape, torch.int8), at((*shape[:3], 1), torch.float32), "s8")
+        with pytest.raises(ValueError, match="32 bits"):
+            sige.qcache_empty(*shape, device="meta")
+    with pytest.raises(ValueError, match="32 bits"):
+        sige.QCache(at((1, 1, 1, 2 ** 30), torch.uint8), at((1, 1, 1, 1), torch.float32), "s4")   # 2^31 channels
+    c = sige.QCache(torch.zeros((1, 4, 4, 16), dtype=torch.int8), torch.zeros((1, 4, 4, 1)), "s8")
+    x = torch.zeros((1, 4, 4, 16), dtype=torch.bfloat16)
+    idx, cnt = torch.zeros((2, 2), dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="32 bits"):
+        sige.sige_qcache_write(x, c, idx=idx, count=cnt, capacity=2, block=2 ** 32 + 4)
+    with pytest.raises(ValueError, match="32 bits"):
+        sige.sige_attention_qcache(at((1, 2 ** 32 + 4, 1, 16), torch.bfloat16), c, c, 2)
+    with pytest.raises(ValueError, match="32 bits"):
+        sige.sige_attention_qcache(x, c, c, 2 ** 32 + 2)
