@@ -267,13 +267,14 @@ struct Args {
 // memory (col: kMaxBn scales, then kMaxBn biases).
 __device__ __forceinline__ void scale16(const int *acc, uint32_t col, float sa, float *v)
 {
+    const TokenScale t = token_scale(sa);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const float4 s = lds_f32x4(col + 16u * q), b = lds_f32x4(col + 4u * kMaxBn + 16u * q);
-        v[4 * q] = qlinear_value(acc[4 * q], sa, s.x) + b.x;
-        v[4 * q + 1] = qlinear_value(acc[4 * q + 1], sa, s.y) + b.y;
-        v[4 * q + 2] = qlinear_value(acc[4 * q + 2], sa, s.z) + b.z;
-        v[4 * q + 3] = qlinear_value(acc[4 * q + 3], sa, s.w) + b.w;
+        v[4 * q] = qlinear_value(acc[4 * q], t, s.x, b.x);
+        v[4 * q + 1] = qlinear_value(acc[4 * q + 1], t, s.y, b.y);
+        v[4 * q + 2] = qlinear_value(acc[4 * q + 2], t, s.z, b.z);
+        v[4 * q + 3] = qlinear_value(acc[4 * q + 3], t, s.w, b.w);
     }
 }
 

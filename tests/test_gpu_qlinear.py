@@ -257,3 +257,25 @@ def test_codes_at_any_byte(c, ao, wo):
     y = sige.sige_qlinear(A, W, dtype=torch.float32)
     torch.cuda.synchronize()
     check(y, a, sa, wt, sw, None, None, torch.float32)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,h,w,c,co", [(1, 16, 16, 320, 320), (1, 1, 3, 1280, 64), (1, 9, 15, 64, 51), (1, 13, 11, 74, 40)])
+def test_scales_at_the_ends_of_the_range(n, h, w, c, co, dtype):
+    """Token scales up to 2^119 and channel scales down to 2^-126, the other way
+    round, and ordinary tokens beside them: finite wherever the value is."""
+    rng = np.random.default_rng(c)
+    a, sa, wt, sw = operands(rng, n, h, w, c, co)
+    ends = np.ldexp(1.0 + rng.random(sa.shape), rng.choice([-126, -40, 0, 60, 97, 110, 118], sa.shape)).astype(np.float32)
+    for lo, hi in ((-126, -110), (-100, -60), (-30, 0)):
+        tok = np.where(rng.random(sa.shape) < 0.7, np.minimum(ends, np.float32(2.0 ** (124 - 24 - hi) if hi > -24 else 3e38)), sa)
+        ch = np.ldexp(1.0 + rng.random(sw.shape), rng.integers(lo, hi, sw.shape)).astype(np.float32)
+        for x, y in ((tok.astype(np.float32), ch),
+                     (np.ldexp(1.0 + rng.random(sa.shape), rng.integers(lo, hi, sa.shape)).astype(np.float32),
+                      np.resize(tok, sw.shape).astype(np.float32))):
+            res = torch.from_numpy(rng.normal(size=(n, h, w, co))).to(dtype)
+            got = sige.sige_qlinear(cache(a, x), cache(wt, y), residual=res.to(DEV), dtype=dtype)
+            torch.cuda.synchronize()
+            ref = oq.qlinear(a.reshape(-1, c), x.reshape(-1), wt.reshape(co, c), y.reshape(-1))
+            assert np.abs(ref).max() < 2.0 ** 127 and torch.isfinite(got).all()
+            check(got, a, x, wt, y, None, res, dtype)
