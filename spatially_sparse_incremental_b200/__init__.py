@@ -667,7 +667,9 @@ def _tile_args(what: str, idx, count, capacity, block):
     if capacity > 0 and idx.numel() < 2 * capacity:
         raise ValueError(f"{what}: the list holds {idx.numel() // 2} tiles, fewer than its capacity {capacity}")
     _in_32_bits(what, block, capacity)
-    return block, idx.data_ptr(), count.data_ptr(), capacity
+    # (a tensor without elements has no address, and a list of no address is every
+    # pixel to the library: any other stands for it, nothing is read there)
+    return block, idx.data_ptr() or 8, count.data_ptr(), capacity
 
 
 def sige_qcache_write(x, cache: QCache, idx=None, count=None, capacity=0, block=1, gn_scale=None, gn_shift=None,

@@ -98,3 +98,34 @@ def test_offsets_past_32_bits(fmt):
     # (the weight rounded, the result rounded; 2^-10 for scores of 2^12 in float32, dh + 4
     # roundings of 2^-24 each; the zero keys' 1.1M weights are below e^-1000)
     assert (np.abs(o - ref[0]) <= np.abs(ref[0]) * 2.0 ** -8 + ref_abs[0] * (2.0 ** -8 + 2.0 ** -5)).all()
+
+
+def test_a_list_without_places_is_no_pixel():
+    """A tile list of shape [0, 2] (its tensor has no address) is an empty list, not
+    every pixel."""
+    rng = np.random.default_rng(8)
+    draw = lambda *shape: torch.from_numpy(rng.normal(size=shape)).to(torch.bfloat16).to(DEV)
+    n, h, w, c = 1, 8, 8, 32
+    none = dict(idx=torch.empty((0, 2), dtype=torch.int32, device=DEV), count=torch.zeros(1, dtype=torch.int32, device=DEV), capacity=0,
+                block=4)
+    tail = dict(none, idx=torch.zeros((4, 2), dtype=torch.int32, device=DEV)[4:])
+    wt = sige.sige_qcache_write(draw(c, 1, 1, c), sige.qcache_empty(c, 1, 1, c))
+    K, V = (sige.sige_qcache_write(draw(n, h, w, c), sige.qcache_empty(n, h, w, c, group=16)) for _ in range(2))
+    A = sige.sige_qcache_write(draw(n, h, w, c), sige.qcache_empty(n, h, w, c))
+    x, y = draw(n, h, w, c), draw(n, h, w, c)
+    kept = (K.codes, K.scales, V.codes, V.scales, A.codes, A.scales, y)
+    before = [t.clone() for t in kept]
+    launches = sige.sige_launch_count()
+    for where in (none, tail):
+        sige.sige_qcache_write(x, K, **where)
+        sige.sige_qcache_read(K, y, **where)
+        sige.sige_qlinear(A, wt, None, y, **where)
+        sige.sige_attention_qcache(x, K, V, 2, y, **where)
+        sige.sige_attention_sparse_q(x, where["idx"], where["count"], 0, 4, wt, wt, None, 2, K, V, y, wk=wt, wv=wt)
+        with pytest.raises((ValueError, sige.SigeError)):
+            sige.sige_qcache_write(x, K, **dict(where, capacity=1))
+        with pytest.raises((ValueError, sige.SigeError)):
+            sige.sige_qcache_write(x, K, **dict(where, block=0))
+    torch.cuda.synchronize()
+    assert sige.sige_launch_count() == launches
+    assert all(torch.equal(a, b) for a, b in zip(kept, before))
