@@ -775,48 +775,56 @@ def sige_attention_qcache_path(dh: int, dvh: int) -> int:
     return int(lib().sige_attention_qcache_path(int(dh), int(dvh)))
 
 
+def _range(t):
+    a = t.data_ptr()
+    return a, a + t.numel() * t.element_size()
+
+
 def _overlap(a, b) -> bool:
-    return a.data_ptr() < b.data_ptr() + b.nbytes and b.data_ptr() < a.data_ptr() + a.nbytes
+    return a[0] < b[1] and b[0] < a[1]
 
 
-def _check_sparse_q(x, where, wq, wo, bo, heads, k_map, v_map, y, wk, wv, residual, key_counts, workspace) -> int:
+def _check_sparse_q(what, x, idx, count, wq, wo, bo, heads, k_map, v_map, y, wk, wv, residual, key_counts, workspace):
     """Everything that a step of sige_attention_sparse_q would refuse, before the
-    first step: once the caches are updated there is no way back.  The device's
-    index."""
-    what = "sige_attention_sparse_q"
-    xs = x.shape
-    _map_desc(what + ": x", x, xs)
-    _tile_args(what, **where)
-    N, H, W, C = xs
-    D, Dv = k_map.shape[3], v_map.shape[3]
-    for name, w, rows, cols in (("wq", wq, D, C), ("wk", wk, D, C), ("wv", wv, Dv, C), ("wo", wo, wo.shape[0], Dv)):
-        if w is not None and (w.format != "s8" or w.shape != (rows, 1, 1, cols) or w.group != cols):
-            raise ValueError(f'{what}: {name} is an "s8" cache [{rows}, 1, 1, {cols}] with one scale a row')
-    for name, w, cache in (("k_map", wk, k_map), ("v_map", wv, v_map)):
-        if cache.shape[0] != N or (w is not None and cache.shape[:3] != (N, H, W)):
-            raise ValueError(f"{what}: {name} of shape {cache.shape} does not fit a map {tuple(xs)}")
-        if w is not None and (_overlap(cache.codes, cache.scales) or _overlap(k_map.codes, v_map.codes) or
-                              _overlap(k_map.scales, v_map.scales)):
-            raise ValueError(f"{what}: the key and value caches share memory")
-    if k_map.shape[1] * k_map.shape[2] != v_map.shape[1] * v_map.shape[2]:
-        raise ValueError(f"{what}: keys {k_map.shape} and values {v_map.shape} differ in number")
+    first step: once the caches are updated there is no way back.  Descriptors of
+    x and y, and the device's index."""
+    xd = _map_desc(what, x, x.shape)
+    N, H, W, C = x.shape
+    ks, vs, rows = k_map.shape, v_map.shape, wo.shape[0]
+    D, Dv = ks[3], vs[3]
+    for name, w, r, c in (("wq", wq, D, C), ("wk", wk, D, C), ("wv", wv, Dv, C), ("wo", wo, rows, Dv)):
+        if w is not None and (w.format != "s8" or w.shape != (r, 1, 1, c) or w.desc.group != c or c > 131071):
+            raise ValueError(f'{what}: {name} is an "s8" cache [{r}, 1, 1, {c}] with one scale a row')
+    if ks[0] != N or vs[0] != N or ks[1] * ks[2] != vs[1] * vs[2] or (wk is not None and ks[:3] != (N, H, W)) or \
+            (wv is not None and vs[:3] != (N, H, W)):
+        raise ValueError(f"{what}: keys {ks} and values {vs} do not fit a map {(N, H, W, C)}")
     if heads < 1 or D % heads or Dv % heads:
         raise ValueError(f"{what}: {heads} heads do not divide {D} and {Dv} channels")
-    if k_map.group % (D // heads) or v_map.group % (Dv // heads) or sige_attention_qcache_path(D // heads, Dv // heads) < 0:
-        raise ValueError(f"{what}: heads of {D // heads} and {Dv // heads} channels, scales of {k_map.group} and {v_map.group}: "
-                         "a scale covers whole heads of up to 256 channels")
+    dh, dvh, kg, vg = D // heads, Dv // heads, k_map.desc.group, v_map.desc.group
+    if kg % dh or vg % dvh or dh > 256 or dvh > 256:
+        raise ValueError(f"{what}: heads of {dh} and {dvh} channels, scales of {kg} and {vg}: a scale covers whole heads of up to "
+                         "256 channels")
     if key_counts is not None and (key_counts.dtype != torch.int32 or key_counts.numel() != N or not key_counts.is_contiguous()):
         raise ValueError(f"{what}: key_counts is a contiguous int32 tensor of one count per item")
-    _map_desc(what + ": y", y, (N, H, W, wo.shape[0]))
-    _f32(what + ": bo", bo, (wo.shape[0],))
-    if residual is not None and (residual.shape != y.shape or residual.dtype != y.dtype or not residual.is_contiguous()):
+    yd = _map_desc(what, y, (N, H, W, rows))
+    _f32(what, bo, (rows,))
+    if residual is not None and (residual.dtype != y.dtype or residual.shape != y.shape or not residual.is_contiguous()):
         raise ValueError(f"{what}: the residual is a contiguous tensor of y's shape and dtype")
-    if any(t is not None and _overlap(y, t) for t in (residual, bo, wo.codes, wo.scales, where["idx"], where["count"], workspace)):
-        raise ValueError(f"{what}: y shares memory with an operand")
+    at = _range(y)
+    for t in (wo.codes, wo.scales, bo, residual, workspace, idx, count):
+        if t is not None and _overlap(at, _range(t)):
+            raise ValueError(f"{what}: y shares memory with an operand")
+    if wk is not None or wv is not None:
+        kv = sorted(_range(t) for t in (k_map.codes, k_map.scales, v_map.codes, v_map.scales))
+        if any(_overlap(a, b) for a, b in zip(kv, kv[1:])):
+            raise ValueError(f"{what}: the key and value caches share memory")
     if workspace is not None and (workspace.nbytes < WORKSPACE_HEADER or workspace.data_ptr() % 16):
         raise ValueError(f"{what}: a workspace of {WORKSPACE_HEADER} bytes, 16-byte aligned, is expected")
-    caches = [t for c in (wq, wk, wv, wo, k_map, v_map) if c is not None for t in (c.codes, c.scales)]
-    return _device_index(what, x, y, where["idx"], where["count"], bo, residual, key_counts, workspace, *caches)
+    tensors = [x, y, idx, count, bo, residual, key_counts, workspace]
+    for c in (wq, wk, wv, wo, k_map, v_map):
+        if c is not None:
+            tensors += (c.codes, c.scales)
+    return xd, yd, _device_index(what, *tensors)
 
 
 def sige_attention_sparse_q(x, idx, count, capacity: int, block: int, wq: QCache, wo: QCache, bo, heads: int,
@@ -831,25 +839,42 @@ def sige_attention_sparse_q(x, idx, count, capacity: int, block: int, wq: QCache
     cached output ``y``.  Queries, keys, values and the step's output are rounded
     to bf16 between the calls, as in sige_attention_sparse.  A call that is
     refused leaves caches and output as they were."""
-    where = dict(idx=idx, count=count, capacity=capacity, block=block)
-    index = _check_sparse_q(x, where, wq, wo, bo, heads, k_map, v_map, y, wk, wv, residual, key_counts, workspace)
-    N, H, W, C = x.shape
-    dev = x.device
-    with _Launch(index, stream):
+    what = "sige_attention_sparse_q"
+    tiles = _tile_args(what, idx, count, capacity, block)
+    xd, yd, index = _check_sparse_q(what, x, idx, count, wq, wo, bo, heads, k_map, v_map, y, wk, wv, residual, key_counts,
+                                    workspace)
+    L, dev = lib(), x.device
+    n, h, w = xd.n, xd.h, xd.w
+    D, Dv = k_map.shape[3], v_map.shape[3]
+
+    def bf16(c):
+        return torch.empty((n, h, w, c), dtype=torch.bfloat16, device=dev), TensorDesc(n, h, w, c, BF16, NHWC)
+
+    def write(t, td, cache):
+        _check(L.sige_qcache_write(t.data_ptr(), td, None, None, 0, *tiles, cache.codes.data_ptr(), cache.scales.data_ptr(), cache.desc,
+                                   st), what)
+        return cache
+
+    def linear(a, wt, bias, res, out, od):
+        _check(L.sige_qlinear(a.codes.data_ptr(), a.scales.data_ptr(), a.desc, wt.codes.data_ptr(), wt.scales.data_ptr(), wt.desc,
+                              _addr(bias), *tiles, _addr(res), out.data_ptr(), od, workspace.data_ptr(), workspace.nbytes, st), what)
+
+    with _Launch(index, stream) as st:
         if workspace is None:
             workspace = zeros_workspace(WORKSPACE_HEADER, dev)
-        xq = sige_qcache_write(x, qcache_empty(N, H, W, C, device=dev), **where)
-        q = torch.empty((N, H, W, wq.shape[0]), dtype=torch.bfloat16, device=dev)
-        sige_qlinear(xq, wq, None, q, workspace=workspace, **where)
-        for w, cache in ((wk, k_map), (wv, v_map)):
-            if w is not None:
-                t = torch.empty(cache.shape, dtype=torch.bfloat16, device=dev)
-                sige_qlinear(xq, w, None, t, workspace=workspace, **where)
-                sige_qcache_write(t, cache, **where)
-        o = torch.empty((N, H, W, v_map.shape[3]), dtype=torch.bfloat16, device=dev)
-        sige_attention_qcache(q, k_map, v_map, heads, o, key_counts=key_counts, workspace=workspace, **where)
-        oq = sige_qcache_write(o, qcache_empty(N, H, W, o.shape[3], device=dev), **where)
-        sige_qlinear(oq, wo, bo, y, residual=residual, workspace=workspace, **where)
+        xq = write(x, xd, qcache_empty(n, h, w, xd.c, device=dev))
+        q, qd = bf16(D)
+        linear(xq, wq, None, None, q, qd)
+        for wt, cache in ((wk, k_map), (wv, v_map)):
+            if wt is not None:
+                t, td = bf16(cache.shape[3])
+                linear(xq, wt, None, None, t, td)
+                write(t, td, cache)
+        o, od = bf16(Dv)
+        _check(L.sige_attention_qcache(q.data_ptr(), qd, k_map.codes.data_ptr(), k_map.scales.data_ptr(), k_map.desc,
+                                       v_map.codes.data_ptr(), v_map.scales.data_ptr(), v_map.desc, _addr(key_counts), heads,
+                                       *tiles, o.data_ptr(), workspace.data_ptr(), workspace.nbytes, st), what)
+        linear(write(o, od, qcache_empty(n, h, w, Dv, device=dev)), wo, bo, residual, y, yd)
     return y
 
 
