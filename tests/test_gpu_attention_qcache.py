@@ -432,3 +432,41 @@ def test_a_refused_layer_changes_nothing():
     sige.sige_attention_sparse_q(**good)
     torch.cuda.synchronize()
     assert not any(torch.equal(a, c) for a, c in zip(before, state()))
+
+
+@pytest.mark.parametrize("cross,kf,vf", [(False, "s8", "e4m3"), (False, "s4", "s8"), (True, "s8", "s4"), (True, "e4m3", "e4m3")])
+def test_layer_and_its_caches(cross, kf, vf):
+    """The context's caches keep every byte; those of a self-attention get, at the
+    listed tokens, what quantising the projections there gives, codes and scales,
+    and keep the rest."""
+    rng = np.random.default_rng(21)
+    n, h, w, C, heads, b = 2, 10, 9, 64, 4, 4
+    idx, where = tile_list(rng, h, w, b, 0.3)
+    x = torch.from_numpy(rng.normal(size=(n, h, w, C))).to(torch.bfloat16).to(DEV)
+    wq, wk, wv, wo = (sige.sige_qcache_write(torch.from_numpy(rng.normal(0, C ** -0.5, size=(C, 1, 1, C)).astype(np.float32)).to(DEV),
+                                             sige.qcache_empty(C, 1, 1, C)) for _ in range(4))
+    shape = (n, 31, 1, C) if cross else (n, h, w, C)
+    K, V = (random_cache(rng, *shape, C // heads, f)[0] for f in (kf, vf))
+    raw = lambda c: (c.codes.view(torch.uint8).cpu().clone(), c.scales.cpu().clone())
+    K0, V0 = raw(K), raw(V)
+    y = torch.zeros((n, h, w, C), dtype=torch.bfloat16, device=DEV)
+    sige.sige_attention_sparse_q(x, where["idx"], where["count"], where["capacity"], b, wq, wo, None, heads, K, V, y,
+                                 wk=None if cross else wk, wv=None if cross else wv)
+    torch.cuda.synchronize()
+    if cross:
+        assert all(torch.equal(a, c) for a, c in zip((*K0, *V0), (*raw(K), *raw(V))))
+        return
+    tok = oq.tokens(idx, b, h, w)
+    rest = np.setdiff1d(np.arange(h * w), tok)
+    xq = sige.sige_qcache_write(x, sige.qcache_empty(n, h, w, C))
+    for cache, before, wt, fmt in ((K, K0, wk, kf), (V, V0, wv, vf)):
+        p = oq.f64(sige.sige_qlinear(xq, wt)).reshape(n, h * w, C)[:, tok]
+        q, s = oq.quantise(p, C // heads, fmt)
+        codes, scales = (t.view(n, h * w, -1).numpy() for t in raw(cache))
+        want = oq.stored(q, fmt)
+        got = codes[:, tok]
+        if fmt == "e4m3":   # -0 and 0 are the same value
+            got, want = np.where(got == 128, 0, got), np.where(want == 128, 0, want)
+        assert np.array_equal(got, want) and np.array_equal(scales[:, tok], s)
+        assert np.array_equal(codes[:, rest], before[0].view(n, h * w, -1).numpy()[:, rest])
+        assert np.array_equal(scales[:, rest], before[1].view(n, h * w, -1).numpy()[:, rest])
