@@ -534,10 +534,12 @@ _QFMT = {"s8": Q_S8, "e4m3": Q_E4M3, "s4": Q_S4}
 _QSTORE = {"s8": torch.int8, "e4m3": torch.float8_e4m3fn, "s4": torch.uint8}
 
 
-def _in_32_bits(what: str, *numbers):
+_INT32_MAX = 0x7FFFFFFF
+
+
+def _too_large(what: str, *numbers):
     """The library's sizes are int32 (ctypes would drop the upper bits)."""
-    if max(numbers) > 0x7FFFFFFF:
-        raise ValueError(f"{what}: a size of {max(numbers)} does not fit 32 bits")
+    return ValueError(f"{what}: a size of {max(numbers)} does not fit 32 bits")
 
 
 class QCache:
@@ -566,7 +568,8 @@ class QCache:
             c *= 2
         if ng < 1 or c % ng:
             raise ValueError(f"{ng} scales a pixel do not divide {c} channels")
-        _in_32_bits("QCache", n, h, w, c)
+        if n | h | w | c > _INT32_MAX:
+            raise _too_large("QCache", n, h, w, c)
         self.codes, self.scales, self.format, self.shape = codes, scales, format, (n, h, w, c)
         self.desc = QCacheDesc(n, h, w, c, fmt, c // ng)
 
@@ -648,8 +651,10 @@ def _map_desc(what: str, t, shape) -> TensorDesc:
         raise ValueError(f"{what}: a map of shape {tuple(t.shape)} does not fit, {tuple(shape)} is expected")
     if not t.is_contiguous() or t.dtype not in _DT:
         raise ValueError(f"{what}: expected a contiguous bf16 or float32 map")
-    _in_32_bits(what, *shape)
-    return TensorDesc(*shape, _DT[t.dtype], NHWC)
+    n, h, w, c = shape
+    if n | h | w | c > _INT32_MAX:
+        raise _too_large(what, *shape)
+    return TensorDesc(n, h, w, c, _DT[t.dtype], NHWC)
 
 
 def _f32(what: str, t, shape):
@@ -666,7 +671,8 @@ def _tile_args(what: str, idx, count, capacity, block):
         raise ValueError(f"{what}: the tile list is a contiguous int32 [capacity, 2] with an int32 count")
     if capacity > 0 and idx.numel() < 2 * capacity:
         raise ValueError(f"{what}: the list holds {idx.numel() // 2} tiles, fewer than its capacity {capacity}")
-    _in_32_bits(what, block, capacity)
+    if block > _INT32_MAX or capacity > _INT32_MAX:
+        raise _too_large(what, block, capacity)
     # (a tensor without elements has no address, and a list of no address is every
     # pixel to the library: any other stands for it, nothing is read there)
     return block, idx.data_ptr() or 8, count.data_ptr(), capacity
@@ -753,7 +759,8 @@ def sige_attention_qcache(q, k: QCache, v: QCache, heads: int, o=None, idx=None,
     if len(qs) != 4 or q.dtype != torch.bfloat16:
         raise ValueError("sige_attention_qcache: q is a bf16 map [N, H, W, D]")
     qd = _map_desc(what, q, qs)
-    _in_32_bits(what, heads)
+    if heads > _INT32_MAX:
+        raise _too_large(what, heads)
     shape = (qs[0], qs[1], qs[2], v.shape[3])
     if o is not None and (o.shape != shape or o.dtype != torch.bfloat16 or not o.is_contiguous()):
         raise ValueError(f"sige_attention_qcache: o is a contiguous bf16 tensor of shape {shape}")
