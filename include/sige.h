@@ -538,7 +538,8 @@ int sige_qcache_read(const void *codes, const float *scales, const sige_qcache_d
  *   workspace: device, >= SIGE_WORKSPACE_HEADER_BYTES (the device error word),
  *              16-byte aligned, zero-filled before its first use
  * The sums run on the tensor cores; sige_qlinear_path says how the codes reach
- * them.  A device-side wait that expires records SIGE_ERR_TIMEOUT: outputs that
+ * them.  Codes staged by threads are read in aligned 4-byte words: up to three
+ * bytes beside them, in a word that holds one, are read and masked off.  A device-side wait that expires records SIGE_ERR_TIMEOUT: outputs that
  * its CTA had not finished are left unwritten, others hold their values.  Errors:
  * SIGE_ERR_INVALID_ARG, SIGE_ERR_UNSUPPORTED (format, group, dtype, layout,
  * c > 131071, c_out > 2^31 - 1025, block > 64, more than 2^31 - 1 pixels or
@@ -574,7 +575,9 @@ int sige_qlinear_path(int32_t c);
  * cores the weights exp(s - max), times the value's scale, are rounded to bf16
  * before the second product (as in (8)).  Values of any finite magnitude give
  * finite results; the sums q . key codes (before the key's scale) have to stay
- * below 2^128.  Errors:
+ * below 2^128.  Where heads or addresses leave no whole vectors, codes are read in
+ * aligned 4-byte words: up to three bytes beside them, in a word that holds one,
+ * are read and masked off.  Errors:
  * SIGE_ERR_INVALID_ARG (NULL, sizes that differ, D or Dv not a multiple of
  * heads, overlap, misaligned list), SIGE_ERR_UNSUPPORTED (q not bf16 NHWC, head
  * width > 256, group not a multiple of the head width, block > 64, sizes past
@@ -589,7 +592,8 @@ int sige_attention_qcache(const void *q, const sige_tensor_desc *qd, const void 
 /* Which kernel sige_attention_qcache runs for head widths dh and dvh: 1 =
  * tcgen05 tensor cores (up to 192; widths that are multiples of 8 and 16-byte
  * aligned buffers are the fast form), 0 = CUDA cores, SIGE_ERR_UNSUPPORTED above
- * 256.  Host only. */
+ * 256.  (Calls of more than 2^24 channels, or 2^27 blocks of 128 queries over all
+ * items and heads, run on the CUDA cores at any width.)  Host only. */
 int sige_attention_qcache_path(int32_t dh, int32_t dvh);
 
 /* ------------------------------------------------------------ utilities */

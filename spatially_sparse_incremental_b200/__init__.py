@@ -615,7 +615,8 @@ class _Launch:
     """Makes device ``dev`` and ``stream`` (None: that device's current stream)
     current for a call and gives the stream's handle: the library launches on
     the current device, and a workspace or an output allocated meanwhile
-    belongs to that stream."""
+    belongs to that stream.  An argument that was allocated on another stream is
+    the caller's to keep until the call has run, as under torch.cuda.stream."""
     __slots__ = ("ctx", "dev", "stream")
 
     def __init__(self, dev: int, stream):

@@ -11,8 +11,8 @@
 // chunk against one block.  Roles of a CTA's 16 warps:
 //   * warp 0 issues S = Q K^T (M 128, N a chunk), warp 1 O += P V (M 128, K a
 //     chunk), each from one elected lane.  One warp for both took about 1300
-//     cycles a job, more than a softmax group.  Warps 0 and 1 because the
-//     schedulers serve the lowest numbers first: 84 -> 83 us on one map;
+//     cycles a job.  Warps 0 and 1 because the schedulers serve the lowest numbers
+//     first: 1 us of 80 on one map;
 //   * six warps stage the operands: the unit's queries once, and for each chunk
 //     the codes (global loads of 8 codes a thread, a chunk ahead in registers),
 //     turned into bf16 rows of 128 bytes with the 128-byte swizzle (K-major for
@@ -23,26 +23,28 @@
 //     moves only when a score lies kSlack above it, so an ordinary job reads its
 //     scores once and leaves O alone.  Four groups at 80 registers were slower.
 // With more units than CTAs a unit is two blocks, one for each group, so that a
-// chunk is staged once for 256 queries (64x64, 8 heads of 40, one map: 80 us, 112
-// in units of one block); otherwise the groups take the chunks of one block in
-// turn and their rows (O, base, sum) are merged through shared memory at the end
-// of the unit.  Where units are few, the CTAs of a cluster also split the keys and
+// chunk is staged once for 256 queries (64x64, 8 heads of 40, one map: 79 us, 111
+// in units of one block), where that saves enough rounds of units; otherwise the
+// groups take the chunks of one block in turn and their rows (O, base, sum) are
+// merged through shared memory at the end of the unit.  Where units are few, the CTAs of a cluster also split the keys and
 // push their rows to the row's owner through distributed shared memory (25 tiles
-// of 4x4 against 4096 keys, 32 units on 148 SMs: 26 us, 57 without the split; 32x32,
-// 8 heads of 80: 23 and 30 us).
+// of 4x4 against 4096 keys, 32 units: 24.5 us, 57 without the split; one 32x32 map,
+// 8 heads of 80: 22 and 30 us).  A launch is at most as many clusters of four as fit
+// the device at once, 33 here: 132 CTAs, 16 of the 148 SMs take no part.
 //
 // Head widths up to 192 in three layouts (64, 128, 192 channels staged a row), each
 // in two forms: vectors of 8 codes and 16-byte query and output vectors, or (kAny:
 // widths that are not multiples of 8, unaligned tensors) codes out of aligned words
-// and the rest element by element: 43 us for the 25 tiles, 135 for the map (the
+// and the rest element by element: 44 us for the 25 tiles, 142 for the map (the
 // CUDA-core kernel: 2575 and 5680).
 //
 // Bound: the softmax groups.  One map (4096 queries and keys, 8 heads of 40) is
 // 134M exponentials, 30 us at 16 a cycle and SM, and 21.5 GFLOP (26 with heads of
 // 40 run as 48), 16 us at the bf16 rate.  A job of 128 queries x 128 keys takes
-// about 2500 cycles of a group: the scores' way out of tensor memory, scaling,
-// exponentials and packing of its 128 values a lane, with the two groups' four
-// schedulers shared with staging (codes to bf16) and issue.
+// about 4700 cycles of a group, two groups at once: the scores' way out of tensor
+// memory, scaling, exponentials and packing of its 128 values a lane, with the two
+// groups' four schedulers shared with staging (codes to bf16) and issue; about 1900
+// of them are the wait for the next scores.
 #include <algorithm>
 #include <atomic>
 #include <math.h>
@@ -60,11 +62,14 @@ constexpr int kRows = 128;
 constexpr int kGroup = 128;         // threads of a softmax group
 constexpr int kStage = 192;         // staging threads
 constexpr int kCluster = 4;
-// Items of at most kShort keys have their weights in two bf16 terms: the rounding
-// of a weight does not average out over few keys, and with one or two it is all
-// that a row's values share (their error was 1.7 times the output rounding's).
-// The second terms lie where the weights of the next kShort keys would, and meet
-// the same values.
+// A weight's rounding to bf16 is as large as an output's, whatever the number of
+// keys: results of 33 to 4096 keys are 1.2 to 1.5 times as far from the exact ones as
+// those of float32 weights (both rounded to bf16 at the end; 1.6 for some sets of
+// four queries).  Items of at most kShort keys, where it does not average out (with
+// one or two keys it is all that a row's values share), have their weights in two
+// bf16 terms, and 1.0.  kShort: the second terms lie where the weights of the next
+// kShort keys would, and meet the same values, so that the narrowest chunk (64
+// keys) holds both and they cost no product.
 constexpr int kShort = 32;
 constexpr float kSlack = 40.0f;     // how far (base 2) a score may lie above the exponent base (kBigScale)
 
@@ -226,8 +231,8 @@ __device__ __forceinline__ uint32_t place(uint32_t atom, int j, int v)
 // One staging thread's share of a chunk of K or V: up to N vectors of 8 codes,
 // vector i being (key j, vector v) number t + kStage i of the chunk, v fastest.
 // Where they lie in the chunk and in shared memory is worked out once; the next
-// chunk's codes are on their way in registers.  kAny: code by code, a row's last
-// vector as far as the head goes.
+// chunk's codes are on their way in registers.  kAny: out of aligned words, a row's
+// last vector as far as the head goes.
 template <int N, int kKeys, bool kAny>
 struct Stager {
     uint32_t src[N];      // offset from the chunk's first key: bytes (kAny: codes)

@@ -21,7 +21,7 @@
 // 20 tokens of a list x 5120 -> 1280: 10.2 us, 21.0 without; one token of a map
 // 6.6 and 8.4.
 //
-// k_qlinear_whole is the same for whole maps (16384 x 640 -> 5120 60 us, 72 by
+// k_qlinear_whole is the same for whole maps (16384 x 640 -> 5120 61 us, 72 by
 // the general kernel; 1280 -> 320 with residual 10.3 and 13.7; 16 tokens x 1280 ->
 // 1280 4.0 and 5.1), k_qlinear_staged for codes that TMA cannot copy.
 #include <algorithm>
