@@ -24,15 +24,14 @@ struct QLinearParams {
 // float32, 2^-24), the token's scale, the channel's scale, then the bias.  The two
 // scales are applied one after the other: their product alone may leave float32's
 // range where the value does not.  So may the sum (below 2^31) times a token scale
-// above 2^96: 2^64 of such a scale come last.  (One multiplication more, 16384 x
-// 640 -> 5120 60.1 us without and 61.4 with it; a second copy of the loop for warps
-// with such a token 60.9, and 25 tiles 320 -> 320 6.35 in place of 6.23.)
+// above 2^96 (is_big): 2^64 of such a scale come last.
 struct TokenScale {
     float first, last;
 };
+__device__ __forceinline__ bool is_big(float sa) { return fabsf(sa) > 0x1p96f; }
 __device__ __forceinline__ TokenScale token_scale(float sa)
 {
-    const bool big = fabsf(sa) > 0x1p96f;
+    const bool big = is_big(sa);
     return TokenScale{big ? sa * 0x1p-64f : sa, big ? 0x1p64f : 1.0f};
 }
 __device__ __forceinline__ float qlinear_value(int acc, TokenScale sa, float sw, float bias)
