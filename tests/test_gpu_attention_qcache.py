@@ -470,3 +470,26 @@ def test_layer_and_its_caches(cross, kf, vf):
         assert np.array_equal(got, want) and np.array_equal(scales[:, tok], s)
         assert np.array_equal(codes[:, rest], before[0].view(n, h * w, -1).numpy()[:, rest])
         assert np.array_equal(scales[:, rest], before[1].view(n, h * w, -1).numpy()[:, rest])
+
+
+@pytest.mark.parametrize("n,h,w,heads,dh,keys,counts", [(2, 48, 48, 8, 40, 700, None), (3, 32, 32, 8, 80, 77, [77, 0, 41]), (32, 8, 8, 8, 40, 300, None),
+                                                        (1, 13, 12, 8, 160, 900, None)])
+def test_whole_maps_repeat_their_bits(n, h, w, heads, dh, keys, counts):
+    """Units of two blocks, of one, and split ones: the same bits again, on two
+    streams at once and with other work in between."""
+    rng = np.random.default_rng(n)
+    q = torch.from_numpy(rng.normal(size=(n, h, w, heads * dh))).to(torch.bfloat16).to(DEV)
+    K, V = (random_cache(rng, n, keys, 1, heads * dh, dh, f)[0] for f in ("s8", "e4m3"))
+    kc = None if counts is None else torch.tensor(counts, dtype=torch.int32, device=DEV)
+    ref = sige.sige_attention_qcache(q, K, V, heads, key_counts=kc)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for _ in range(10):
+        for s in streams:
+            outs.append(sige.sige_attention_qcache(q, K, V, heads, key_counts=kc, stream=s))
+            with torch.cuda.stream(s):
+                torch.empty(1 << 22, device=DEV).normal_()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, ref) for o in outs)
